@@ -1,7 +1,7 @@
 /*
  * mss.h -- C ABI of libmss, the MI355X (gfx950) Mamba selective-scan library.
  *
- * Six operations.  The scan forward and backward can also run in reverse
+ * Ten operations.  The scan forward and backward can also run in reverse
  * time (mss_scan_args.reverse), the second direction of a bidirectional
  * layer (SpeechLens kernel-optimization notes, the bidirectional variant in
  * its rejected-fusion list):
@@ -77,6 +77,32 @@
  *     real part as in the real case, the rotation from the imaginary part,
  *     the real part of the output).  fp32 activations only.
  *
+ *  7. mss_causal_conv1d_prompts: operation 3 for a batch of prompts of any
+ *     lengths, packed one after another along the token axis, with a cache of
+ *     windows: prompt i starts from the window in its cache slot (or from
+ *     zeros) and leaves its last width-1 samples there.
+ *
+ *  8. mss_head_scan_prompts: the head-wise selective scan over packed prompts.
+ *     Head h has headdim columns p, one decay rate A = -exp(A_log[h]) and one
+ *     time step per token; the heads of a group g share B and C, whose dstate
+ *     entries n may be up to MSS_MAX_HEAD_DSTATE:
+ *        delta    = softplus(dt_raw[t,h] + dt_bias[h])     (or without softplus)
+ *        S[p,n]  <- exp(delta * A) * S[p,n] + delta * x[t,h,p] * B[t,g,n]
+ *        y        = sum_n C[t,g,n] * S[p,n] + D[h] * x[t,h,p]
+ *        out[t,h,p] = y * z[t,h,p] * sigmoid(z[t,h,p])       (if z is given)
+ *     Prompt i starts from the state in its cache slot (or from zero) and
+ *     leaves its last state there.
+ *
+ *  9. mss_head_scan_step: operations 7 and 8 for one token a row, on both
+ *     caches: each row's channels (x of every head, then B, then C of every
+ *     group) go through the conv step and SiLU, then through one step of the
+ *     head-wise scan.
+ *
+ * 10. mss_rms_norm: r = x (+ residual), y = r / sqrt(mean(r^2) + eps) * weight
+ *     over the columns of each row, written in io_dtype or in 8 bits (e4m3)
+ *     with one fp32 scale a row or a block of MSS_SCALE_BLOCK columns; r is
+ *     written back as the new residual.
+ *
  * Conventions shared by every entry point
  *  - All tensor pointers are DEVICE pointers owned by the caller.  The library
  *    never allocates, frees or retains caller memory and keeps no per-call
@@ -119,7 +145,7 @@
 extern "C" {
 #endif
 
-#define MSS_ABI_VERSION 5
+#define MSS_ABI_VERSION 6
 
 /* Chunk states: the state entering every MSS_STATE_CHUNK-step chunk of
  * logical time, fp32, laid out [ceil(L / MSS_STATE_CHUNK)][b][d][MSS_MAX_DSTATE]
@@ -130,6 +156,8 @@ extern "C" {
 #define MSS_STATE_CHUNK 16
 #define MSS_MAX_DSTATE 16
 #define MSS_MAX_CONV_WIDTH 4
+#define MSS_MAX_HEAD_DSTATE 128
+#define MSS_SCALE_BLOCK 128
 
 /* Device scratch that mss_selective_scan_fwd_noalloc holds per GPU (16 MiB):
  * enough for the time-segment carries of any shape (at most 6.3 MB, for
@@ -145,7 +173,8 @@ typedef enum mss_status {
                                     /* conv width outside [1, MSS_MAX_CONV_WIDTH]      */
     MSS_ERR_BAD_STRIDE = 3,         /* negative, overlapping or no unit-stride axis    */
     MSS_ERR_UNSUPPORTED_DTYPE = 4,  /* io_dtype is not MSS_F32 or MSS_BF16             */
-    MSS_ERR_UNSUPPORTED_DSTATE = 5, /* dstate outside [1, MSS_MAX_DSTATE]              */
+    MSS_ERR_UNSUPPORTED_DSTATE = 5, /* dstate outside [1, MSS_MAX_DSTATE] (head-wise   */
+                                    /* operations: [1, MSS_MAX_HEAD_DSTATE])           */
     MSS_ERR_MISALIGNED = 6,         /* a pointer is not aligned to its element size    */
     MSS_ERR_WORKSPACE_TOO_SMALL = 7,/* workspace_bytes below the required size         */
     MSS_ERR_ALIASING = 8,           /* an output overlaps an input                     */
@@ -463,6 +492,186 @@ mss_status mss_causal_conv1d_fwd(const mss_conv_args *args, void *stream);
 /* One decode step of the conv1d (see the top of this file).  The window
  * `state` is the only in/out buffer; out must not overlap it or any input. */
 mss_status mss_causal_conv1d_update(const mss_conv_step_args *args, void *stream);
+
+/* Packed prompts.  `tokens` rows hold `seqs` prompts one after another:
+ * prompt i is rows cu_seqlens[i] .. cu_seqlens[i+1]-1 (int32, on the device,
+ * cu_seqlens[0] = 0, never decreasing, at most `tokens`; a prompt may be
+ * empty).  Rows from cu_seqlens[seqs] on belong to no prompt: their outputs are
+ * left as they were.  slots[i] (int32, on the device; NULL: i) is prompt i's
+ * entry in a cache of `cache_slots`; a prompt whose slot is outside
+ * [0, cache_slots) is skipped, its rows of out left as they were.  resume[i]
+ * (int32, on the device; NULL: 0) nonzero: the prompt starts from its cache
+ * entry; 0: from zero, whatever the entry holds.  An empty prompt leaves its
+ * entry as it was (resume) or zero.  Two prompts of one call must not share a
+ * slot; entries of other slots are left as they were.  Values of cu_seqlens
+ * outside these rules give wrong results, never an access out of bounds. */
+
+/* Arguments of mss_causal_conv1d_prompts.  Set struct_size = sizeof(mss_conv_prompts_args). */
+typedef struct mss_conv_prompts_args {
+    uint32_t struct_size;
+    int32_t io_dtype;            /* mss_dtype of x, out and window                       */
+    int64_t tokens;              /* 0 <= T <= 2^30                                       */
+    int64_t dim;                 /* D >= 1 channels                                      */
+    int64_t width;               /* taps, 1..MSS_MAX_CONV_WIDTH                          */
+    int64_t seqs;                /* prompts, 1..2^20                                     */
+    int64_t cache_slots;
+
+    const void *x;               /* [t,d] (NULL iff tokens == 0)                         */
+    int64_t x_stride[2];
+    const float *weight;         /* [d,k] fp32 taps, oldest sample first                 */
+    int64_t weight_stride[2];
+    const float *bias;           /* [d] fp32 contiguous; NULL means 0                    */
+    const int32_t *cu_seqlens;   /* [seqs + 1]                                           */
+    const int32_t *slots;        /* [seqs]                                               */
+    const int32_t *resume;       /* [seqs]                                               */
+    void *window;                /* [slot][d][width-1] io_dtype, oldest first, each slot */
+    int64_t window_stride;       /* contiguous; elements from slot to slot (NULL iff     */
+                                 /* width == 1)                                          */
+    void *out;                   /* [t,d] io_dtype (NULL iff tokens == 0)                */
+    int64_t out_stride[2];
+    int32_t activation;          /* mss_activation                                       */
+    int32_t reserved0;           /* must be 0                                            */
+} mss_conv_prompts_args;
+
+/* Arguments of mss_head_scan_prompts.  Set struct_size = sizeof(mss_head_scan_args). */
+typedef struct mss_head_scan_args {
+    uint32_t struct_size;
+    int32_t io_dtype;            /* mss_dtype of x, dt_raw, z, B, C, out                 */
+    int64_t tokens;              /* 0 <= T <= 2^30                                       */
+    int64_t heads;               /* H >= 1, a multiple of groups                         */
+    int64_t headdim;             /* P >= 1                                               */
+    int64_t dstate;              /* N, 1..MSS_MAX_HEAD_DSTATE                            */
+    int64_t groups;              /* G >= 1; head h reads B and C of group h / (H / G)    */
+    int64_t seqs;                /* prompts, 1..2^20                                     */
+    int64_t cache_slots;
+
+    const void *x;               /* [t,h,p], unit stride in p (NULL iff tokens == 0)     */
+    int64_t x_stride[3];
+    const void *dt_raw;          /* [t,h] (NULL iff tokens == 0)                         */
+    int64_t dt_stride[2];
+    const float *A_log;          /* [h] fp32 contiguous                                  */
+    const void *B;               /* [t,g,n], unit stride in n (NULL iff tokens == 0)     */
+    int64_t B_stride[3];
+    const void *C;               /* [t,g,n], unit stride in n (NULL iff tokens == 0)     */
+    int64_t C_stride[3];
+    const float *D;              /* [h] fp32 contiguous; NULL means 0                    */
+    const void *z;               /* [t,h,p], unit stride in p; NULL means no gate        */
+    int64_t z_stride[3];
+    const float *dt_bias;        /* [h] fp32 contiguous; NULL means 0                    */
+    const int32_t *cu_seqlens;   /* [seqs + 1]                                           */
+    const int32_t *slots;        /* [seqs]                                               */
+    const int32_t *resume;       /* [seqs]                                               */
+    float *state;                /* [slot][h][p][n] fp32, each slot contiguous, 16-byte  */
+    int64_t state_stride;        /* aligned; elements from slot to slot                  */
+    void *out;                   /* [t,h,p], unit stride in p (NULL iff tokens == 0)     */
+    int64_t out_stride[3];
+    int32_t delta_softplus;      /* nonzero: delta = softplus(dt_raw + dt_bias)          */
+    int32_t reserved0;           /* must be 0                                            */
+    void *workspace;             /* device scratch, 256-byte aligned, of at least        */
+    size_t workspace_bytes;      /* mss_head_scan_prompts_workspace_size bytes           */
+} mss_head_scan_args;
+
+/* Arguments of mss_head_scan_step.  Set struct_size = sizeof(mss_head_step_args).
+ * Row b's cache entries are those of slots[b] (int32, on the device; NULL: b);
+ * a row whose slot is outside [0, cache_slots) is skipped, its out left as it
+ * was.  Two rows of one call must not share a slot. */
+typedef struct mss_head_step_args {
+    uint32_t struct_size;
+    int32_t io_dtype;            /* mss_dtype of xbc, dt_raw, z, window, out             */
+    int64_t rows;                /* 1 <= rows                                            */
+    int64_t heads;               /* H, a multiple of groups                              */
+    int64_t headdim;             /* P                                                    */
+    int64_t dstate;              /* N, 1..MSS_MAX_HEAD_DSTATE                            */
+    int64_t groups;              /* G                                                    */
+    int64_t width;               /* conv taps, 1..MSS_MAX_CONV_WIDTH                     */
+    int64_t cache_slots;
+
+    float *state;                /* [slot][h][p][n] fp32, each slot contiguous, 16-byte  */
+    int64_t state_stride;        /* aligned; elements from slot to slot                  */
+    void *window;                /* [slot][c][width-1] io_dtype, c over the H P + 2 G N  */
+    int64_t window_stride;       /* channels, each slot contiguous (NULL iff width == 1) */
+    const void *xbc;             /* [b,c] new samples: x [H][P], then B [G][N], C [G][N] */
+    int64_t xbc_stride[2];
+    const void *dt_raw;          /* [b,h]                                                */
+    int64_t dt_stride[2];
+    const float *A_log;          /* [h] fp32 contiguous                                  */
+    const float *weight;         /* [c,k] fp32 taps, oldest sample first                 */
+    int64_t weight_stride[2];
+    const float *bias;           /* [c] fp32 contiguous; NULL means 0                    */
+    const float *D;              /* [h] fp32 contiguous; NULL means 0                    */
+    const void *z;               /* [b,h,p]; NULL means no gate                          */
+    int64_t z_stride[3];
+    const float *dt_bias;        /* [h] fp32 contiguous; NULL means 0                    */
+    const int32_t *slots;        /* [rows]                                               */
+    void *out;                   /* [b,h,p] io_dtype                                     */
+    int64_t out_stride[3];
+    int32_t delta_softplus;
+    int32_t reserved0;           /* must be 0                                            */
+    void *workspace;             /* device scratch, 256-byte aligned, of at least        */
+    size_t workspace_bytes;      /* mss_head_scan_step_workspace_size bytes              */
+} mss_head_step_args;
+
+/* Output of mss_rms_norm. */
+typedef enum mss_quant {
+    MSS_QUANT_NONE = 0,          /* out in io_dtype                                      */
+    MSS_QUANT_ROW = 1,           /* out in e4m3, one scale a row                         */
+    MSS_QUANT_BLOCK = 2          /* out in e4m3, one scale a MSS_SCALE_BLOCK columns     */
+} mss_quant;
+
+/* Arguments of mss_rms_norm.  Set struct_size = sizeof(mss_norm_args). */
+typedef struct mss_norm_args {
+    uint32_t struct_size;
+    int32_t io_dtype;            /* mss_dtype of x (and of out without quant)            */
+    int32_t residual_dtype;      /* mss_dtype of residual and residual_out               */
+    int32_t quant;               /* mss_quant                                            */
+    int64_t rows;                /* >= 1                                                 */
+    int64_t dim;                 /* columns, 1..32768 (a multiple of MSS_SCALE_BLOCK for */
+                                 /* MSS_QUANT_BLOCK)                                     */
+    const void *x;               /* [r,d], unit stride in d                              */
+    int64_t x_stride;
+    const void *residual;        /* [r,d], unit stride in d; NULL means 0                */
+    int64_t residual_stride;
+    const float *weight;         /* [d] fp32 contiguous                                  */
+    void *out;                   /* [r,d] io_dtype or e4m3, unit stride in d             */
+    int64_t out_stride;
+    float *scale;                /* [r] or [r, d / MSS_SCALE_BLOCK] fp32 contiguous:     */
+                                 /* value = e4m3 * scale; NULL iff quant is none         */
+    void *residual_out;          /* [r,d]: x + residual; may be `residual` itself (same  */
+    int64_t residual_out_stride; /* stride); NULL: not written                           */
+    float eps;                   /* >= 0                                                 */
+    int32_t reserved0;           /* must be 0                                            */
+} mss_norm_args;
+
+/* Conv over packed prompts (see the top of this file).  Channel-last rows with
+ * aligned vectors move whole vectors; any non-negative strides are accepted.
+ * out must not overlap any input; window is the only in/out buffer.  Each
+ * output is rounded once from an fp32 sum. */
+mss_status mss_causal_conv1d_prompts(const mss_conv_prompts_args *args, void *stream);
+
+/* Bytes of device workspace mss_head_scan_prompts needs.  Depends only on the
+ * sizes, not on the prompts' lengths.  Returns 0 and sets *status on invalid
+ * sizes. */
+size_t mss_head_scan_prompts_workspace_size(const mss_head_scan_args *args, mss_status *status);
+
+/* Head-wise scan over packed prompts (see the top of this file).  state is the
+ * only in/out buffer; out must not overlap any input.  A call's workspace is
+ * its own until the call has run: two calls that may overlap in time need two. */
+mss_status mss_head_scan_prompts(const mss_head_scan_args *args, void *stream);
+
+/* Bytes of device workspace mss_head_scan_step needs (from the sizes alone). */
+size_t mss_head_scan_step_workspace_size(const mss_head_step_args *args, mss_status *status);
+
+/* One token a row through conv and head-wise scan (see the top of this file).
+ * state and window are updated in place; out must not overlap any input. */
+mss_status mss_head_scan_step(const mss_head_step_args *args, void *stream);
+
+/* Root-mean-square norm with the residual's addition (see the top of this
+ * file).  The sum x + residual is taken in fp32; its mean square, and y, come
+ * from the unrounded sum.  A scale is max|y| / 448 over its row or block, 1
+ * where that is below the normal range or not a number; a row that holds an
+ * infinity or a NaN gives NaN wherever the formula does.  Only residual_out may overlap an input, and only by being
+ * `residual`. */
+mss_status mss_rms_norm(const mss_norm_args *args, void *stream);
 
 #ifdef __cplusplus
 }

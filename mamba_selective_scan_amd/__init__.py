@@ -16,6 +16,14 @@ is no CPU or PyTorch fallback; without the built library every call raises.
     g = selective_scan_bwd(u, delta_raw, A_log, B, C, dout, D, z, dt_bias)  # dict of grads
     out = selective_scan(u, delta_raw, A_log, B, C, D, z, dt_bias)  # autograd: fwd + bwd
 
+The head-wise operations (one decay a head, B and C shared by groups of heads,
+packed prompts, caches by slot) are in heads.py:
+
+    u = causal_conv1d_prompts(x, weight, bias, cu_seqlens=cu, window=windows, slots=slots)
+    y = head_scan_prompts(x, dt_raw, A_log, B, C, D, z, dt_bias, cu_seqlens=cu, state=states)
+    y = head_scan_step(states, windows, xbc, dt_raw, A_log, weight, bias, D, z, dt_bias)
+    q, scale, residual = rms_norm(x, weight, residual=residual, quant="row")
+
 Shapes (logical index order, any strides): u, delta_raw, z, out [B, D, L];
 B, C [B, N, L]; A_log [D, N]; D, dt_bias [D]; states [B, D, N] (fp32,
 contiguous).  A channel-last [B, L, D] buffer is passed as its transpose(1, 2)
@@ -35,8 +43,20 @@ from ._lib import MSS_MAX_DSTATE, MssError
 __all__ = ["selective_scan_fwd", "selective_scan_fwd_noalloc", "selective_state_update", "scan_workspace_size",
            "causal_conv1d_fwd", "causal_conv1d_update", "selective_scan_bwd",
            "scan_bwd_workspace_size", "selective_scan", "selective_scan_fwd_complex",
-           "scan_complex_workspace_size", "MssError", "MSS_MAX_DSTATE",
-           "library_path"]
+           "scan_complex_workspace_size", "causal_conv1d_prompts", "head_scan_prompts",
+           "head_scan_step", "rms_norm", "MssError", "MSS_MAX_DSTATE", "library_path"]
+
+_HEAD_OPS = ("causal_conv1d_prompts", "head_scan_prompts", "head_scan_step", "rms_norm")
+
+
+def __getattr__(name):
+    # the head-wise operations live in a module that imports torch: loaded on
+    # first use, so that importing this one does not
+    if name in _HEAD_OPS:
+        from . import heads
+        globals().update({n: getattr(heads, n) for n in _HEAD_OPS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def library_path() -> str:

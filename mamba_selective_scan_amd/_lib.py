@@ -13,15 +13,20 @@ import os
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmss.so")
 
-MSS_ABI_VERSION = 5
+MSS_ABI_VERSION = 6
 MSS_MAX_DSTATE = 16
 MSS_STATE_CHUNK = 16
 MSS_MAX_CONV_WIDTH = 4
+MSS_MAX_HEAD_DSTATE = 128
+MSS_SCALE_BLOCK = 128
 MSS_NOALLOC_SCRATCH_BYTES = 16 << 20
 MSS_F32 = 0
 MSS_BF16 = 1
 MSS_ACT_NONE = 0
 MSS_ACT_SILU = 1
+MSS_QUANT_NONE = 0
+MSS_QUANT_ROW = 1
+MSS_QUANT_BLOCK = 2
 
 STATUS = {
     0: "MSS_OK",
@@ -43,7 +48,10 @@ EXPORTS = ("mss_abi_version", "mss_status_string", "mss_selective_scan_workspace
            "mss_selective_scan_fwd", "mss_selective_state_update", "mss_causal_conv1d_fwd",
            "mss_causal_conv1d_update", "mss_selective_scan_bwd_workspace_size",
            "mss_selective_scan_bwd", "mss_selective_scan_fwd_complex",
-           "mss_selective_scan_fwd_noalloc", "mss_selective_scan_fwd_complex_workspace_size")
+           "mss_selective_scan_fwd_noalloc", "mss_selective_scan_fwd_complex_workspace_size",
+           "mss_causal_conv1d_prompts", "mss_head_scan_prompts",
+           "mss_head_scan_prompts_workspace_size", "mss_head_scan_step",
+           "mss_head_scan_step_workspace_size", "mss_rms_norm")
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -203,6 +211,78 @@ def new_step_args() -> StepArgs:
     return a
 
 
+class ConvPromptsArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("io_dtype", _i32),
+        ("tokens", _i64), ("dim", _i64), ("width", _i64), ("seqs", _i64), ("cache_slots", _i64),
+        ("x", _vp), ("x_stride", _i64 * 2),
+        ("weight", _vp), ("weight_stride", _i64 * 2),
+        ("bias", _vp),
+        ("cu_seqlens", _vp), ("slots", _vp), ("resume", _vp),
+        ("window", _vp), ("window_stride", _i64),
+        ("out", _vp), ("out_stride", _i64 * 2),
+        ("activation", _i32), ("reserved0", _i32),
+    ]
+
+
+class HeadScanArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("io_dtype", _i32),
+        ("tokens", _i64), ("heads", _i64), ("headdim", _i64), ("dstate", _i64), ("groups", _i64),
+        ("seqs", _i64), ("cache_slots", _i64),
+        ("x", _vp), ("x_stride", _i64 * 3),
+        ("dt_raw", _vp), ("dt_stride", _i64 * 2),
+        ("A_log", _vp),
+        ("B", _vp), ("B_stride", _i64 * 3),
+        ("C", _vp), ("C_stride", _i64 * 3),
+        ("D", _vp),
+        ("z", _vp), ("z_stride", _i64 * 3),
+        ("dt_bias", _vp),
+        ("cu_seqlens", _vp), ("slots", _vp), ("resume", _vp),
+        ("state", _vp), ("state_stride", _i64),
+        ("out", _vp), ("out_stride", _i64 * 3),
+        ("delta_softplus", _i32), ("reserved0", _i32),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class HeadStepArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("io_dtype", _i32),
+        ("rows", _i64), ("heads", _i64), ("headdim", _i64), ("dstate", _i64), ("groups", _i64),
+        ("width", _i64), ("cache_slots", _i64),
+        ("state", _vp), ("state_stride", _i64),
+        ("window", _vp), ("window_stride", _i64),
+        ("xbc", _vp), ("xbc_stride", _i64 * 2),
+        ("dt_raw", _vp), ("dt_stride", _i64 * 2),
+        ("A_log", _vp),
+        ("weight", _vp), ("weight_stride", _i64 * 2),
+        ("bias", _vp),
+        ("D", _vp),
+        ("z", _vp), ("z_stride", _i64 * 3),
+        ("dt_bias", _vp),
+        ("slots", _vp),
+        ("out", _vp), ("out_stride", _i64 * 3),
+        ("delta_softplus", _i32), ("reserved0", _i32),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("io_dtype", _i32), ("residual_dtype", _i32),
+        ("quant", _i32),
+        ("rows", _i64), ("dim", _i64),
+        ("x", _vp), ("x_stride", _i64),
+        ("residual", _vp), ("residual_stride", _i64),
+        ("weight", _vp),
+        ("out", _vp), ("out_stride", _i64),
+        ("scale", _vp),
+        ("residual_out", _vp), ("residual_out_stride", _i64),
+        ("eps", ctypes.c_float), ("reserved0", _i32),
+    ]
+
+
 class MssError(RuntimeError):
     """A libmss call returned a status other than MSS_OK."""
 
@@ -243,6 +323,20 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.mss_causal_conv1d_fwd.restype = ctypes.c_int
     lib.mss_causal_conv1d_update.argtypes = [ctypes.POINTER(ConvStepArgs), _vp]
     lib.mss_causal_conv1d_update.restype = ctypes.c_int
+    lib.mss_causal_conv1d_prompts.argtypes = [ctypes.POINTER(ConvPromptsArgs), _vp]
+    lib.mss_causal_conv1d_prompts.restype = ctypes.c_int
+    lib.mss_head_scan_prompts_workspace_size.argtypes = [ctypes.POINTER(HeadScanArgs),
+                                                         ctypes.POINTER(ctypes.c_int)]
+    lib.mss_head_scan_prompts_workspace_size.restype = ctypes.c_size_t
+    lib.mss_head_scan_prompts.argtypes = [ctypes.POINTER(HeadScanArgs), _vp]
+    lib.mss_head_scan_prompts.restype = ctypes.c_int
+    lib.mss_head_scan_step_workspace_size.argtypes = [ctypes.POINTER(HeadStepArgs),
+                                                      ctypes.POINTER(ctypes.c_int)]
+    lib.mss_head_scan_step_workspace_size.restype = ctypes.c_size_t
+    lib.mss_head_scan_step.argtypes = [ctypes.POINTER(HeadStepArgs), _vp]
+    lib.mss_head_scan_step.restype = ctypes.c_int
+    lib.mss_rms_norm.argtypes = [ctypes.POINTER(NormArgs), _vp]
+    lib.mss_rms_norm.restype = ctypes.c_int
     return lib
 
 

@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libmss.so")
 SOURCES = ["mss_api.hip", "scan_fwd.hip", "state_update.hip", "conv1d.hip", "scan_bwd.hip",
-           "scan_cplx.hip"]
+           "scan_cplx.hip", "head_api.hip", "conv_prompts.hip", "head_scan.hip", "head_step.hip",
+           "rms_norm.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 instructions are disabled for every kernel: the compiler would

@@ -1,0 +1,365 @@
+// head_api.hip -- the C ABI of the head-wise operations: argument checks,
+// launch planning and stream-ordered enqueue.  As in mss_api.hip, every check
+// runs on the host before any HIP call.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "mss.h"
+#include "mss_checks.hpp"
+#include "mss_head.hpp"
+
+namespace {
+
+using mss::Extent;
+using mss::aligned;
+using mss::extent_of;
+using mss::non_overlapping;
+using mss::overlaps;
+using mss::strides_nonneg;
+
+constexpr int64_t kMaxInt = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxTokens = int64_t{1} << 30;
+constexpr int64_t kMaxSeqs = int64_t{1} << 20;
+constexpr int64_t kMaxNormDim = 32768;
+const int64_t kOne[1] = {1};
+
+bool bad_dtype(int32_t t) { return t != MSS_F32 && t != MSS_BF16; }
+int64_t elem(int32_t t) { return t == MSS_BF16 ? 2 : 4; }
+
+Extent vec(const void* p, int64_t n, int64_t es) { return extent_of(p, &n, kOne, 1, es); }
+
+// [slot][inner] with contiguous inner entries.
+Extent cache_extent(const void* p, int64_t slots, int64_t inner, int64_t stride, int64_t es) {
+  const int64_t sz[2] = {slots, inner}, st[2] = {stride, 1};
+  return extent_of(p, sz, st, 2, es);
+}
+bool cache_stride_ok(int64_t slots, int64_t inner, int64_t stride) {
+  return slots == 1 ? stride >= 0 : stride >= inner;
+}
+
+template <size_t N>
+bool any_overlap(const Extent& e, const Extent (&ins)[N]) {
+  for (const Extent& i : ins)
+    if (overlaps(e, i)) return true;
+  return false;
+}
+
+// Waves along the rows: short runs while they keep the grid small, so that a
+// short prompt's rows are read in parallel, and runs of kConvRun rows otherwise.
+constexpr int64_t kConvRun = 32;
+constexpr int64_t kConvShortRun = 4;
+constexpr int64_t kConvWaves = 4096;
+
+mss_status check_head_shape(int64_t heads, int64_t headdim, int64_t dstate, int64_t groups) {
+  if (heads < 1 || headdim < 1 || groups < 1 || heads > kMaxInt || headdim > kMaxInt ||
+      groups > heads || heads % groups != 0)
+    return MSS_ERR_BAD_SHAPE;
+  if (dstate < 1 || dstate > MSS_MAX_HEAD_DSTATE) return MSS_ERR_UNSUPPORTED_DSTATE;
+  if (heads * headdim > kMaxInt / 4 || groups * dstate > kMaxInt / 4) return MSS_ERR_BAD_SHAPE;
+  return MSS_OK;
+}
+
+mss_status check_scan_shape(const mss_head_scan_args* a) {
+  if (a == nullptr || a->struct_size != sizeof(mss_head_scan_args) || a->reserved0 != 0)
+    return MSS_ERR_BAD_STRUCT;
+  if (bad_dtype(a->io_dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
+  if (a->tokens < 0 || a->tokens > kMaxTokens || a->seqs < 1 || a->seqs > kMaxSeqs ||
+      a->cache_slots < 1 || a->cache_slots > kMaxInt)
+    return MSS_ERR_BAD_SHAPE;
+  return check_head_shape(a->heads, a->headdim, a->dstate, a->groups);
+}
+
+mss_status check_step_shape(const mss_head_step_args* a) {
+  if (a == nullptr || a->struct_size != sizeof(mss_head_step_args) || a->reserved0 != 0)
+    return MSS_ERR_BAD_STRUCT;
+  if (bad_dtype(a->io_dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
+  if (a->rows < 1 || a->rows > kMaxInt || a->cache_slots < 1 || a->cache_slots > kMaxInt ||
+      a->width < 1 || a->width > MSS_MAX_CONV_WIDTH)
+    return MSS_ERR_BAD_SHAPE;
+  const mss_status st = check_head_shape(a->heads, a->headdim, a->dstate, a->groups);
+  if (st != MSS_OK) return st;
+  const int64_t chans = a->heads * a->headdim + 2 * a->groups * a->dstate;
+  if (chans > kMaxInt || a->rows > kMaxInt / chans || a->rows * a->heads > kMaxInt / ((a->headdim + 7) / 8))
+    return MSS_ERR_BAD_SHAPE;
+  return MSS_OK;
+}
+
+mss::Prompts prompts(int64_t tokens, int64_t seqs, int64_t slots, const int32_t* cu,
+                     const int32_t* slot, const int32_t* resume) {
+  return {static_cast<int>(tokens), static_cast<int>(seqs), static_cast<int>(slots), cu, slot, resume};
+}
+
+}  // namespace
+
+extern "C" {
+
+mss_status mss_causal_conv1d_prompts(const mss_conv_prompts_args* a, void* stream) {
+  if (a == nullptr || a->struct_size != sizeof(mss_conv_prompts_args) || a->reserved0 != 0)
+    return MSS_ERR_BAD_STRUCT;
+  if (bad_dtype(a->io_dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
+  if (a->tokens < 0 || a->tokens > kMaxTokens || a->dim < 1 || a->dim > kMaxInt / 4 || a->width < 1 ||
+      a->width > MSS_MAX_CONV_WIDTH || a->seqs < 1 || a->seqs > kMaxSeqs || a->cache_slots < 1 ||
+      a->cache_slots > kMaxInt)
+    return MSS_ERR_BAD_SHAPE;
+  if (a->activation != MSS_ACT_NONE && a->activation != MSS_ACT_SILU) return MSS_ERR_BAD_STRUCT;
+  const int64_t T = a->tokens, W = a->width, es = elem(a->io_dtype);
+  if (a->weight == nullptr || a->cu_seqlens == nullptr || (W > 1 && a->window == nullptr) ||
+      (T > 0 && (a->x == nullptr || a->out == nullptr)))
+    return MSS_ERR_NULL_POINTER;
+  if (!strides_nonneg(a->x_stride, 2) || !strides_nonneg(a->out_stride, 2) ||
+      !strides_nonneg(a->weight_stride, 2))
+    return MSS_ERR_BAD_STRIDE;
+  const int64_t xs[2] = {T, a->dim}, ws[2] = {a->dim, W};
+  if (T > 0 && !non_overlapping(xs, a->out_stride, 2)) return MSS_ERR_BAD_STRIDE;
+  if (W > 1 && !cache_stride_ok(a->cache_slots, a->dim * (W - 1), a->window_stride))
+    return MSS_ERR_BAD_STRIDE;
+  if (!aligned(a->x, es) || !aligned(a->out, es) || !aligned(a->window, es) || !aligned(a->weight, 4) ||
+      !aligned(a->bias, 4) || !aligned(a->cu_seqlens, 4) || !aligned(a->slots, 4) || !aligned(a->resume, 4))
+    return MSS_ERR_MISALIGNED;
+  const Extent ins[] = {T > 0 ? extent_of(a->x, xs, a->x_stride, 2, es) : Extent{},
+                        extent_of(a->weight, ws, a->weight_stride, 2, 4),
+                        vec(a->bias, a->dim, 4), vec(a->cu_seqlens, a->seqs + 1, 4),
+                        vec(a->slots, a->seqs, 4), vec(a->resume, a->seqs, 4)};
+  const Extent eo = T > 0 ? extent_of(a->out, xs, a->out_stride, 2, es) : Extent{};
+  const Extent ew = W > 1 ? cache_extent(a->window, a->cache_slots, a->dim * (W - 1), a->window_stride, es)
+                          : Extent{};
+  if (any_overlap(eo, ins) || any_overlap(ew, ins) || overlaps(eo, ew)) return MSS_ERR_ALIASING;
+
+  mss::ConvPromptsArgs k{};
+  k.q = prompts(T, a->seqs, a->cache_slots, a->cu_seqlens, a->slots, a->resume);
+  k.dim = static_cast<int>(a->dim);
+  k.width = static_cast<int>(W);
+  k.silu = a->activation == MSS_ACT_SILU ? 1 : 0;
+  for (int i = 0; i < 2; ++i) {
+    k.sx[i] = xs[i] == 1 ? 1 : a->x_stride[i];
+    k.so[i] = xs[i] == 1 ? 1 : a->out_stride[i];
+    k.sw[i] = a->weight_stride[i];
+  }
+  k.swin = a->window_stride;
+  const int64_t lane_cols = 16 / es;
+  k.colgroups = static_cast<int>((a->dim + 64 * lane_cols - 1) / (64 * lane_cols));
+  k.run = static_cast<int>(std::clamp(T * k.colgroups / kConvWaves, kConvShortRun, kConvRun));
+  k.nruns = (T + k.run - 1) / k.run;
+  if ((k.nruns + a->seqs) * k.colgroups > 4 * kMaxInt) return MSS_ERR_BAD_SHAPE;
+  k.x = a->x;
+  k.weight = a->weight;
+  k.bias = a->bias;
+  k.window = a->window;
+  k.out = a->out;
+  const hipError_t e = mss::launch_conv_prompts(k, a->io_dtype == MSS_BF16, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
+}
+
+size_t mss_head_scan_prompts_workspace_size(const mss_head_scan_args* a, mss_status* status) {
+  const mss_status st = check_scan_shape(a);
+  if (status != nullptr) *status = st;
+  return 0;
+}
+
+mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
+  const mss_status shape = check_scan_shape(a);
+  if (shape != MSS_OK) return shape;
+  const int64_t T = a->tokens, H = a->heads, P = a->headdim, N = a->dstate, G = a->groups;
+  const int64_t es = elem(a->io_dtype);
+  if (a->A_log == nullptr || a->cu_seqlens == nullptr || a->state == nullptr ||
+      (T > 0 && (a->x == nullptr || a->dt_raw == nullptr || a->B == nullptr || a->C == nullptr ||
+                 a->out == nullptr)))
+    return MSS_ERR_NULL_POINTER;
+  if (!strides_nonneg(a->x_stride, 3) || !strides_nonneg(a->dt_stride, 2) || !strides_nonneg(a->B_stride, 3) ||
+      !strides_nonneg(a->C_stride, 3) || (a->z != nullptr && !strides_nonneg(a->z_stride, 3)) ||
+      !strides_nonneg(a->out_stride, 3))
+    return MSS_ERR_BAD_STRIDE;
+  if (T > 0 && ((P > 1 && (a->x_stride[2] != 1 || a->out_stride[2] != 1 ||
+                           (a->z != nullptr && a->z_stride[2] != 1))) ||
+                (N > 1 && (a->B_stride[2] != 1 || a->C_stride[2] != 1))))
+    return MSS_ERR_BAD_STRIDE;
+  const int64_t xs[3] = {T, H, P}, ds[2] = {T, H}, bs[3] = {T, G, N};
+  if (T > 0 && !non_overlapping(xs, a->out_stride, 3)) return MSS_ERR_BAD_STRIDE;
+  if (H * P > kMaxInt * 64 / N || !cache_stride_ok(a->cache_slots, H * P * N, a->state_stride))
+    return MSS_ERR_BAD_STRIDE;
+  if (!aligned(a->x, es) || !aligned(a->dt_raw, es) || !aligned(a->B, es) || !aligned(a->C, es) ||
+      !aligned(a->z, es) || !aligned(a->out, es) || !aligned(a->A_log, 4) || !aligned(a->D, 4) ||
+      !aligned(a->dt_bias, 4) || !aligned(a->state, 16) || !aligned(a->cu_seqlens, 4) ||
+      !aligned(a->slots, 4) || !aligned(a->resume, 4) || !aligned(a->workspace, 256))
+    return MSS_ERR_MISALIGNED;
+  const bool any = T > 0;
+  const Extent none{};
+  const Extent ins[] = {any ? extent_of(a->x, xs, a->x_stride, 3, es) : none,
+                        any ? extent_of(a->dt_raw, ds, a->dt_stride, 2, es) : none,
+                        any ? extent_of(a->B, bs, a->B_stride, 3, es) : none,
+                        any ? extent_of(a->C, bs, a->C_stride, 3, es) : none,
+                        any ? extent_of(a->z, xs, a->z_stride, 3, es) : none,
+                        vec(a->A_log, H, 4), vec(a->D, H, 4), vec(a->dt_bias, H, 4),
+                        vec(a->cu_seqlens, a->seqs + 1, 4), vec(a->slots, a->seqs, 4),
+                        vec(a->resume, a->seqs, 4)};
+  const Extent eo = any ? extent_of(a->out, xs, a->out_stride, 3, es) : none;
+  const Extent es_ = cache_extent(a->state, a->cache_slots, H * P * N, a->state_stride, 4);
+  if (any_overlap(eo, ins) || any_overlap(es_, ins) || overlaps(eo, es_)) return MSS_ERR_ALIASING;
+  if (a->seqs * H > kMaxInt / ((P + 15) / 16)) return MSS_ERR_BAD_SHAPE;
+
+  mss::HeadScanArgs k{};
+  k.q = prompts(T, a->seqs, a->cache_slots, a->cu_seqlens, a->slots, a->resume);
+  k.heads = static_cast<int>(H);
+  k.headdim = static_cast<int>(P);
+  k.dstate = static_cast<int>(N);
+  k.groups = static_cast<int>(G);
+  k.softplus = a->delta_softplus != 0 ? 1 : 0;
+  std::memcpy(k.sx, a->x_stride, sizeof(k.sx));
+  std::memcpy(k.sdt, a->dt_stride, sizeof(k.sdt));
+  std::memcpy(k.sB, a->B_stride, sizeof(k.sB));
+  std::memcpy(k.sC, a->C_stride, sizeof(k.sC));
+  std::memcpy(k.sz, a->z_stride, sizeof(k.sz));
+  std::memcpy(k.so, a->out_stride, sizeof(k.so));
+  k.sstate = a->state_stride;
+  k.x = a->x;
+  k.dt = a->dt_raw;
+  k.A_log = a->A_log;
+  k.B = a->B;
+  k.C = a->C;
+  k.D = a->D;
+  k.z = a->z;
+  k.dt_bias = a->dt_bias;
+  k.state = a->state;
+  k.out = a->out;
+  const hipError_t e = mss::launch_head_scan(k, a->io_dtype == MSS_BF16, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
+}
+
+size_t mss_head_scan_step_workspace_size(const mss_head_step_args* a, mss_status* status) {
+  const mss_status st = check_step_shape(a);
+  if (status != nullptr) *status = st;
+  if (st != MSS_OK) return 0;
+  return static_cast<size_t>(a->rows * (a->heads * a->headdim + 2 * a->groups * a->dstate) * 4);
+}
+
+mss_status mss_head_scan_step(const mss_head_step_args* a, void* stream) {
+  const mss_status shape = check_step_shape(a);
+  if (shape != MSS_OK) return shape;
+  const int64_t R = a->rows, H = a->heads, P = a->headdim, N = a->dstate, G = a->groups, W = a->width;
+  const int64_t es = elem(a->io_dtype), chans = H * P + 2 * G * N;
+  if (a->state == nullptr || (W > 1 && a->window == nullptr) || a->xbc == nullptr || a->dt_raw == nullptr ||
+      a->A_log == nullptr || a->weight == nullptr || a->out == nullptr)
+    return MSS_ERR_NULL_POINTER;
+  if (!strides_nonneg(a->xbc_stride, 2) || !strides_nonneg(a->dt_stride, 2) ||
+      !strides_nonneg(a->weight_stride, 2) || (a->z != nullptr && !strides_nonneg(a->z_stride, 3)) ||
+      !strides_nonneg(a->out_stride, 3))
+    return MSS_ERR_BAD_STRIDE;
+  const int64_t xs[2] = {R, chans}, ds[2] = {R, H}, ws[2] = {chans, W}, os[3] = {R, H, P};
+  if (!non_overlapping(os, a->out_stride, 3)) return MSS_ERR_BAD_STRIDE;
+  if (!cache_stride_ok(a->cache_slots, H * P * N, a->state_stride) ||
+      (W > 1 && !cache_stride_ok(a->cache_slots, chans * (W - 1), a->window_stride)))
+    return MSS_ERR_BAD_STRIDE;
+  if (!aligned(a->state, 16) || !aligned(a->window, es) || !aligned(a->xbc, es) || !aligned(a->dt_raw, es) ||
+      !aligned(a->z, es) || !aligned(a->out, es) || !aligned(a->A_log, 4) || !aligned(a->weight, 4) ||
+      !aligned(a->bias, 4) || !aligned(a->D, 4) || !aligned(a->dt_bias, 4) || !aligned(a->slots, 4) ||
+      !aligned(a->workspace, 256))
+    return MSS_ERR_MISALIGNED;
+  const size_t need = static_cast<size_t>(R * chans * 4);
+  if (a->workspace == nullptr || a->workspace_bytes < need) return MSS_ERR_WORKSPACE_TOO_SMALL;
+  const Extent ins[] = {extent_of(a->xbc, xs, a->xbc_stride, 2, es), extent_of(a->dt_raw, ds, a->dt_stride, 2, es),
+                        extent_of(a->z, os, a->z_stride, 3, es), extent_of(a->weight, ws, a->weight_stride, 2, 4),
+                        vec(a->A_log, H, 4), vec(a->bias, chans, 4), vec(a->D, H, 4), vec(a->dt_bias, H, 4),
+                        vec(a->slots, R, 4)};
+  const Extent outs[] = {extent_of(a->out, os, a->out_stride, 3, es),
+                         cache_extent(a->state, a->cache_slots, H * P * N, a->state_stride, 4),
+                         W > 1 ? cache_extent(a->window, a->cache_slots, chans * (W - 1), a->window_stride, es)
+                               : Extent{},
+                         vec(a->workspace, static_cast<int64_t>(need), 1)};
+  for (int i = 0; i < 4; ++i) {
+    if (any_overlap(outs[i], ins)) return MSS_ERR_ALIASING;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outs[j])) return MSS_ERR_ALIASING;
+  }
+
+  mss::HeadStepArgs k{};
+  k.rows = static_cast<int>(R);
+  k.heads = static_cast<int>(H);
+  k.headdim = static_cast<int>(P);
+  k.dstate = static_cast<int>(N);
+  k.groups = static_cast<int>(G);
+  k.width = static_cast<int>(W);
+  k.softplus = a->delta_softplus != 0 ? 1 : 0;
+  k.cache_slots = static_cast<int>(a->cache_slots);
+  std::memcpy(k.sx, a->xbc_stride, sizeof(k.sx));
+  std::memcpy(k.sdt, a->dt_stride, sizeof(k.sdt));
+  std::memcpy(k.sw, a->weight_stride, sizeof(k.sw));
+  std::memcpy(k.sz, a->z_stride, sizeof(k.sz));
+  std::memcpy(k.so, a->out_stride, sizeof(k.so));
+  k.sstate = a->state_stride;
+  k.swin = a->window_stride;
+  k.xbc = a->xbc;
+  k.dt = a->dt_raw;
+  k.A_log = a->A_log;
+  k.weight = a->weight;
+  k.bias = a->bias;
+  k.D = a->D;
+  k.z = a->z;
+  k.dt_bias = a->dt_bias;
+  k.slots = a->slots;
+  k.state = a->state;
+  k.window = a->window;
+  k.out = a->out;
+  k.u = static_cast<float*>(a->workspace);
+  const hipError_t e = mss::launch_head_step(k, a->io_dtype == MSS_BF16, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
+}
+
+mss_status mss_rms_norm(const mss_norm_args* a, void* stream) {
+  if (a == nullptr || a->struct_size != sizeof(mss_norm_args) || a->reserved0 != 0) return MSS_ERR_BAD_STRUCT;
+  if (bad_dtype(a->io_dtype) || bad_dtype(a->residual_dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
+  if (a->quant != MSS_QUANT_NONE && a->quant != MSS_QUANT_ROW && a->quant != MSS_QUANT_BLOCK)
+    return MSS_ERR_BAD_STRUCT;
+  const int64_t R = a->rows, D = a->dim;
+  if (R < 1 || R > kMaxInt || D < 1 || D > kMaxNormDim ||
+      (a->quant == MSS_QUANT_BLOCK && D % MSS_SCALE_BLOCK != 0) || !(a->eps >= 0.0f))
+    return MSS_ERR_BAD_SHAPE;
+  if (a->x == nullptr || a->weight == nullptr || a->out == nullptr ||
+      (a->quant != MSS_QUANT_NONE && a->scale == nullptr))
+    return MSS_ERR_NULL_POINTER;
+  const int64_t es = elem(a->io_dtype), rs = elem(a->residual_dtype);
+  const int64_t eso = a->quant == MSS_QUANT_NONE ? es : 1;
+  const bool in_place = a->residual_out != nullptr && a->residual_out == a->residual;
+  if (a->x_stride < 0 || (a->residual != nullptr && a->residual_stride < 0) ||
+      (R > 1 && (a->out_stride < D || (a->residual_out != nullptr && a->residual_out_stride < D) ||
+                 (in_place && a->residual_out_stride != a->residual_stride))))
+    return MSS_ERR_BAD_STRIDE;
+  if (!aligned(a->x, es) || !aligned(a->residual, rs) || !aligned(a->weight, 4) || !aligned(a->out, eso) ||
+      !aligned(a->scale, 4) || !aligned(a->residual_out, rs))
+    return MSS_ERR_MISALIGNED;
+  const int64_t sz[2] = {R, D};
+  auto rows = [&](const void* p, int64_t stride, int64_t e) {
+    const int64_t st[2] = {stride, 1};
+    return extent_of(p, sz, st, 2, e);
+  };
+  const int64_t nscale = a->quant == MSS_QUANT_BLOCK ? R * (D / MSS_SCALE_BLOCK) : R;
+  const Extent ex = rows(a->x, a->x_stride, es), er = rows(a->residual, a->residual_stride, rs);
+  const Extent ew = vec(a->weight, D, 4);
+  const Extent eo = rows(a->out, a->out_stride, eso), ero = rows(a->residual_out, a->residual_out_stride, rs);
+  const Extent esc = a->quant == MSS_QUANT_NONE ? Extent{} : vec(a->scale, nscale, 4);
+  const Extent ins[] = {ex, er, ew};
+  if (any_overlap(eo, ins) || any_overlap(esc, ins) || overlaps(ero, ex) || overlaps(ero, ew) ||
+      (!in_place && overlaps(ero, er)) || overlaps(eo, ero) || overlaps(eo, esc) || overlaps(ero, esc))
+    return MSS_ERR_ALIASING;
+  mss::NormArgs k{};
+  k.rows = R;
+  k.dim = static_cast<int>(D);
+  k.sx = a->x_stride;
+  k.sr = a->residual_stride;
+  k.so = a->out_stride;
+  k.sro = a->residual_out_stride;
+  k.eps = a->eps;
+  k.x = a->x;
+  k.res = a->residual;
+  k.weight = a->weight;
+  k.out = a->out;
+  k.scale = a->scale;
+  k.res_out = a->residual_out;
+  const hipError_t e = mss::launch_norm(k, a->io_dtype == MSS_BF16, a->residual_dtype == MSS_BF16, a->quant,
+                                        static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
+}
+
+}  // extern "C"

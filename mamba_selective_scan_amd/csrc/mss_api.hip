@@ -11,6 +11,7 @@
 
 #include "mss.h"
 #include "mss_internal.hpp"
+#include "mss_checks.hpp"
 #include "mss_cplx.hpp"
 
 namespace {
@@ -18,6 +19,12 @@ namespace {
 using mss::kCh;
 using mss::kMaxState;
 using mss::kT;
+using mss::Extent;
+using mss::aligned;
+using mss::extent_of;
+using mss::non_overlapping;
+using mss::overlaps;
+using mss::strides_nonneg;
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxSeqlen = int64_t{1} << 30;  // time indices, padded, stay in int32
@@ -38,23 +45,6 @@ constexpr int64_t kTargetTiles = 4096;
 constexpr int64_t kAggWaves = 8 * 1024;
 constexpr int64_t kAggMinPartChunks = 4;
 
-struct Extent {
-  uintptr_t lo = 0, hi = 0;  // byte range [lo, hi)
-  bool valid = false;
-};
-
-Extent extent_of(const void* p, const int64_t* sizes, const int64_t* strides, int rank,
-                 int64_t elem) {
-  Extent e;
-  if (p == nullptr) return e;
-  int64_t span = 0;
-  for (int i = 0; i < rank; ++i) span += (sizes[i] - 1) * strides[i];
-  e.lo = reinterpret_cast<uintptr_t>(p);
-  e.hi = e.lo + static_cast<uintptr_t>((span + 1) * elem);
-  e.valid = true;
-  return e;
-}
-
 // Bytes of the chunk-state array: [ceil(L / 16)][batch][dim][16] fp32.
 Extent chunk_states_extent(const void* p, int64_t batch, int64_t dim, int64_t seqlen) {
   Extent e;
@@ -66,36 +56,8 @@ Extent chunk_states_extent(const void* p, int64_t batch, int64_t dim, int64_t se
   return e;
 }
 
-bool overlaps(const Extent& a, const Extent& b) {
-  return a.valid && b.valid && a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned(const void* p, int64_t a) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(a)) == 0;
-}
-
 void norm_strides(int64_t* out, const int64_t* st, const int64_t* sizes) {
   for (int i = 0; i < 3; ++i) out[i] = sizes[i] == 1 ? 1 : st[i];
-}
-
-bool strides_nonneg(const int64_t* st, int rank) {
-  for (int i = 0; i < rank; ++i)
-    if (st[i] < 0) return false;
-  return true;
-}
-
-// Distinct indices map to distinct elements (needed for outputs only).
-bool non_overlapping(const int64_t* sizes, const int64_t* strides, int rank) {
-  int idx[3] = {0, 1, 2};
-  std::sort(idx, idx + rank, [&](int a, int b) { return strides[a] < strides[b]; });
-  int64_t need = 1;
-  for (int k = 0; k < rank; ++k) {
-    const int i = idx[k];
-    if (sizes[i] == 1) continue;
-    if (strides[i] < need) return false;
-    need = strides[i] * sizes[i];
-  }
-  return true;
 }
 
 // Each kCh-channel x kT-step tile (16-state x kT-step for B and C) is
@@ -530,9 +492,9 @@ const char* mss_status_string(mss_status status) {
     case MSS_ERR_BAD_SHAPE: return "invalid shape (sizes must be >= 1 and fit the grid; conv width 1..4)";
     case MSS_ERR_BAD_STRIDE: return "invalid stride (negative, overlapping output, or a tile spans >= 2 GiB)";
     case MSS_ERR_UNSUPPORTED_DTYPE: return "unsupported io dtype (expected MSS_F32 or MSS_BF16)";
-    case MSS_ERR_UNSUPPORTED_DSTATE: return "dstate must be between 1 and 16";
+    case MSS_ERR_UNSUPPORTED_DSTATE: return "dstate must be between 1 and 16 (head-wise operations: 1 and 128)";
     case MSS_ERR_MISALIGNED: return "a pointer is not aligned to its element size";
-    case MSS_ERR_WORKSPACE_TOO_SMALL: return "workspace missing or smaller than mss_selective_scan_workspace_size";
+    case MSS_ERR_WORKSPACE_TOO_SMALL: return "workspace missing or smaller than the workspace_size function of the call says";
     case MSS_ERR_ALIASING: return "an output overlaps an input";
     case MSS_ERR_BAD_STRUCT: return "arguments struct is NULL, of the wrong size, or has reserved fields set";
     case MSS_ERR_HIP: return "the HIP runtime reported an error while enqueuing";
