@@ -72,6 +72,34 @@ mss_status check_scan_shape(const mss_head_scan_args* a) {
   return check_head_shape(a->heads, a->headdim, a->dstate, a->groups);
 }
 
+// How a head-wise scan is cut over time: prompts longer than seg_len run as
+// segments, so that a few long prompts still fill the card.  From the sizes
+// alone: the prompts' lengths stay on the device.
+struct HeadScanPlan {
+  int64_t ptiles, tiles, seg_len = 0, cut_slots = 0, cut_prompts = 0;
+  size_t parts = 0, workspace = 0;
+};
+constexpr int64_t kHeadSegTiles = 512;  // workgroups wanted: two a CU
+constexpr int64_t kHeadSegMin = 256;    // tokens of a segment at least
+
+HeadScanPlan head_scan_plan(const mss_head_scan_args* a) {
+  HeadScanPlan p;
+  p.ptiles = (a->headdim + 31) / 32;
+  p.tiles = a->groups * ((a->heads / a->groups * p.ptiles + 3) / 4);
+  int64_t seg = std::max(kHeadSegMin, (a->tokens * p.tiles + kHeadSegTiles - 1) / kHeadSegTiles);
+  seg = (seg + 63) / 64 * 64;
+  if (seg < a->tokens) {
+    // a cut prompt has more than seg tokens, so at most 2 len / seg segments
+    p.seg_len = seg;
+    p.cut_slots = 2 * a->tokens / seg;
+    p.cut_prompts = std::min(a->seqs, a->tokens / seg);
+    const size_t states = static_cast<size_t>(a->heads * a->headdim * a->dstate) * 4;
+    p.parts = (p.cut_slots * states + 255) / 256 * 256;
+    p.workspace = p.parts + static_cast<size_t>(p.cut_slots * a->heads) * 4;
+  }
+  return p;
+}
+
 mss_status check_step_shape(const mss_head_step_args* a) {
   if (a == nullptr || a->struct_size != sizeof(mss_head_step_args) || a->reserved0 != 0)
     return MSS_ERR_BAD_STRUCT;
@@ -156,7 +184,7 @@ mss_status mss_causal_conv1d_prompts(const mss_conv_prompts_args* a, void* strea
 size_t mss_head_scan_prompts_workspace_size(const mss_head_scan_args* a, mss_status* status) {
   const mss_status st = check_scan_shape(a);
   if (status != nullptr) *status = st;
-  return 0;
+  return st == MSS_OK ? head_scan_plan(a).workspace : 0;
 }
 
 mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
@@ -198,9 +226,23 @@ mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
   const Extent eo = any ? extent_of(a->out, xs, a->out_stride, 3, es) : none;
   const Extent es_ = cache_extent(a->state, a->cache_slots, H * P * N, a->state_stride, 4);
   if (any_overlap(eo, ins) || any_overlap(es_, ins) || overlaps(eo, es_)) return MSS_ERR_ALIASING;
-  if (a->seqs * H > kMaxInt / ((P + 15) / 16)) return MSS_ERR_BAD_SHAPE;
+  const HeadScanPlan plan = head_scan_plan(a);
+  if ((a->seqs + plan.cut_slots) * plan.tiles > kMaxInt ||
+      plan.cut_prompts * ((H * P * N + 1023) / 1024) > kMaxInt)
+    return MSS_ERR_BAD_SHAPE;
+  if (plan.workspace > 0) {
+    if (a->workspace == nullptr || a->workspace_bytes < plan.workspace) return MSS_ERR_WORKSPACE_TOO_SMALL;
+    const Extent ew = vec(a->workspace, static_cast<int64_t>(plan.workspace), 1);
+    if (any_overlap(ew, ins) || overlaps(ew, eo) || overlaps(ew, es_)) return MSS_ERR_ALIASING;
+  }
 
   mss::HeadScanArgs k{};
+  k.ptiles = static_cast<int>(plan.ptiles);
+  k.seg_len = static_cast<int>(plan.seg_len);
+  k.cut_slots = static_cast<int>(plan.cut_slots);
+  k.cut_prompts = static_cast<int>(plan.cut_prompts);
+  k.parts = static_cast<float*>(a->workspace);
+  k.decays = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + plan.parts);
   k.q = prompts(T, a->seqs, a->cache_slots, a->cu_seqlens, a->slots, a->resume);
   k.heads = static_cast<int>(H);
   k.headdim = static_cast<int>(P);

@@ -48,6 +48,12 @@ struct HeadScanArgs {
   const float* dt_bias;
   float* state;
   void* out;
+  int ptiles;       // 32-column tiles of a head
+  int seg_len;      // longer prompts are cut into segments of at most this many tokens (0: none is)
+  int cut_slots;    // room for the segments of all cut prompts
+  int cut_prompts;  // at most this many prompts are cut
+  float* parts;     // workspace [cut_slots][H][P][N]
+  float* decays;    // workspace [cut_slots][H]
 };
 
 struct HeadStepArgs {

@@ -267,7 +267,7 @@ def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=
     y = r / sqrt(mean(r^2) + eps) * weight, with weight [D] fp32.
 
     quant None: returns y in x's dtype.  quant "row": returns (q, scale) with q
-    float8_e4m3fn and scale [R] fp32, y = q * scale; quant "block": scale
+    float8_e4m3fn and scale [R, 1] fp32, y = q * scale; quant "block": scale
     [R, D / 128].  With a residual, r in the residual's dtype is returned last;
     ``residual_out`` may be ``residual`` itself, which is then updated in place.
     """
@@ -291,7 +291,7 @@ def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=
     if quant is not None:
         if quant == "block" and dim % _lib.MSS_SCALE_BLOCK:
             raise ValueError(f"quant 'block' needs a multiple of {_lib.MSS_SCALE_BLOCK} columns, got {dim}")
-        want = (rows,) if quant == "row" else (rows, dim // _lib.MSS_SCALE_BLOCK)
+        want = (rows, 1 if quant == "row" else dim // _lib.MSS_SCALE_BLOCK)
         if scale is None:
             scale = torch.empty(want, dtype=torch.float32, device=dev)
         elif not _like(scale, "scale", want, torch.float32, dev).is_contiguous():

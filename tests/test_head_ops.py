@@ -161,6 +161,45 @@ def test_scan_lengths(mss, lens, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,heads,headdim,dstate", [((1500, 3, 700, 0, 257), 3, 64, 128), ((513,), 2, 33, 20),
+                                                       ((2305, 256, 257), 1, 32, 64)])
+def test_scan_cut_over_time(mss, lens, heads, headdim, dstate, io):
+    """Prompts long enough to run as segments, next to some that are not."""
+    v, c = scan_inputs(gen(9), lens, heads, headdim, dstate, 1, io, extra=1, rates=(-2.0, 2.0))
+    scan_check(mss, f"scan cut {lens} {io}", v, c)
+    c["resume"] = c["slots"] = None
+    scan_check(mss, f"scan cut fresh {lens} {io}", v, c)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,at", [((100,), 37), ((700, 40), 300)])
+def test_scan_is_causal_past_nan_and_infinity(mss, lens, at, io):
+    """What follows an infinity or a NaN in x or B is what the recurrence gives;
+    what comes before it is as without it."""
+    v, c = scan_inputs(gen(10), lens, 2, 40, 24, 1, io)
+    c["resume"] = None
+    v["D"] = None
+    args = lambda: (v["x"], v["dt_raw"], v["A_log"], v["B"], v["C"], v["D"], v["z"], v["dt_bias"])  # noqa: E731
+    clean = mss.head_scan_prompts(*args(), cu_seqlens=c["cu"], state=c["state"].clone(), slots=c["slots"])
+    for name, index, value in [("x", (at, 1, 3), float("nan")), ("x", (at, 1, 3), float("inf")),
+                               ("B", (at, 0, 5), float("-inf"))]:
+        kept = v[name].clone()
+        v[name][index] = value
+        state = c["state"].clone()
+        got = mss.head_scan_prompts(*args(), cu_seqlens=c["cu"], state=state, slots=c["slots"])
+        want, wstate = ref.scan_prompts(*args(), c["cu"], c["state"], c["slots"])
+        torch.cuda.synchronize()
+        got, state, clean_ = ref.d(got), ref.d(state), ref.d(clean)
+        for what, x, y in (("out", got, want), ("state", state, wstate)):
+            for test in (torch.isnan, torch.isinf):
+                wrong = int((test(x) != test(y)).sum())
+                assert wrong == 0, f"{name} {value}: {wrong} values of {what} differ in {test.__name__}"
+        # the same sums, a chunk's in another order
+        ref.within(f"{name} {value} before", got[:at], clean_[:at], 2.0 ** -6 * clean_[:at].abs().amax((0, 2), True))
+        v[name].copy_(kept)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("heads,headdim,dstate,groups",
                          [(1, 1, 1, 1), (3, 5, 7, 3), (5, 33, 17, 1), (4, 48, 64, 4), (2, 130, 100, 1),
                           (7, 64, 16, 7), (9, 32, 128, 3), (8, 96, 24, 2)])
@@ -475,7 +514,7 @@ def test_captured_run(mss):
         g2 = gen(13)
         return (randn(g2, 3, heads, headdim, dstate), randn(g2, 3, chans, 3, dtype=torch.bfloat16),
                 (torch.zeros(t, heads, headdim, dtype=torch.bfloat16, device="cuda"),
-                 torch.zeros(t, n, dtype=torch.uint8, device="cuda"), torch.zeros(t, device="cuda"),
+                 torch.zeros(t, n, dtype=torch.uint8, device="cuda"), torch.zeros(t, 1, device="cuda"),
                  torch.zeros(3, heads, headdim, dtype=torch.bfloat16, device="cuda")))
 
     eager, graphed = buffers(), buffers()
