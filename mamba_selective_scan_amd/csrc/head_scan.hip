@@ -56,15 +56,18 @@ template <typename IO>
 struct Frag;
 template <>
 struct Frag<bf16_t> {
-  bf16x8 v;
-  __device__ inline float get(int e) const { return static_cast<float>(v[e]); }
-  __device__ inline void set(int e, float x) { v[e] = static_cast<__bf16>(x); }
+  union {
+    bf16x8 v;
+    uint32_t w[4];
+  };
+  __device__ inline float get(int e) const { return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16); }
+  __device__ inline void set2(int e, float x, float y) { w[e / 2] = bf16x2_bits(x, y); }
 };
 template <>
 struct Frag<float> {
   float v[8];
   __device__ inline float get(int e) const { return v[e]; }
-  __device__ inline void set(int e, float x) { v[e] = x; }
+  __device__ inline void set2(int e, float x, float y) { v[e] = x, v[e + 1] = y; }
 };
 
 __device__ inline f32x4 mma(const Frag<bf16_t>& a, const Frag<bf16_t>& b, f32x4 acc) {
@@ -86,30 +89,43 @@ __device__ inline float long_decay(float x) { return fmaxf(fast_exp2(x), 1.17549
 __device__ constexpr int tok(int e) { return (e & 1) | ((e & 2) << 1) | ((e & 4) >> 1); }
 
 // ------------------------------------------------------- LDS tiles
-// Row-major [rows][COLS], 16-byte chunks swizzled by the row.
+// Row-major [rows][COLS], 16-byte chunks swizzled by the row.  A lane's address
+// is formed once (`lane_*`); each read xors a constant into its swizzled bits
+// and adds a constant, so the reads of a loop share a few addresses.
 template <typename IO, int COLS>
 struct Tile {
   static constexpr int kChunks = COLS * static_cast<int>(sizeof(IO)) / 16;  // of a row: 4 or more
   static constexpr int kElems = 16 / sizeof(IO);
-  __device__ static inline int offset(int row, int chunk) {
-    const int s = kChunks >= 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
-    return (row * kChunks + s) * 16;
-  }
-  // row r, columns col .. col+7 (col a multiple of 8)
-  __device__ static inline Frag<IO> row(const char* t, int r, int col) {
+  static constexpr int kRow = COLS * static_cast<int>(sizeof(IO));          // bytes
+  static constexpr int kMask = kChunks >= 8 ? 7 : 3;
+  __device__ static inline int swizzle(int row) { return kChunks >= 8 ? row & 7 : (row >> 1) & 3; }
+  __device__ static inline int offset(int row, int chunk) { return row * kRow + (chunk ^ swizzle(row)) * 16; }
+  // byte distance and xor that take a lane from a chunk to the one `by` (a constant) further
+  __device__ static constexpr int flip(int by) { return (by & kMask) * 16; }
+  __device__ static constexpr int ahead(int by) { return (by & ~kMask) * 16; }
+
+  // Row fragments: row r, columns 32 q + 8 g .. + 7.  Rows 16 apart share an address.
+  __device__ static inline int lane_row(int r, int g) { return offset(r, sizeof(IO) == 2 ? g : 2 * g); }
+  __device__ static inline Frag<IO> row(const char* t, int lane, int rows, int q) {
     Frag<IO> f;
     if constexpr (sizeof(IO) == 2) {
-      f.v = *reinterpret_cast<const bf16x8*>(t + offset(r, col / 8));
+      f.v = *reinterpret_cast<const bf16x8*>(t + (lane ^ flip(4 * q)) + ahead(4 * q) + rows * kRow);
     } else {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(t + offset(r, col / 4));
-      const f32x4 b = *reinterpret_cast<const f32x4*>(t + offset(r, col / 4 + 1));
+      const f32x4 a = *reinterpret_cast<const f32x4*>(t + lane + ahead(8 * q) + rows * kRow);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(t + (lane ^ 16) + ahead(8 * q) + rows * kRow);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f.v[i] = a[i], f.v[4 + i] = b[i];
     }
     return f;
   }
-  // rows r0 + tok(0..7), one column a lane: col0 + 8 (c / 4) + c % 4 + 4 half
-  __device__ static inline Frag<IO> col(const char* t, int r0, int col0, int half, int c) {
+  // Column fragments: rows 32 ks + 8 g + tok(0..7), one column a lane: 32 q +
+  // 8 (c / 4) + c % 4 + 4 half.  bf16: the lane names 4 columns of one row and
+  // receives 4 rows of its column.
+  __device__ static inline int lane_col(int g, int c) {
+    if constexpr (sizeof(IO) == 2) return offset(8 * g + ((c >> 2) & 1) + ((c >> 1) & 4), c & 3);
+    return offset(8 * g, 2 * (c >> 2)) + 4 * (c & 3);
+  }
+  __device__ static inline Frag<IO> col(const char* t, int lane, int ks, int q, int half) {
     Frag<IO> f;
     if constexpr (sizeof(IO) == 2) {
       union {
@@ -118,18 +134,18 @@ struct Tile {
       } u;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // the lane names 4 columns of one row; it receives 4 rows of its column
-        const int lr = c >> 2;
-        const int r = r0 + (lr & 1) + ((lr & 2) << 1) + 2 * h;
-        char* p = const_cast<char*>(t) + offset(r, col0 / 8 + (c & 3)) + 8 * half;
+        // two rows on: bit 1 of the row, which is bit 1 of an 8-chunk swizzle
+        // and bit 0 of a 4-chunk one
+        const int x = flip(4 * q) ^ (h ? (kChunks >= 8 ? 32 : 16) : 0);
+        char* p = const_cast<char*>(t) + (lane ^ x) + ahead(4 * q) + (32 * ks + 2 * h) * kRow + 8 * half;
         u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
       }
       f.v = u.v;
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        f.v[e] = *reinterpret_cast<const float*>(t + offset(r0 + tok(e), (col0 + 8 * (c >> 2) + 4 * half) / 4) +
-                                                 4 * (c & 3));
+        f.v[e] = *reinterpret_cast<const float*>(t + (lane ^ ((tok(e) ^ half) * 16)) + ahead(8 * q) +
+                                                 (32 * ks + tok(e)) * kRow);
     }
     return f;
   }
@@ -152,19 +168,79 @@ __device__ inline u32x4 load16(const IO* p, int n) {
   return u.v;
 }
 
-// Whether any of the elements is an infinity or a NaN.
+// `rows` rows `stride` bytes apart: offsets past them read as 0 and write
+// nothing.  (A row's columns end before the next row starts.)
+__device__ inline __amdgpu_buffer_rsrc_t rows_of(const void* p, int rows, int stride) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, rows * stride, kRsrcFlags);
+}
+__device__ inline u32x4 buf_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// 8 elements as they lie in memory (16 or 32 bytes), as fp32, and back.
 template <typename IO>
-__device__ inline bool not_finite(u32x4 v) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+struct Raw8 {
+  u32x4 v[sizeof(IO) / 2];
+  __device__ inline float get(int e) const {
+    if constexpr (sizeof(IO) == 2)
+      return __uint_as_float(e & 1 ? v[0][e / 2] & 0xffff0000u : v[0][e / 2] << 16);
+    else
+      return __uint_as_float(v[e / 4][e & 3]);
+  }
+  __device__ inline void set(const float* f) {
     if constexpr (sizeof(IO) == 2) {
-      top |= ((v[i] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[0][i] = bf16x2_bits(f[2 * i], f[2 * i + 1]);
     } else {
-      top |= ((v[i] & 0x7fffffffu) + 0x00800000u) & 0x80000000u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i / 4][i & 3] = __float_as_uint(f[i]);
     }
   }
-  return top != 0;
+};
+
+// Largest exponent fields seen: 0x7f80 in one of the halves (the whole, in
+// fp32) tells an infinity or a NaN.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <typename IO>
+__device__ inline uint32_t top_exponents(u32x4 v, uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(IO) == 2)
+      top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, v[i] & 0x7f807f80u),
+                                                                   __builtin_bit_cast(u16x2, top)));
+    else
+      top = max(top, v[i] & 0x7f800000u);
+  }
+  return top;
+}
+template <typename IO>
+__device__ inline bool not_finite(uint32_t top) {
+  return sizeof(IO) == 2 ? (top >> 16) == 0x7f80u || (top & 0xffffu) == 0x7f80u : top == 0x7f800000u;
+}
+
+// Sums over the lanes up to each one, in 64 bits: rotations within the 16-lane
+// rows, then each row's last lane broadcast into the next row, and lane 31 into
+// the upper half.
+template <int CTRL, int ROWS>
+__device__ inline double add_moved(double v) {
+  const uint64_t b = __double_as_longlong(v);
+  const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xF, true);
+  const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xF, true);
+  return v + __longlong_as_double((static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32) | static_cast<uint32_t>(lo));
+}
+__device__ inline double lane_sums(double v) {
+  v = add_moved<0x111, 0xF>(v);  // row_shr:1
+  v = add_moved<0x112, 0xF>(v);
+  v = add_moved<0x114, 0xF>(v);
+  v = add_moved<0x118, 0xF>(v);
+  v = add_moved<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  return add_moved<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+}
+__device__ inline double lane_value(double v, int l) {
+  const uint64_t b = __double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), l);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), l);
+  return __longlong_as_double((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
 // ------------------------------------------------------- segments
@@ -220,6 +296,49 @@ __device__ inline Where find_cut(const HeadScanArgs& a, int at, bool by_prompt) 
 
 // ------------------------------------------------------- the walk
 
+// What a chunk's tokens contribute to its exponentials, one value a token and
+// wave.  e^(c_i - c_j) is taken as a product of two factors about a reference
+// between them: for the 16 x 32 piece (it, ks) of the triangle the sum at token
+// 32 ks + 15 where the piece meets the diagonal (near), at token 31 for the
+// pieces past the first 32 tokens (far).  The near factors may exceed 1, by as
+// much as 16 tokens decay; a chunk where one passes 2^kSteep takes each
+// exponential by itself.
+constexpr float kSteep = 100.0f;
+// Values that are formed anew at each place that uses them.  The walk's loop
+// needs nearly every register for its tiles: addresses kept across it would push
+// them out to memory, and each of their reloads would wait for every load in
+// flight.
+__device__ inline int anew(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+__device__ inline int thread_anew() {
+  int v = threadIdx.x;
+  asm volatile("" : "+v"(v));
+  return v;
+}
+typedef const __attribute__((address_space(4))) HeadScanArgs* KernelArgs;
+__device__ inline KernelArgs args_anew() {
+  auto p = (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+// Keeps the reads of one step from moving up into the step before, where their
+// registers are still in use.
+__device__ inline void step_end() { __builtin_amdgcn_sched_barrier(0); }
+
+template <int Q>
+struct Times {
+  float enter[Q];       // e^c_i
+  float row_near[Q];    // e^(c_i - near)
+  float col_near[Q];    // delta_j e^(near - c_j)
+  float row_far[Q];     // e^(c_i - far), i >= 32
+  float col_far[Q];     // delta_j e^(far - c_j), j < 32
+  float left[Q];        // delta_j e^(c_Q - c_j)
+  float sum[2][Q];      // c_i as two floats, in powers of two
+  float delta[Q];
+};
+
 template <typename IO, int NP, int Q>
 struct Shape {
   static constexpr int kUnits = Q == 64 ? 6 : 2;  // 32 x 16 pieces of the lower triangle
@@ -230,28 +349,28 @@ struct Shape {
     char c[Q * NP * sizeof(IO)];
     char x[kWaves][Q * kCols * sizeof(IO)];
     f32x4 s[kUnits * 2][64];
-    float sum[kWaves][2][Q];   // c_i as two floats, in powers of two
-    float delta[kWaves][Q];
-    float left[kWaves][Q];     // delta_j e^(c_Q - c_j)
-    int odd[2];                // a chunk holds something not finite
+    Times<Q> time[2][kWaves];
+    int odd[2];  // a chunk holds something not finite
   };
 };
 
-// AGG: only what a segment adds to a zero state, and its decay.
-template <typename IO, int NP, int Q, bool AGG>
+// AGG: only what a segment adds to a zero state, and its decay.  VEC: rows are
+// whole 16-byte vectors (else element by element at their ends).
+template <typename IO, int NP, int Q, bool AGG, bool VEC>
 __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   using S = Shape<IO, NP, Q>;
   using BC = typename S::BC;
   using X = typename S::X;
   constexpr int kE = 16 / sizeof(IO);
+  constexpr int kES = sizeof(IO);
   constexpr int kK = NP / 32;                          // K-steps over the states
   constexpr int kT = Q / 32;                           // K-steps over the tokens
   constexpr int kLoadBC = Q * BC::kChunks / 256;       // 16-byte loads a thread
   constexpr int kLoadX = Q * X::kChunks / 64;          // 16-byte loads a lane
+  constexpr int kRowsBC = 256 / BC::kChunks, kRowsX = 64 / X::kChunks;  // rows between them
   __shared__ __attribute__((aligned(16))) typename S::Lds lds;
 
-  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int g = lane >> 4, c = lane & 15;
+  const int wave = uniform(threadIdx.x >> 6);
 
   // which tile of which segment
   const int jobs = a.heads / a.groups * a.ptiles;      // of one group
@@ -273,8 +392,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   const int slot = slot_of(a.q.slots, a.q.cache_slots, w.seq);
   if (slot < 0) return;
   const int per = segment_tokens<Q>(len, w.nseg);
-  const int begin = sp.begin + w.seg * per;
-  const int end = min(sp.end, begin + per);
+  const int begin = uniform(sp.begin + w.seg * per);
+  const int end = uniform(min(sp.end, begin + per));
   const bool cut = w.nseg > 1;
   const bool from_cache = resumes(a.q, w.seq);
   if (len == 0 && from_cache) return;
@@ -289,269 +408,418 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 
   // the state: tile [n = 32 q + 8 g + 4 tn + r][p = 8 (c / 4) + c % 4 + 4 tp]
   f32x4 st[kK][2][2];
-  const int pcol = 8 * (c >> 2) + (c & 3);
-  const float* enter = AGG ? nullptr : cut ? part : from_cache ? cache : nullptr;
+  // where this tile's state lies in memory: what a cut prompt's segment enters
+  // with or adds, or the prompt's cache entry
+  float* home = cut ? part : cache;
+  auto state_in = [&](bool from) __attribute__((always_inline)) {
+    const int th = thread_anew(), n0 = 8 * ((th >> 4) & 3), N = anew(a.dstate);
+    const float* at = home + static_cast<int64_t>(8 * ((th >> 2) & 3) + (th & 3)) * N + n0;
+    const int ps = pc - 8 * ((th >> 2) & 3) - (th & 3);
 #pragma unroll
-  for (int q = 0; q < kK; ++q)
+    for (int q = 0; q < kK; ++q)
 #pragma unroll
-    for (int tp = 0; tp < 2; ++tp) {
-      const int p = pcol + 4 * tp, n = 32 * q + 8 * g;
-      float v[8] = {};
-      if (enter != nullptr) load_part<float, 8>(enter + static_cast<int64_t>(p) * a.dstate + n, p < pc ? a.dstate - n : 0, v);
+      for (int tp = 0; tp < 2; ++tp) {
+        float v[8] = {};
+        if (from) load_part<float, 8>(at + 4 * tp * N + 32 * q, 4 * tp < ps ? N - n0 - 32 * q : 0, v);
 #pragma unroll
-      for (int tn = 0; tn < 2; ++tn)
-        st[q][tn][tp] = f32x4{v[4 * tn], v[4 * tn + 1], v[4 * tn + 2], v[4 * tn + 3]};
-    }
+        for (int e = 0; e < 8; ++e) st[q][e >> 2][tp][e & 3] = v[e];
+        step_end();
+      }
+  };
+  auto state_out = [&]() __attribute__((always_inline)) {
+    const int th = thread_anew(), n0 = 8 * ((th >> 4) & 3), N = anew(a.dstate);
+    float* at = home + static_cast<int64_t>(8 * ((th >> 2) & 3) + (th & 3)) * N + n0;
+    const int ps = pc - 8 * ((th >> 2) & 3) - (th & 3);
+#pragma unroll
+    for (int q = 0; q < kK; ++q)
+#pragma unroll
+      for (int tp = 0; tp < 2; ++tp) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = st[q][e >> 2][tp][e & 3];
+        store_part<float, 8>(at + 4 * tp * N + 32 * q, 4 * tp < ps ? N - n0 - 32 * q : 0, v);
+        step_end();
+      }
+  };
+  state_in(!AGG && (cut || from_cache));
 
-  const IO* xh = static_cast<const IO*>(a.x) + h * a.sx[1] + p0;
-  const IO* Bg = static_cast<const IO*>(a.B) + grp * a.sB[1];
-  const IO* Cg = static_cast<const IO*>(a.C) + grp * a.sC[1];
-  const IO* dth = static_cast<const IO*>(a.dt) + h * a.sdt[1];
   const float rate = -expf(a.A_log[h]) * kLog2e;
   const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
   const float skip = a.D != nullptr ? a.D[h] : 0.0f;
 
   u32x4 pb[kLoadBC], pcc[AGG ? 1 : kLoadBC], px[kLoadX];
-  float pdt = 0.0f;
   auto fetch = [&](int t) __attribute__((always_inline)) {
+    const KernelArgs k = args_anew();
+    const int th = thread_anew();
+    // this thread's chunks of B and C, and this lane's of x: row and column of the first
+    const int rb = th / BC::kChunks, nb = th % BC::kChunks * kE;
+    const int rx = (th & 63) / X::kChunks, nx = (th & 63) % X::kChunks * kE;
+    const IO* xh = static_cast<const IO*>(k->x) + t * k->sx[0] + h * k->sx[1] + p0;
+    const IO* Bg = static_cast<const IO*>(k->B) + t * k->sB[0] + grp * k->sB[1];
+    const IO* Cg = static_cast<const IO*>(k->C) + t * k->sC[0] + grp * k->sC[1];
+    if constexpr (VEC) {
+      // byte offsets from the chunk's first row (a tile spans less than 2 GiB)
+      const int eB = static_cast<int>(k->sB[0]) * kES, eC = static_cast<int>(k->sC[0]) * kES;
+      const int eX = static_cast<int>(k->sx[0]) * kES;
+      const int rows = max(min(end - t, Q), 0);
+      uint32_t o = nx < pc ? rx * eX + nx * kES : kOffNone;
+      const auto rX = rows_of(xh, rows, eX);
 #pragma unroll
-    for (int i = 0; i < kLoadBC; ++i) {
-      const int k = i * 256 + static_cast<int>(threadIdx.x);
-      const int r = t + k / BC::kChunks, n = k % BC::kChunks * kE;
-      const int valid = r < end ? a.dstate - n : 0;
-      pb[i] = load16<IO>(Bg + r * a.sB[0] + n, valid);
-      if constexpr (!AGG) pcc[i] = load16<IO>(Cg + r * a.sC[0] + n, valid);
-    }
+      for (int i = 0; i < kLoadX; ++i, o += kRowsX * eX) px[i] = buf_load16(rX, o);
+      o = nb < k->dstate ? rb * eB + nb * kES : kOffNone;
+      const auto rB = rows_of(Bg, rows, eB);
 #pragma unroll
-    for (int i = 0; i < kLoadX; ++i) {
-      const int k = i * 64 + lane;
-      const int r = t + k / X::kChunks, p = k % X::kChunks * kE;
-      px[i] = load16<IO>(xh + r * a.sx[0] + p, r < end ? pc - p : 0);
+      for (int i = 0; i < kLoadBC; ++i, o += kRowsBC * eB) pb[i] = buf_load16(rB, o);
+      if constexpr (!AGG) {
+        o = nb < k->dstate ? rb * eC + nb * kES : kOffNone;
+        const auto rC = rows_of(Cg, rows, eC);
+#pragma unroll
+        for (int i = 0; i < kLoadBC; ++i, o += kRowsBC * eC) pcc[i] = buf_load16(rC, o);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoadBC; ++i) {
+        const int r = rb + i * kRowsBC;
+        const int valid = t + r < end ? k->dstate - nb : 0;
+        pb[i] = load16<IO>(Bg + r * k->sB[0] + nb, valid);
+        if constexpr (!AGG) pcc[i] = load16<IO>(Cg + r * k->sC[0] + nb, valid);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoadX; ++i) {
+        const int r = rx + i * kRowsX;
+        px[i] = load16<IO>(xh + r * k->sx[0] + nx, t + r < end ? pc - nx : 0);
+      }
     }
-    const int r = t + lane;
-    pdt = lane < Q && r < end ? io_traits<IO>::load(dth + r * a.sdt[0]) : 0.0f;
+  };
+  // one token a lane (past the segment's end: its last one, which is not used)
+  auto fetch_dt = [&](int t) __attribute__((always_inline)) {
+    const KernelArgs k = args_anew();
+    const IO* dth = static_cast<const IO*>(k->dt) + h * k->sdt[1];
+    return dth[min(t + (thread_anew() & 63), end - 1) * k->sdt[0]];
+  };
+  double total = 0.0;   // the segment's decay (AGG)
+  float decay = 1.0f;   // of the chunk that times() last formed
+  bool steep = false;
+  auto times = [&](int t, IO raw, int par) __attribute__((always_inline)) {
+    const int lane = thread_anew() & 63;
+    float dl = io_traits<IO>::load(&raw) + bias;
+    const float sp = softplus(dl);
+    dl = a.softplus ? sp : dl;
+    dl = lane < Q && t + lane < end ? dl : 0.0f;
+    const double sum = lane_sums(static_cast<double>(dl * rate));
+    const double last = lane_value(sum, Q - 1);
+    decay = long_decay(static_cast<float>(last));
+    if (AGG) total += last;
+    Times<Q>& m = lds.time[par][wave];
+    const float left = dl * fast_exp2(static_cast<float>(last - sum));
+    if constexpr (AGG) {
+      if (Q == 64 || lane < Q) {
+        m.left[lane] = left;
+        m.delta[lane] = dl;
+      }
+    } else {
+      const double n0 = lane_value(sum, 15), n1 = lane_value(sum, 47), far = lane_value(sum, 31);
+      const float dn = static_cast<float>(sum - (Q == 64 && lane >= 32 ? n1 : n0)), df = static_cast<float>(sum - far);
+      // far factors that are used: rows from 32 on, columns before
+      const float grow = lane < 32 ? -df : df;
+      const float worst = Q == 64 ? fmaxf(fabsf(dn), grow) : lane < Q ? fabsf(dn) : 0.0f;
+      steep = __ballot(!(worst <= kSteep)) != 0;
+      const float hi = static_cast<float>(sum);
+      if (Q == 64 || lane < Q) {
+        m.enter[lane] = long_decay(hi);
+        m.row_near[lane] = fast_exp2(dn);
+        m.col_near[lane] = dl * fast_exp2(-dn);
+        if constexpr (Q == 64) {
+          m.row_far[lane] = fast_exp2(df);
+          m.col_far[lane] = dl * fast_exp2(-df);
+        }
+        m.left[lane] = left;
+        m.sum[0][lane] = hi;
+        m.sum[1][lane] = static_cast<float>(sum - hi);
+        m.delta[lane] = dl;
+      }
+    }
   };
 
   if (threadIdx.x < 2) lds.odd[threadIdx.x] = 0;
-  double total = 0.0;  // the segment's decay (AGG)
-  fetch(begin);
+  if (begin < end) {
+    fetch(begin);
+    times(begin, fetch_dt(begin), 0);
+  }
   __syncthreads();
   int par = 0;
   for (int t = begin; t < end; t += Q, par ^= 1) {
     // ---- this chunk into LDS
-    bool odd = false;
+    uint32_t odd = 0;
+    const int th = thread_anew();
+    const int wB = BC::offset(th / BC::kChunks, th % BC::kChunks);
+    const int wX = X::offset((th & 63) / X::kChunks, (th & 63) % X::kChunks);
 #pragma unroll
     for (int i = 0; i < kLoadBC; ++i) {
-      const int k = i * 256 + static_cast<int>(threadIdx.x);
-      const int o = BC::offset(k / BC::kChunks, k % BC::kChunks);
-      *reinterpret_cast<u32x4*>(lds.b + o) = pb[i];
-      odd |= not_finite<IO>(pb[i]);
-      if constexpr (!AGG) *reinterpret_cast<u32x4*>(lds.c + o) = pcc[i];
+      *reinterpret_cast<u32x4*>(lds.b + wB + i * kRowsBC * BC::kRow) = pb[i];
+      odd = top_exponents<IO>(pb[i], odd);
+      if constexpr (!AGG) *reinterpret_cast<u32x4*>(lds.c + wB + i * kRowsBC * BC::kRow) = pcc[i];
     }
 #pragma unroll
     for (int i = 0; i < kLoadX; ++i) {
-      const int k = i * 64 + lane;
-      *reinterpret_cast<u32x4*>(lds.x[wave] + X::offset(k / X::kChunks, k % X::kChunks)) = px[i];
-      odd |= not_finite<IO>(px[i]);
+      *reinterpret_cast<u32x4*>(lds.x[wave] + wX + i * kRowsX * X::kRow) = px[i];
+      odd = top_exponents<IO>(px[i], odd);
     }
-    if (odd) lds.odd[par] = 1;
-    // ---- time steps and the sums of their exponents
-    const bool live = lane < Q && t + lane < end;
-    float dl = pdt + bias;
-    dl = live ? (a.softplus ? softplus(dl) : dl) : 0.0f;
-    double sum = static_cast<double>(dl * rate);
-#pragma unroll
-    for (int o = 1; o < Q; o *= 2) {
-      const double up = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += up;
-    }
-    const double last = __shfl(sum, Q - 1, 64);
-    const float decay = long_decay(static_cast<float>(last));
-    if (AGG) total += last;
-    if (lane < Q) {
-      const float hi = static_cast<float>(sum);
-      lds.sum[wave][0][lane] = hi;
-      lds.sum[wave][1][lane] = static_cast<float>(sum - hi);
-      lds.delta[wave][lane] = dl;
-      lds.left[wave][lane] = dl * fast_exp2(static_cast<float>(last - sum));
-    }
+    if (not_finite<IO>(odd)) lds.odd[par] = 1;
+    const IO raw = fetch_dt(t + Q);
     __syncthreads();
-    const bool walk = lds.odd[par] != 0;
+    const bool walk = uniform(lds.odd[par]) != 0;
     if (threadIdx.x == 0) lds.odd[par ^ 1] = 0;
-    if (t + Q < end) fetch(t + Q);
+    const Times<Q>& m = lds.time[par][wave];
 
     if constexpr (!AGG) {
       // ---- C B^T, two tiles [j x i] a piece, shared out over the waves
-      if (!walk) {
+      const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, lane = th & 63;
+      const int lrow = BC::lane_row(c, g);
+      const int lj = BC::lane_row(8 * (c >> 2) + ((c & 1) | ((c & 2) << 1)) + 2 * (wave & 1), g);  // rows j
 #pragma unroll
-        for (int k = 0; k < S::kUnits * 2 / kWaves; ++k) {
-          const int tile = k * kWaves + wave;
-          const int unit = tile >> 1, half = tile & 1;
-          const int ks = unit >> 2, it = ks ? unit - 2 : unit;
-          const int j = 32 * ks + 8 * (c >> 2) + ((c & 1) | ((c & 2) << 1)) + 2 * half;
-          f32x4 acc = {0, 0, 0, 0};
+      for (int k = 0; k < S::kUnits * 2 / kWaves; ++k) {
+        const int tile = k * kWaves + wave;
+        const int unit = tile >> 1;
+        const int ks = unit >> 2, it = ks ? unit - 2 : unit;
+        f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-          for (int q = 0; q < kK; ++q)
-            acc = mma(BC::row(lds.b, j, 32 * q + 8 * g), BC::row(lds.c, 16 * it + c, 32 * q + 8 * g), acc);
-          lds.s[tile][lane] = acc;
-        }
+        for (int q = 0; q < kK; ++q)
+          acc = mma(BC::row(lds.b, lj, 32 * ks, q), BC::row(lds.c, lrow, 16 * it, q), acc);
+        lds.s[tile][lane] = acc;
       }
       __syncthreads();
     }
 
-    if (on && !walk) {
-      Frag<IO> xt[kT][2];
+    if constexpr (!AGG) {
+      if (on && !walk) {
+        const KernelArgs k = args_anew();
+        const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, lane = th & 63;
+        const int lrow = BC::lane_row(c, g), lx = X::lane_row(c, g), lxc = X::lane_col(g, c);
+        const bool gate = k->z != nullptr;
+        // S C^T: the state's bf16 fragments each serve every tile of tokens
+        f32x4 y[Q / 16][2];
 #pragma unroll
-      for (int ks = 0; ks < kT; ++ks)
-#pragma unroll
-        for (int tp = 0; tp < 2; ++tp) xt[ks][tp] = X::col(lds.x[wave], 32 * ks + 8 * g, 0, tp, c);
-      if constexpr (!AGG) {
-        Frag<IO> sb[kK][2];  // the state as an operand [p x n]
-#pragma unroll
-        for (int q = 0; q < kK; ++q)
+        for (int q = 0; q < kK; ++q) {
+          Frag<IO> sb[2];
 #pragma unroll
           for (int tp = 0; tp < 2; ++tp)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sb[q][tp].set(e, st[q][e >> 2][tp][e & 3]);
+            for (int e = 0; e < 8; e += 2) sb[tp].set2(e, st[q][e >> 2][tp][e & 3], st[q][e >> 2][tp][(e & 3) + 1]);
+#pragma unroll
+          for (int it = 0; it < Q / 16; ++it) {
+            const Frag<IO> cf = BC::row(lds.c, lrow, 16 * it, q);
+#pragma unroll
+            for (int tp = 0; tp < 2; ++tp) y[it][tp] = mma(sb[tp], cf, q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
+          }
+          step_end();
+        }
+#pragma unroll
+        for (int it = 0; it < Q / 16; ++it) {
+          const float ei = m.enter[16 * it + c];
+#pragma unroll
+          for (int tp = 0; tp < 2; ++tp) y[it][tp] *= ei;
+        }
+        // the gate, on its way while the chunk's own tokens are added
+        Raw8<IO> z[VEC ? Q / 16 : 1];
+        if constexpr (VEC) {
+          const int eZ = static_cast<int>(k->sz[0]) * kES;
+          const auto rZ = rows_of(static_cast<const IO*>(k->z) + t * k->sz[0] + h * k->sz[1] + p0,
+                                  gate ? min(end - t, Q) : 0, eZ);
+          uint32_t o = 8 * g < pc ? c * eZ + 8 * g * kES : kOffNone;
+#pragma unroll
+          for (int it = 0; it < Q / 16; ++it, o += 16 * eZ)
+#pragma unroll
+            for (int v = 0; v < kES / 2; ++v) z[it].v[v] = buf_load16(rZ, o + 16 * v);
+        }
+        step_end();
+        // the chunk's own tokens
+#pragma unroll
+        for (int ks = 0; ks < kT; ++ks) {
+          Frag<IO> xt[2];
+#pragma unroll
+          for (int tp = 0; tp < 2; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
+#pragma unroll
+          for (int it = 2 * ks; it < Q / 16; ++it) {
+            const int i = 16 * it + c;
+            const int unit = ks ? it + 2 : it;
+            const bool far = it / 2 > ks;
+            const f32x4 s0 = lds.s[2 * unit][lane], s1 = lds.s[2 * unit + 1][lane];
+            const int below = 16 * (it & 1) + c - 8 * g;  // token slots up to this one are summed
+            Frag<IO> w;
+            float row = 1.0f;
+            float v[8];
+            if (!steep) {
+              row = far ? m.row_far[i] : m.row_near[i];
+              const float* col = (far ? m.col_far : m.col_near) + 32 * ks + 8 * g;
+              const f32x4 c0 = *reinterpret_cast<const f32x4*>(col), c1 = *reinterpret_cast<const f32x4*>(col + 4);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[e] = (e < 4 ? s0[e & 3] : s1[e & 3]) * (tok(e) < 4 ? c0[tok(e) & 3] : c1[tok(e) & 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int j = 32 * ks + 8 * g + tok(e);
+                const float d = (m.sum[0][i] - m.sum[0][j]) + (m.sum[1][i] - m.sum[1][j]);
+                v[e] = (e < 4 ? s0[e & 3] : s1[e & 3]) * (fast_exp2(d) * m.delta[j]);
+              }
+            }
+            if (!far) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = tok(e) <= below ? v[e] : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) w.set2(e, v[e], v[e + 1]);
+#pragma unroll
+            for (int tp = 0; tp < 2; ++tp) {
+              const f32x4 u = mma(xt[tp], w, f32x4{0, 0, 0, 0});
+#pragma unroll
+              for (int r = 0; r < 4; ++r) y[it][tp][r] = fmaf(row, u[r], y[it][tp][r]);
+            }
+            step_end();
+          }
+        }
+        IO* oh = static_cast<IO*>(k->out) + t * k->so[0] + h * k->so[1] + p0;
+        const int eO = static_cast<int>(k->so[0]) * kES;
+        const auto rO = rows_of(oh, min(end - t, Q), eO);
+        uint32_t to = 8 * g < pc ? c * eO + 8 * g * kES : kOffNone;
 #pragma unroll
         for (int it = 0; it < Q / 16; ++it) {
           const int i = 16 * it + c;
-          const float ch = lds.sum[wave][0][i], cl = lds.sum[wave][1][i];
-          f32x4 y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll
-          for (int q = 0; q < kK; ++q) {
-            const Frag<IO> cf = BC::row(lds.c, i, 32 * q + 8 * g);
-#pragma unroll
-            for (int tp = 0; tp < 2; ++tp) y[tp] = mma(sb[q][tp], cf, y[tp]);
-          }
-          const float ei = long_decay(ch);
-#pragma unroll
-          for (int tp = 0; tp < 2; ++tp) y[tp] *= ei;
-#pragma unroll
-          for (int ks = 0; ks <= it / 2; ++ks) {
-            const int unit = ks ? it + 2 : it;
-            const f32x4 s0 = lds.s[2 * unit][lane], s1 = lds.s[2 * unit + 1][lane];
-            Frag<IO> m;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int j = 32 * ks + 8 * g + tok(e);
-              float d = ch - lds.sum[wave][0][j];
-              if constexpr (sizeof(IO) == 4) d += cl - lds.sum[wave][1][j];
-              const float v = (e < 4 ? s0[e & 3] : s1[e & 3]) * (fast_exp2(d) * lds.delta[wave][j]);
-              m.set(e, j <= i ? v : 0.0f);
-            }
-#pragma unroll
-            for (int tp = 0; tp < 2; ++tp) y[tp] = mma(xt[ks][tp], m, y[tp]);
-          }
           // ---- skip, gate, out: lane holds token i, columns 8 g .. 8 g + 7
-          const int r = t + i;
-          const int n = r < end ? pc - 8 * g : 0;
-          const Frag<IO> xi = X::row(lds.x[wave], i, 8 * g);
+          const Frag<IO> xi = X::row(lds.x[wave], lx, 16 * it, 0);
           float o[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf(skip, xi.get(e), y[e >> 2][e & 3]);
-          if (a.z != nullptr) {
-            float z[8];
-            load_part<IO, 8>(static_cast<const IO*>(a.z) + r * a.sz[0] + h * a.sz[1] + p0 + 8 * g, n, z);
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(skip, xi.get(e), y[it][e >> 2][e & 3]);
+          if constexpr (VEC) {
+            if (gate) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] *= silu(z[e]);
+              for (int e = 0; e < 8; ++e) o[e] *= silu(z[it].get(e));
+            }
+            Raw8<IO> u;
+            u.set(o);
+#pragma unroll
+            for (int k = 0; k < kES / 2; ++k)
+              __builtin_amdgcn_raw_buffer_store_b128(u.v[k], rO, to + 16 * k, 0, 0);
+            to += 16 * eO;
+          } else {
+            const int n = t + i < end ? pc - 8 * g : 0;
+            if (gate) {
+              float zz[8];
+              load_part<IO, 8>(static_cast<const IO*>(k->z) + (t + i) * k->sz[0] + h * k->sz[1] + p0 + 8 * g, n, zz);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] *= silu(zz[e]);
+            }
+            store_part<IO, 8>(oh + i * k->so[0] + 8 * g, n, o);
           }
-          store_part<IO, 8>(static_cast<IO*>(a.out) + r * a.so[0] + h * a.so[1] + p0 + 8 * g, n, o);
+          step_end();
         }
       }
-      // ---- the state
+    }
+
+    // ---- the next chunk's rows and time steps
+    fetch(t + Q);  // (past the end: zeros; under a condition the old values would stay live until here)
+    step_end();
+    const float dec = decay;
+    times(t + Q, raw, par ^ 1);
+    step_end();
+
+    // ---- the state
+    if (on && !walk) {
+      const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4;
+      const int lcol = BC::lane_col(g, c), lxc = X::lane_col(g, c);
 #pragma unroll
       for (int q = 0; q < kK; ++q)
 #pragma unroll
         for (int tn = 0; tn < 2; ++tn)
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp) st[q][tn][tp] *= decay;
+          for (int tp = 0; tp < 2; ++tp) st[q][tn][tp] *= dec;
 #pragma unroll
       for (int ks = 0; ks < kT; ++ks) {
         constexpr int kParts = sizeof(IO) == 2 ? 3 : 1;
-        Frag<IO> v[2][kParts];
+        Frag<IO> xt[2], v[2][kParts];
+#pragma unroll
+        for (int tp = 0; tp < 2; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
+        const float* left = m.left + 32 * ks + 8 * g;
+        const f32x4 l0 = *reinterpret_cast<const f32x4*>(left), l1 = *reinterpret_cast<const f32x4*>(left + 4);
 #pragma unroll
         for (int tp = 0; tp < 2; ++tp)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float r = xt[ks][tp].get(e) * lds.left[wave][32 * ks + 8 * g + tok(e)];
+          for (int e = 0; e < 8; e += 2) {
+            float r0 = xt[tp].get(e) * (tok(e) < 4 ? l0[tok(e) & 3] : l1[tok(e) & 3]);
+            float r1 = xt[tp].get(e + 1) * (tok(e + 1) < 4 ? l0[tok(e + 1) & 3] : l1[tok(e + 1) & 3]);
 #pragma unroll
             for (int k = 0; k < kParts; ++k) {
-              v[tp][k].set(e, r);
-              r -= v[tp][k].get(e);
+              v[tp][k].set2(e, r0, r1);
+              r0 -= v[tp][k].get(e);
+              r1 -= v[tp][k].get(e + 1);
             }
           }
-#pragma unroll
-        for (int q = 0; q < kK; ++q)
-#pragma unroll
-          for (int tn = 0; tn < 2; ++tn) {
-            const Frag<IO> bt = BC::col(lds.b, 32 * ks + 8 * g, 32 * q, tn, c);
-#pragma unroll
-            for (int tp = 0; tp < 2; ++tp)
-#pragma unroll
-              for (int k = kParts - 1; k >= 0; --k) st[q][tn][tp] = mma(bt, v[tp][k], st[q][tn][tp]);
-          }
-      }
-    } else if (on) {
-      // ---- token by token
-      for (int i = 0; i < Q && t + i < end; ++i) {
-        const float dti = lds.delta[wave][i], e = fast_exp2(dti * rate);
-        float y[2], x[2];
-#pragma unroll
-        for (int tp = 0; tp < 2; ++tp) {
-          const int p = pcol + 4 * tp;
-          x[tp] = io_traits<IO>::load(reinterpret_cast<const IO*>(lds.x[wave] + X::offset(i, p / kE)) + p % kE);
-          y[tp] = 0.0f;
-        }
 #pragma unroll
         for (int q = 0; q < kK; ++q) {
-          const Frag<IO> b = BC::row(lds.b, i, 32 * q + 8 * g);
-          const Frag<IO> cf = BC::row(lds.c, i, 32 * q + 8 * g);
+          Frag<IO> bt[2];
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp)
+          for (int tn = 0; tn < 2; ++tn) bt[tn] = BC::col(lds.b, lcol, ks, q, tn);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (32 * q + 8 * g + k < a.dstate) {  // the others stay 0, whatever x is
-                const float s = fmaf(e, st[q][k >> 2][tp][k & 3], dti * x[tp] * b.get(k));
-                st[q][k >> 2][tp][k & 3] = s;
-                if (!AGG) y[tp] = fmaf(cf.get(k), s, y[tp]);
-              }
-            }
+          for (int k = kParts - 1; k >= 0; --k)
+#pragma unroll
+            for (int tn = 0; tn < 2; ++tn)
+#pragma unroll
+              for (int tp = 0; tp < 2; ++tp) st[q][tn][tp] = mma(bt[tn], v[tp][k], st[q][tn][tp]);
         }
-        if constexpr (!AGG) {
-          const int64_t r = t + i;
+        step_end();
+      }
+    } else if (on) {
+      // ---- token by token, the state in memory: nothing of this may take
+      // registers from the products
+      state_out();
+      const KernelArgs k = args_anew();
+      const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4;
+#pragma unroll 1
+      for (int i = 0; i < Q && t + i < end; ++i) {
+        const float dti = m.delta[i], e = fast_exp2(dti * rate);
+#pragma unroll 1
+        for (int p = 8 * (c >> 2) + (c & 3), tp = 0; tp < 2; ++tp, p += 4) {
+          const float x = io_traits<IO>::load(reinterpret_cast<const IO*>(lds.x[wave] + X::offset(i, p / kE)) + p % kE);
+          float y = 0.0f;
+#pragma unroll 1
+          for (int n = 8 * g; n < NP; n += 32) {
+            const int valid = p < pc ? k->dstate - n : 0;
+            float* at = home + static_cast<int64_t>(p) * k->dstate + n;
+            float s[8], b[8], cc[8];
+            load_part<float, 8>(at, valid, s);
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp) {
-            const int p = pcol + 4 * tp;
-            y[tp] += __shfl_xor(y[tp], 16, 64);
-            y[tp] += __shfl_xor(y[tp], 32, 64);
+            for (int r = 0; r < 8; ++r) {
+              const int o = BC::offset(i, (n + r) / kE);
+              b[r] = io_traits<IO>::load(reinterpret_cast<const IO*>(lds.b + o) + (n + r) % kE);
+              cc[r] = AGG ? 0.0f : io_traits<IO>::load(reinterpret_cast<const IO*>(lds.c + o) + (n + r) % kE);
+              s[r] = fmaf(e, s[r], dti * x * b[r]);
+              if (!AGG && r < valid) y = fmaf(cc[r], s[r], y);
+            }
+            store_part<float, 8>(at, valid, s);
+          }
+          if constexpr (!AGG) {
+            y += __shfl_xor(y, 16, 64);
+            y += __shfl_xor(y, 32, 64);
+            const int r = t + i;
             if (g == 0 && p < pc) {
-              float o = fmaf(skip, x[tp], y[tp]);
-              if (a.z != nullptr)
-                o *= silu(io_traits<IO>::load(static_cast<const IO*>(a.z) + r * a.sz[0] + h * a.sz[1] + p0 + p));
-              io_traits<IO>::store(static_cast<IO*>(a.out) + r * a.so[0] + h * a.so[1] + p0 + p, o);
+              float o = fmaf(skip, x, y);
+              if (k->z != nullptr)
+                o *= silu(io_traits<IO>::load(static_cast<const IO*>(k->z) + r * k->sz[0] + h * k->sz[1] + p0 + p));
+              io_traits<IO>::store(static_cast<IO*>(k->out) + r * k->so[0] + h * k->so[1] + p0 + p, o);
             }
           }
         }
       }
+      state_in(true);
     }
     __syncthreads();
   }
 
   // ---- the state that the segment leaves
   if (!on || (!AGG && cut)) return;
-  float* leave = AGG ? part : cache;
-#pragma unroll
-  for (int q = 0; q < kK; ++q)
-#pragma unroll
-    for (int tp = 0; tp < 2; ++tp) {
-      const int p = pcol + 4 * tp, n = 32 * q + 8 * g;
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = st[q][e >> 2][tp][e & 3];
-      store_part<float, 8>(leave + static_cast<int64_t>(p) * a.dstate + n, p < pc ? a.dstate - n : 0, v);
-    }
-  if (AGG && lane == 0 && p0 == 0) a.decays[static_cast<int64_t>(w.index) * a.heads + h] = long_decay(static_cast<float>(total));
+  state_out();
+  if (AGG && (threadIdx.x & 63) == 0 && p0 == 0) a.decays[static_cast<int64_t>(w.index) * a.heads + h] = long_decay(static_cast<float>(total));
 }
 
 // The states entering the segments of a cut prompt, in place of what the
@@ -597,18 +865,23 @@ __global__ __launch_bounds__(256) void head_scan_carry_kernel(HeadScanArgs a, in
   store_part<float, 4>(cache, n, s);
 }
 
-template <typename IO, int NP, int Q>
-hipError_t launch_n(const HeadScanArgs& a, hipStream_t stream) {
+template <typename IO, int NP, int Q, bool VEC>
+hipError_t launch_v(const HeadScanArgs& a, hipStream_t stream) {
   const int64_t tiles = static_cast<int64_t>(a.groups) * ((a.heads / a.groups * a.ptiles + kWaves - 1) / kWaves);
   if (a.cut_slots > 0) {
-    head_scan_kernel<IO, NP, Q, true><<<dim3(static_cast<unsigned>(a.cut_slots * tiles)), 256, 0, stream>>>(a);
+    head_scan_kernel<IO, NP, Q, true, VEC><<<dim3(static_cast<unsigned>(a.cut_slots * tiles)), 256, 0, stream>>>(a);
     const int64_t blocks = (static_cast<int64_t>(a.heads) * a.headdim * a.dstate + 1023) / 1024;
     head_scan_carry_kernel<<<dim3(static_cast<unsigned>(blocks * a.cut_prompts)), 256, 0, stream>>>(
         a, static_cast<int>(blocks));
   }
-  head_scan_kernel<IO, NP, Q, false>
+  head_scan_kernel<IO, NP, Q, false, VEC>
       <<<dim3(static_cast<unsigned>((a.cut_slots + a.q.seqs) * tiles)), 256, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <typename IO, int NP, int Q>
+hipError_t launch_n(const HeadScanArgs& a, hipStream_t stream) {
+  return a.vec ? launch_v<IO, NP, Q, true>(a, stream) : launch_v<IO, NP, Q, false>(a, stream);
 }
 
 // Chunks of 64 tokens in bf16 and 32 in fp32, whose tiles are twice as wide.

@@ -48,6 +48,7 @@ struct HeadScanArgs {
   const float* dt_bias;
   float* state;
   void* out;
+  int vec;          // rows of x, B, C, z and out are whole aligned 16-byte vectors
   int ptiles;       // 32-column tiles of a head
   int seg_len;      // longer prompts are cut into segments of at most this many tokens (0: none is)
   int cut_slots;    // room for the segments of all cut prompts
