@@ -45,6 +45,7 @@ constexpr int kWaves = 4;
 constexpr int kCols = 32;  // columns p of a wave's tile
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -62,12 +63,22 @@ struct Frag<bf16_t> {
   };
   __device__ inline float get(int e) const { return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16); }
   __device__ inline void set2(int e, float x, float y) { w[e / 2] = bf16x2_bits(x, y); }
+  // what x is more than slot e (exact: one instruction, with no unpacking).  The
+  // pair (-1, 0) comes from a register: as a constant the compiler encodes it as
+  // (0, -1)'s inline form and the wrong half is taken.
+  __device__ inline float more(int e, float x) const {
+    uint32_t minus = e & 1 ? 0xbf800000u : 0x0000bf80u;
+    asm("" : "+s"(minus));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[e / 2]), __builtin_bit_cast(bf16x2, minus), x,
+                                           false);
+  }
 };
 template <>
 struct Frag<float> {
   float v[8];
   __device__ inline float get(int e) const { return v[e]; }
   __device__ inline void set2(int e, float x, float y) { v[e] = x, v[e + 1] = y; }
+  __device__ inline float more(int e, float x) const { return x - v[e]; }
 };
 
 __device__ inline f32x4 mma(const Frag<bf16_t>& a, const Frag<bf16_t>& b, f32x4 acc) {
@@ -317,12 +328,6 @@ __device__ inline int thread_anew() {
   asm volatile("" : "+v"(v));
   return v;
 }
-typedef const __attribute__((address_space(4))) HeadScanArgs* KernelArgs;
-__device__ inline KernelArgs args_anew() {
-  auto p = (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(p));
-  return p;
-}
 // Keeps the reads of one step from moving up into the step before, where their
 // registers are still in use.
 __device__ inline void step_end() { __builtin_amdgcn_sched_barrier(0); }
@@ -339,12 +344,17 @@ struct Times {
   float delta[Q];
 };
 
+template <int Q>
+struct SumTimes {
+  float left[Q], delta[Q];
+};
+
 template <typename IO, int NP, int Q>
 struct Shape {
   static constexpr int kUnits = Q == 64 ? 6 : 2;  // 32 x 16 pieces of the lower triangle
   using BC = Tile<IO, NP>;
   using X = Tile<IO, kCols>;
-  struct Lds {
+  struct Walk {
     char b[Q * NP * sizeof(IO)];
     char c[Q * NP * sizeof(IO)];
     char x[kWaves][Q * kCols * sizeof(IO)];
@@ -352,12 +362,19 @@ struct Shape {
     Times<Q> time[2][kWaves];
     int odd[2];  // a chunk holds something not finite
   };
+  struct Sum {
+    char b[Q * NP * sizeof(IO)];
+    alignas(16) char c[16];  // (no C)
+    char x[kWaves][Q * kCols * sizeof(IO)];
+    SumTimes<Q> time[2][kWaves];
+    int odd[2];
+  };
 };
 
 // AGG: only what a segment adds to a zero state, and its decay.  VEC: rows are
 // whole 16-byte vectors (else element by element at their ends).
 template <typename IO, int NP, int Q, bool AGG, bool VEC>
-__global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
+__global__ __launch_bounds__(256, AGG ? 3 : 2) void head_scan_kernel(HeadScanArgs a) {
   using S = Shape<IO, NP, Q>;
   using BC = typename S::BC;
   using X = typename S::X;
@@ -368,7 +385,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   constexpr int kLoadBC = Q * BC::kChunks / 256;       // 16-byte loads a thread
   constexpr int kLoadX = Q * X::kChunks / 64;          // 16-byte loads a lane
   constexpr int kRowsBC = 256 / BC::kChunks, kRowsX = 64 / X::kChunks;  // rows between them
-  __shared__ __attribute__((aligned(16))) typename S::Lds lds;
+  using Lds = std::conditional_t<AGG, typename S::Sum, typename S::Walk>;
+  __shared__ __attribute__((aligned(16))) Lds lds;
 
   const int wave = uniform(threadIdx.x >> 6);
 
@@ -397,6 +415,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   const bool cut = w.nseg > 1;
   const bool from_cache = resumes(a.q, w.seq);
   if (len == 0 && from_cache) return;
+  if (AGG && w.seg == w.nseg - 1) return;  // nothing enters after it
 
   const bool on = job < jobs;
   const int h = grp * (a.heads / a.groups) + (on ? job / a.ptiles : 0);
@@ -447,32 +466,36 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   const float bias = a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f;
   const float skip = a.D != nullptr ? a.D[h] : 0.0f;
 
+  // rows of the chunk to be fetched next, and of the one being walked
+  const IO* xf = static_cast<const IO*>(a.x) + begin * a.sx[0] + h * a.sx[1] + p0;
+  const IO* Bf = static_cast<const IO*>(a.B) + begin * a.sB[0] + grp * a.sB[1];
+  const IO* Cf = static_cast<const IO*>(a.C) + begin * a.sC[0] + grp * a.sC[1];
+  const IO* zw = static_cast<const IO*>(a.z) + begin * a.sz[0] + h * a.sz[1] + p0;
+  IO* ow = static_cast<IO*>(a.out) + begin * a.so[0] + h * a.so[1] + p0;
+  const bool gate = a.z != nullptr;
+
   u32x4 pb[kLoadBC], pcc[AGG ? 1 : kLoadBC], px[kLoadX];
   auto fetch = [&](int t) __attribute__((always_inline)) {
-    const KernelArgs k = args_anew();
     const int th = thread_anew();
     // this thread's chunks of B and C, and this lane's of x: row and column of the first
     const int rb = th / BC::kChunks, nb = th % BC::kChunks * kE;
     const int rx = (th & 63) / X::kChunks, nx = (th & 63) % X::kChunks * kE;
-    const IO* xh = static_cast<const IO*>(k->x) + t * k->sx[0] + h * k->sx[1] + p0;
-    const IO* Bg = static_cast<const IO*>(k->B) + t * k->sB[0] + grp * k->sB[1];
-    const IO* Cg = static_cast<const IO*>(k->C) + t * k->sC[0] + grp * k->sC[1];
     if constexpr (VEC) {
       // byte offsets from the chunk's first row (a tile spans less than 2 GiB)
-      const int eB = static_cast<int>(k->sB[0]) * kES, eC = static_cast<int>(k->sC[0]) * kES;
-      const int eX = static_cast<int>(k->sx[0]) * kES;
+      const int eX = static_cast<int>(a.sx[0]) * kES, eB = static_cast<int>(a.sB[0]) * kES;
+      const int eC = static_cast<int>(a.sC[0]) * kES;
       const int rows = max(min(end - t, Q), 0);
       uint32_t o = nx < pc ? rx * eX + nx * kES : kOffNone;
-      const auto rX = rows_of(xh, rows, eX);
+      const auto rX = rows_of(xf, rows, eX);
 #pragma unroll
       for (int i = 0; i < kLoadX; ++i, o += kRowsX * eX) px[i] = buf_load16(rX, o);
-      o = nb < k->dstate ? rb * eB + nb * kES : kOffNone;
-      const auto rB = rows_of(Bg, rows, eB);
+      o = nb < a.dstate ? rb * eB + nb * kES : kOffNone;
+      const auto rB = rows_of(Bf, rows, eB);
 #pragma unroll
       for (int i = 0; i < kLoadBC; ++i, o += kRowsBC * eB) pb[i] = buf_load16(rB, o);
       if constexpr (!AGG) {
-        o = nb < k->dstate ? rb * eC + nb * kES : kOffNone;
-        const auto rC = rows_of(Cg, rows, eC);
+        o = nb < a.dstate ? rb * eC + nb * kES : kOffNone;
+        const auto rC = rows_of(Cf, rows, eC);
 #pragma unroll
         for (int i = 0; i < kLoadBC; ++i, o += kRowsBC * eC) pcc[i] = buf_load16(rC, o);
       }
@@ -480,22 +503,24 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
       for (int i = 0; i < kLoadBC; ++i) {
         const int r = rb + i * kRowsBC;
-        const int valid = t + r < end ? k->dstate - nb : 0;
-        pb[i] = load16<IO>(Bg + r * k->sB[0] + nb, valid);
-        if constexpr (!AGG) pcc[i] = load16<IO>(Cg + r * k->sC[0] + nb, valid);
+        const int valid = t + r < end ? a.dstate - nb : 0;
+        pb[i] = load16<IO>(Bf + r * a.sB[0] + nb, valid);
+        if constexpr (!AGG) pcc[i] = load16<IO>(Cf + r * a.sC[0] + nb, valid);
       }
 #pragma unroll
       for (int i = 0; i < kLoadX; ++i) {
         const int r = rx + i * kRowsX;
-        px[i] = load16<IO>(xh + r * k->sx[0] + nx, t + r < end ? pc - nx : 0);
+        px[i] = load16<IO>(xf + r * a.sx[0] + nx, t + r < end ? pc - nx : 0);
       }
     }
+    xf += Q * a.sx[0];
+    Bf += Q * a.sB[0];
+    Cf += Q * a.sC[0];
   };
   // one token a lane (past the segment's end: its last one, which is not used)
   auto fetch_dt = [&](int t) __attribute__((always_inline)) {
-    const KernelArgs k = args_anew();
-    const IO* dth = static_cast<const IO*>(k->dt) + h * k->sdt[1];
-    return dth[min(t + (thread_anew() & 63), end - 1) * k->sdt[0]];
+    const IO* dth = static_cast<const IO*>(a.dt) + h * a.sdt[1];
+    return dth[min(t + (thread_anew() & 63), end - 1) * a.sdt[0]];
   };
   double total = 0.0;   // the segment's decay (AGG)
   float decay = 1.0f;   // of the chunk that times() last formed
@@ -510,7 +535,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     const double last = lane_value(sum, Q - 1);
     decay = long_decay(static_cast<float>(last));
     if (AGG) total += last;
-    Times<Q>& m = lds.time[par][wave];
+    auto& m = lds.time[par][wave];
     const float left = dl * fast_exp2(static_cast<float>(last - sum));
     if constexpr (AGG) {
       if (Q == 64 || lane < Q) {
@@ -547,8 +572,10 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     times(begin, fetch_dt(begin), 0);
   }
   __syncthreads();
-  int par = 0;
-  for (int t = begin; t < end; t += Q, par ^= 1) {
+  int par = 0, t = begin;
+  for (;;) {
+  bool walk = false;
+  for (; t < end; t += Q, par ^= 1) {
     // ---- this chunk into LDS
     uint32_t odd = 0;
     const int th = thread_anew();
@@ -568,15 +595,17 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     if (not_finite<IO>(odd)) lds.odd[par] = 1;
     const IO raw = fetch_dt(t + Q);
     __syncthreads();
-    const bool walk = uniform(lds.odd[par]) != 0;
+    walk = uniform(lds.odd[par]) != 0;
     if (threadIdx.x == 0) lds.odd[par ^ 1] = 0;
-    const Times<Q>& m = lds.time[par][wave];
+    if (walk) break;
+    const auto& m = lds.time[par][wave];
 
+    f32x4 y[AGG ? 1 : Q / 16][2];
     if constexpr (!AGG) {
-      // ---- C B^T, two tiles [j x i] a piece, shared out over the waves
       const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, lane = th & 63;
       const int lrow = BC::lane_row(c, g);
       const int lj = BC::lane_row(8 * (c >> 2) + ((c & 1) | ((c & 2) << 1)) + 2 * (wave & 1), g);  // rows j
+      // ---- C B^T, two tiles [j x i] a piece, shared out over the waves
 #pragma unroll
       for (int k = 0; k < S::kUnits * 2 / kWaves; ++k) {
         const int tile = k * kWaves + wave;
@@ -588,49 +617,46 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
           acc = mma(BC::row(lds.b, lj, 32 * ks, q), BC::row(lds.c, lrow, 16 * it, q), acc);
         lds.s[tile][lane] = acc;
       }
+      step_end();
+      // ---- S C^T: the state's fragments each serve every tile of tokens
+#pragma unroll
+      for (int q = 0; q < kK; ++q) {
+        Frag<IO> sb[2];
+#pragma unroll
+        for (int tp = 0; tp < 2; ++tp)
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) sb[tp].set2(e, st[q][e >> 2][tp][e & 3], st[q][e >> 2][tp][(e & 3) + 1]);
+#pragma unroll
+        for (int it = 0; it < Q / 16; ++it) {
+          const Frag<IO> cf = BC::row(lds.c, lrow, 16 * it, q);
+#pragma unroll
+          for (int tp = 0; tp < 2; ++tp) y[it][tp] = mma(sb[tp], cf, q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
+        }
+      }
+      step_end();
       __syncthreads();
     }
 
     if constexpr (!AGG) {
-      if (on && !walk) {
-        const KernelArgs k = args_anew();
+      {
         const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, lane = th & 63;
-        const int lrow = BC::lane_row(c, g), lx = X::lane_row(c, g), lxc = X::lane_col(g, c);
-        const bool gate = k->z != nullptr;
-        // S C^T: the state's bf16 fragments each serve every tile of tokens
-        f32x4 y[Q / 16][2];
+        const int lx = X::lane_row(c, g), lxc = X::lane_col(g, c);
+        // the gate, on its way while the chunk's own tokens are added
+        Raw8<IO> z[VEC ? Q / 16 : 1];
+        if constexpr (VEC) {
+          const int eZ = static_cast<int>(a.sz[0]) * kES;
+          const auto rZ = rows_of(zw, gate ? min(end - t, Q) : 0, eZ);
+          uint32_t o = 8 * g < pc ? c * eZ + 8 * g * kES : kOffNone;
 #pragma unroll
-        for (int q = 0; q < kK; ++q) {
-          Frag<IO> sb[2];
+          for (int it = 0; it < Q / 16; ++it, o += 16 * eZ)
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp)
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) sb[tp].set2(e, st[q][e >> 2][tp][e & 3], st[q][e >> 2][tp][(e & 3) + 1]);
-#pragma unroll
-          for (int it = 0; it < Q / 16; ++it) {
-            const Frag<IO> cf = BC::row(lds.c, lrow, 16 * it, q);
-#pragma unroll
-            for (int tp = 0; tp < 2; ++tp) y[it][tp] = mma(sb[tp], cf, q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
-          }
-          step_end();
+            for (int v = 0; v < kES / 2; ++v) z[it].v[v] = buf_load16(rZ, o + 16 * v);
         }
 #pragma unroll
         for (int it = 0; it < Q / 16; ++it) {
           const float ei = m.enter[16 * it + c];
 #pragma unroll
           for (int tp = 0; tp < 2; ++tp) y[it][tp] *= ei;
-        }
-        // the gate, on its way while the chunk's own tokens are added
-        Raw8<IO> z[VEC ? Q / 16 : 1];
-        if constexpr (VEC) {
-          const int eZ = static_cast<int>(k->sz[0]) * kES;
-          const auto rZ = rows_of(static_cast<const IO*>(k->z) + t * k->sz[0] + h * k->sz[1] + p0,
-                                  gate ? min(end - t, Q) : 0, eZ);
-          uint32_t o = 8 * g < pc ? c * eZ + 8 * g * kES : kOffNone;
-#pragma unroll
-          for (int it = 0; it < Q / 16; ++it, o += 16 * eZ)
-#pragma unroll
-            for (int v = 0; v < kES / 2; ++v) z[it].v[v] = buf_load16(rZ, o + 16 * v);
         }
         step_end();
         // the chunk's own tokens
@@ -639,18 +665,20 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
           Frag<IO> xt[2];
 #pragma unroll
           for (int tp = 0; tp < 2; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
+          constexpr int kIt = Q / 16;
+          Frag<IO> w[kIt];
+          float row[kIt];
 #pragma unroll
-          for (int it = 2 * ks; it < Q / 16; ++it) {
+          for (int it = 2 * ks; it < kIt; ++it) {
             const int i = 16 * it + c;
             const int unit = ks ? it + 2 : it;
             const bool far = it / 2 > ks;
             const f32x4 s0 = lds.s[2 * unit][lane], s1 = lds.s[2 * unit + 1][lane];
             const int below = 16 * (it & 1) + c - 8 * g;  // token slots up to this one are summed
-            Frag<IO> w;
-            float row = 1.0f;
             float v[8];
+            row[it] = 1.0f;
             if (!steep) {
-              row = far ? m.row_far[i] : m.row_near[i];
+              row[it] = far ? m.row_far[i] : m.row_near[i];
               const float* col = (far ? m.col_far : m.col_near) + 32 * ks + 8 * g;
               const f32x4 c0 = *reinterpret_cast<const f32x4*>(col), c1 = *reinterpret_cast<const f32x4*>(col + 4);
 #pragma unroll
@@ -669,19 +697,23 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
               for (int e = 0; e < 8; ++e) v[e] = tok(e) <= below ? v[e] : 0.0f;
             }
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) w.set2(e, v[e], v[e + 1]);
-#pragma unroll
-            for (int tp = 0; tp < 2; ++tp) {
-              const f32x4 u = mma(xt[tp], w, f32x4{0, 0, 0, 0});
-#pragma unroll
-              for (int r = 0; r < 4; ++r) y[it][tp][r] = fmaf(row, u[r], y[it][tp][r]);
-            }
-            step_end();
+            for (int e = 0; e < 8; e += 2) w[it].set2(e, v[e], v[e + 1]);
           }
+          f32x4 u[kIt][2];
+#pragma unroll
+          for (int it = 2 * ks; it < kIt; ++it)
+#pragma unroll
+            for (int tp = 0; tp < 2; ++tp) u[it][tp] = mma(xt[tp], w[it], f32x4{0, 0, 0, 0});
+#pragma unroll
+          for (int it = 2 * ks; it < kIt; ++it)
+#pragma unroll
+            for (int tp = 0; tp < 2; ++tp)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) y[it][tp][r] = fmaf(row[it], u[it][tp][r], y[it][tp][r]);
+          step_end();
         }
-        IO* oh = static_cast<IO*>(k->out) + t * k->so[0] + h * k->so[1] + p0;
-        const int eO = static_cast<int>(k->so[0]) * kES;
-        const auto rO = rows_of(oh, min(end - t, Q), eO);
+        const int eO = static_cast<int>(a.so[0]) * kES;
+        const auto rO = rows_of(ow, min(end - t, Q), eO);
         uint32_t to = 8 * g < pc ? c * eO + 8 * g * kES : kOffNone;
 #pragma unroll
         for (int it = 0; it < Q / 16; ++it) {
@@ -706,11 +738,11 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
             const int n = t + i < end ? pc - 8 * g : 0;
             if (gate) {
               float zz[8];
-              load_part<IO, 8>(static_cast<const IO*>(k->z) + (t + i) * k->sz[0] + h * k->sz[1] + p0 + 8 * g, n, zz);
+              load_part<IO, 8>(zw + i * a.sz[0] + 8 * g, n, zz);
 #pragma unroll
               for (int e = 0; e < 8; ++e) o[e] *= silu(zz[e]);
             }
-            store_part<IO, 8>(oh + i * k->so[0] + 8 * g, n, o);
+            store_part<IO, 8>(ow + i * a.so[0] + 8 * g, n, o);
           }
           step_end();
         }
@@ -725,7 +757,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     step_end();
 
     // ---- the state
-    if (on && !walk) {
+    {
       const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4;
       const int lcol = BC::lane_col(g, c), lxc = X::lane_col(g, c);
 #pragma unroll
@@ -751,8 +783,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
             for (int k = 0; k < kParts; ++k) {
               v[tp][k].set2(e, r0, r1);
-              r0 -= v[tp][k].get(e);
-              r1 -= v[tp][k].get(e + 1);
+              r0 = v[tp][k].more(e, r0);
+              r1 = v[tp][k].more(e + 1, r1);
             }
           }
 #pragma unroll
@@ -769,12 +801,18 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
         }
         step_end();
       }
-    } else if (on) {
+    }
+    zw += Q * a.sz[0];
+    ow += Q * a.so[0];
+    __syncthreads();
+  }
+  if (!walk) break;
+    const auto& m = lds.time[par][wave];
+    if (on) {
       // ---- token by token, the state in memory: nothing of this may take
       // registers from the products
       state_out();
-      const KernelArgs k = args_anew();
-      const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4;
+      const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, N = anew(a.dstate);
 #pragma unroll 1
       for (int i = 0; i < Q && t + i < end; ++i) {
         const float dti = m.delta[i], e = fast_exp2(dti * rate);
@@ -784,8 +822,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
           float y = 0.0f;
 #pragma unroll 1
           for (int n = 8 * g; n < NP; n += 32) {
-            const int valid = p < pc ? k->dstate - n : 0;
-            float* at = home + static_cast<int64_t>(p) * k->dstate + n;
+            const int valid = p < pc ? N - n : 0;
+            float* at = home + static_cast<int64_t>(p) * N + n;
             float s[8], b[8], cc[8];
             load_part<float, 8>(at, valid, s);
 #pragma unroll
@@ -801,30 +839,35 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
           if constexpr (!AGG) {
             y += __shfl_xor(y, 16, 64);
             y += __shfl_xor(y, 32, 64);
-            const int r = t + i;
             if (g == 0 && p < pc) {
               float o = fmaf(skip, x, y);
-              if (k->z != nullptr)
-                o *= silu(io_traits<IO>::load(static_cast<const IO*>(k->z) + r * k->sz[0] + h * k->sz[1] + p0 + p));
-              io_traits<IO>::store(static_cast<IO*>(k->out) + r * k->so[0] + h * k->so[1] + p0 + p, o);
+              if (gate) o *= silu(io_traits<IO>::load(zw + i * a.sz[0] + p));
+              io_traits<IO>::store(ow + i * a.so[0] + p, o);
             }
           }
         }
       }
       state_in(true);
     }
+    fetch(t + Q);
+    times(t + Q, fetch_dt(t + Q), par ^ 1);
+    zw += Q * a.sz[0];
+    ow += Q * a.so[0];
+    t += Q;
+    par ^= 1;
     __syncthreads();
   }
 
   // ---- the state that the segment leaves
-  if (!on || (!AGG && cut)) return;
+  if (!on || (!AGG && w.seg < w.nseg - 1)) return;
+  if (!AGG) home = cache;
   state_out();
   if (AGG && (threadIdx.x & 63) == 0 && p0 == 0) a.decays[static_cast<int64_t>(w.index) * a.heads + h] = long_decay(static_cast<float>(total));
 }
 
 // The states entering the segments of a cut prompt, in place of what the
-// segments add, and the state the prompt leaves: four states a thread, kAhead
-// segments loaded before the first is used.
+// segments add (the last one's place holds nothing yet): four states a thread,
+// kAhead segments loaded before the first is used.
 __global__ __launch_bounds__(256) void head_scan_carry_kernel(HeadScanArgs a, int blocks) {
   constexpr int kAhead = 8;
   const Where w = find_cut(a, blockIdx.x / blocks, true);
@@ -839,7 +882,7 @@ __global__ __launch_bounds__(256) void head_scan_carry_kernel(HeadScanArgs a, in
   int h[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) h[k] = static_cast<int>(min(i + k, all - 1) / (static_cast<int64_t>(a.headdim) * a.dstate));
-  float* cache = a.state + slot * a.sstate + i;
+  const float* cache = a.state + slot * a.sstate + i;
   float* part = a.parts + w.index * all + i;
   const float* decay = a.decays + static_cast<int64_t>(w.index) * a.heads;
   float s[4] = {};
@@ -862,7 +905,6 @@ __global__ __launch_bounds__(256) void head_scan_carry_kernel(HeadScanArgs a, in
       }
     }
   }
-  store_part<float, 4>(cache, n, s);
 }
 
 template <typename IO, int NP, int Q, bool VEC>
