@@ -374,7 +374,7 @@ struct Shape {
 // AGG: only what a segment adds to a zero state, and its decay.  VEC: rows are
 // whole 16-byte vectors (else element by element at their ends).
 template <typename IO, int NP, int Q, bool AGG, bool VEC>
-__global__ __launch_bounds__(256, AGG ? 3 : 2) void head_scan_kernel(HeadScanArgs a) {
+__global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   using S = Shape<IO, NP, Q>;
   using BC = typename S::BC;
   using X = typename S::X;
@@ -604,34 +604,50 @@ __global__ __launch_bounds__(256, AGG ? 3 : 2) void head_scan_kernel(HeadScanArg
     if constexpr (!AGG) {
       const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, lane = th & 63;
       const int lrow = BC::lane_row(c, g);
-      const int lj = BC::lane_row(8 * (c >> 2) + ((c & 1) | ((c & 2) << 1)) + 2 * (wave & 1), g);  // rows j
-      // ---- C B^T, two tiles [j x i] a piece, shared out over the waves
-#pragma unroll
-      for (int k = 0; k < S::kUnits * 2 / kWaves; ++k) {
-        const int tile = k * kWaves + wave;
-        const int unit = tile >> 1;
-        const int ks = unit >> 2, it = ks ? unit - 2 : unit;
-        f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-        for (int q = 0; q < kK; ++q)
-          acc = mma(BC::row(lds.b, lj, 32 * ks, q), BC::row(lds.c, lrow, 16 * it, q), acc);
-        lds.s[tile][lane] = acc;
-      }
-      step_end();
+      // ---- C B^T, three tiles [j x i] a wave (Q = 64): tokens j of its half of
+      // one 32 with the tiles i that reach it, so that a fragment of B serves two
+      // or three tiles, and one of C these and the state's
+      constexpr int kPer = S::kUnits * 2 / kWaves;
+      const int half = wave & 1;
+      const bool upper = Q == 64 && wave >= 2;  // j in 32 .. 63, and one tile of the lower 32
+      const int jr = 8 * (c >> 2) + ((c & 1) | ((c & 2) << 1)) + 2 * half;
+      const int lj = BC::lane_row(jr, g), lju = upper ? lj + 32 * BC::kRow : lj;
+      f32x4 acc[kPer];
       // ---- S C^T: the state's fragments each serve every tile of tokens
 #pragma unroll
       for (int q = 0; q < kK; ++q) {
-        Frag<IO> sb[2];
+        Frag<IO> sb[2], cf[Q / 16];
+#pragma unroll
+        for (int it = 0; it < Q / 16; ++it) cf[it] = BC::row(lds.c, lrow, 16 * it, q);
+        const Frag<IO> b = BC::row(lds.b, lju, 0, q);
+        if constexpr (Q == 64) {
+          const f32x4 z = {0, 0, 0, 0};
+          if (upper) {
+            const Frag<IO> b0 = BC::row(lds.b, lj, 0, q);
+            acc[0] = mma(b, cf[2], q == 0 ? z : acc[0]);
+            acc[1] = mma(b, cf[3], q == 0 ? z : acc[1]);
+            acc[2] = mma(b0, cf[3], q == 0 ? z : acc[2]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) acc[k] = mma(b, cf[k], q == 0 ? z : acc[k]);
+          }
+        } else {
+          acc[0] = mma(b, wave >= 2 ? cf[1] : cf[0], q == 0 ? f32x4{0, 0, 0, 0} : acc[0]);
+        }
 #pragma unroll
         for (int tp = 0; tp < 2; ++tp)
 #pragma unroll
           for (int e = 0; e < 8; e += 2) sb[tp].set2(e, st[q][e >> 2][tp][e & 3], st[q][e >> 2][tp][(e & 3) + 1]);
 #pragma unroll
-        for (int it = 0; it < Q / 16; ++it) {
-          const Frag<IO> cf = BC::row(lds.c, lrow, 16 * it, q);
+        for (int it = 0; it < Q / 16; ++it)
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp) y[it][tp] = mma(sb[tp], cf, q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
-        }
+          for (int tp = 0; tp < 2; ++tp) y[it][tp] = mma(sb[tp], cf[it], q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
+      }
+      // piece (ks, it) is number it (ks = 0) or it + 2
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int unit = Q == 64 ? (upper ? (k < 2 ? 4 + k : 3) : k) : wave >> 1;
+        lds.s[2 * unit + half][lane] = acc[k];
       }
       step_end();
       __syncthreads();
