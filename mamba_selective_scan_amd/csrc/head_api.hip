@@ -75,20 +75,35 @@ mss_status check_scan_shape(const mss_head_scan_args* a) {
 // How a head-wise scan is cut over time: prompts longer than seg_len run as
 // segments, so that a few long prompts still fill the card.  From the sizes
 // alone: the prompts' lengths stay on the device.
+//
+// One long prompt wants as many segments as workgroups can run at once and not
+// one more (24 heads of 64 x 128, 32768 tokens in bf16: 191 us at 480 workgroups
+// of 512, 234 us at 516).  Segments shorter than four chunks spend more on the
+// states between them than they gain (one prompt of 4096: 61 us at 256 tokens,
+// 80 us at 64); a call of up to eight chunks is not cut at all (200 tokens:
+// 29 us whole, 35 us in segments of 64).  Longer than kSegMax, a batch of equal
+// prompts does not care (8 x 4096 tokens of 80 heads: 528 us whole, 535 us at
+// 1024) while one of unequal prompts would wait for its longest (24 prompts,
+// 32768 tokens: 571 us at 1024, 622 us at 2560).
 struct HeadScanPlan {
   int64_t ptiles, tiles, seg_len = 0, cut_slots = 0, cut_prompts = 0;
   size_t parts = 0, workspace = 0;
 };
-constexpr int64_t kHeadSegTiles = 512;  // workgroups wanted: two a CU
-constexpr int64_t kHeadSegMin = 256;    // tokens of a segment at least
+constexpr int64_t kCus = 256;
+constexpr int64_t kSegMax = 1024;
 
 HeadScanPlan head_scan_plan(const mss_head_scan_args* a) {
   HeadScanPlan p;
   p.ptiles = (a->headdim + 31) / 32;
   p.tiles = a->groups * ((a->heads / a->groups * p.ptiles + 3) / 4);
-  int64_t seg = std::max(kHeadSegMin, (a->tokens * p.tiles + kHeadSegTiles - 1) / kHeadSegTiles);
-  seg = (seg + 63) / 64 * 64;
-  if (seg < a->tokens) {
+  const bool f32 = a->io_dtype == MSS_F32;
+  const int64_t chunk = f32 ? 32 : 64;
+  // workgroups a CU holds (by LDS and registers): three of the small fp32 kernels
+  const int64_t slots = kCus * (f32 && a->dstate <= 64 ? 3 : 2);
+  const int64_t want = std::max<int64_t>(1, slots / p.tiles);
+  int64_t seg = ((a->tokens + want - 1) / want + chunk - 1) / chunk * chunk;
+  seg = std::clamp(seg, 4 * chunk, kSegMax);
+  if (a->tokens > 8 * chunk) {
     // a cut prompt has more than seg tokens, so at most 2 len / seg segments
     p.seg_len = seg;
     p.cut_slots = 2 * a->tokens / seg;
