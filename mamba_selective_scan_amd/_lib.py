@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmss.so")
@@ -281,6 +282,24 @@ class NormArgs(ctypes.Structure):
         ("residual_out", _vp), ("residual_out_stride", _i64),
         ("eps", ctypes.c_float), ("reserved0", _i32),
     ]
+
+
+def packer(cls):
+    """A function that makes a ``cls`` from its fields' values in order, without
+    struct_size (arrays flattened, None for a null pointer): one call of struct
+    instead of a store through ctypes for each field."""
+    codes = {ctypes.c_uint32: "I", _i32: "i", _i64: "q", _vp: "P", ctypes.c_size_t: "N",
+             ctypes.c_float: "f"}
+    fmt = "@"
+    for _, t in cls._fields_:
+        n = getattr(t, "_length_", None)
+        fmt += codes[t] if n is None else f"{n}{codes[t._type_]}"
+    pack, size, make = struct.Struct(fmt).pack, ctypes.sizeof(cls), cls.from_buffer_copy
+
+    def new(*values):
+        return make(pack(size, *values).ljust(size, b"\0"))
+
+    return new
 
 
 class MssError(RuntimeError):

@@ -19,16 +19,36 @@ namespace mss {
 namespace {
 
 constexpr int kWaves = 4;   // jobs per workgroup
-constexpr int kAhead = 4;   // rows loaded before the first of them is used
+constexpr int kAhead = 8;   // rows loaded before the first of them is used
 
-template <typename IO, int V, bool UNIT>
-__device__ inline void load_cols(const IO* row, int64_t sd, int n, float* v) {
-  if constexpr (UNIT) {
-    load_part<IO, V>(row, n, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = i < n ? io_traits<IO>::load(row + i * sd) : 0.0f;
+// A row's vector of channels as it lies in memory (a load in flight holds no
+// more registers than its bytes), and as fp32.
+template <typename IO, int V>
+struct Row {
+  typename vecio<IO, V>::raw q;
+  __device__ inline float get(int i) const {
+    if constexpr (sizeof(IO) == 4)
+      return q[i];
+    else
+      return __uint_as_float(i & 1 ? q[i / 2] & 0xffff0000u : q[i / 2] << 16);
   }
+};
+template <typename IO, int V, bool UNIT>
+__device__ inline Row<IO, V> load_cols(const IO* row, int64_t sd, int n) {
+  Row<IO, V> r;
+  if (UNIT && n >= V) {
+    r.q = *reinterpret_cast<const typename vecio<IO, V>::raw*>(row);
+    return r;
+  }
+  union {
+    IO e[V];
+    Row<IO, V> r;
+  } u;
+  u.r.q = typename vecio<IO, V>::raw(0);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) u.e[i] = row[i * sd];
+  return u.r;
 }
 template <typename IO, int V, bool UNIT>
 __device__ inline void store_cols(IO* row, int64_t sd, int n, const float* v) {
@@ -57,29 +77,33 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompts_kernel(ConvPromptsAr
   float wk[W][V], bias[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
+    // (a weight whose taps lie together, as layers hold it, in one vector)
     const int d = min(c + i, a.dim - 1);
+    if (W == 4 && a.sw[1] == 1) {
+      float t[4];
+      vecio<float, 4>::load(a.weight + d * a.sw[0], t);
 #pragma unroll
-    for (int k = 0; k < W; ++k) wk[k][i] = a.weight[d * a.sw[0] + k * a.sw[1]];
-    bias[i] = a.bias != nullptr ? a.bias[d] : 0.0f;
-  }
-  float win[H > 0 ? H : 1][V];
-  auto slide = [&](const float* v) __attribute__((always_inline)) {
+      for (int k = 0; k < W; ++k) wk[k][i] = t[k];
+    } else {
 #pragma unroll
-    for (int k = 0; k + 1 < H; ++k)
-#pragma unroll
-      for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
-    if constexpr (H > 0) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) win[H - 1][i] = v[i];
+      for (int k = 0; k < W; ++k) wk[k][i] = a.weight[d * a.sw[0] + k * a.sw[1]];
     }
+    bias[i] = 0.0f;
+  }
+  if (a.bias != nullptr) load_part<float, V>(a.bias + c, nc, bias);
+  Row<IO, V> win[H > 0 ? H : 1];
+  auto slide = [&](const Row<IO, V>& v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k + 1 < H; ++k) win[k] = win[k + 1];
+    if constexpr (H > 0) win[H - 1] = v;
   };
-  auto filter = [&](const float* v, float* y) __attribute__((always_inline)) {
+  auto filter = [&](const Row<IO, V>& v, float* y) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float acc = bias[i];
 #pragma unroll
-      for (int k = 0; k < H; ++k) acc = fmaf(wk[k][i], win[k][i], acc);
-      acc = fmaf(wk[H][i], v[i], acc);
+      for (int k = 0; k < H; ++k) acc = fmaf(wk[k][i], win[k].get(i), acc);
+      acc = fmaf(wk[H][i], v.get(i), acc);
       y[i] = a.silu ? silu(acc) : acc;
     }
   };
@@ -93,12 +117,12 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompts_kernel(ConvPromptsAr
     Span sp = prompt_span(a.q, s);
     bool keep = slot_of(a.q.slots, a.q.cache_slots, s) >= 0;
 #pragma unroll
-    for (int k = 0; k < H; ++k) load_cols<IO, V, UNIT>(x + max(t - H + k, 0) * a.sx[0], a.sx[1], nc, win[k]);
+    for (int k = 0; k < H; ++k) win[k] = load_cols<IO, V, UNIT>(x + max(t - H + k, 0) * a.sx[0], a.sx[1], nc);
     for (; t < t1; t += kAhead) {
-      float v[kAhead][V];
+      Row<IO, V> v[kAhead];
 #pragma unroll
       for (int r = 0; r < kAhead; ++r)
-        load_cols<IO, V, UNIT>(x + min(t + r, t1 - 1) * a.sx[0], a.sx[1], nc, v[r]);
+        v[r] = load_cols<IO, V, UNIT>(x + min(t + r, t1 - 1) * a.sx[0], a.sx[1], nc);
 #pragma unroll
       for (int r = 0; r < kAhead; ++r) {
         if (t + r < t1) {
@@ -128,18 +152,26 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompts_kernel(ConvPromptsAr
     const bool from_cache = resumes(a.q, s);
     if (len == 0 && from_cache) return;
     IO* cache = static_cast<IO*>(a.window) + slot * a.swin + static_cast<int64_t>(c) * H;
+    union Loose {
+      IO e[V];
+      Row<IO, V> r;
+    };
 #pragma unroll
-    for (int k = 0; k < H; ++k)
+    for (int k = 0; k < H; ++k) {
+      Loose u;
+      u.r.q = typename vecio<IO, V>::raw(0);
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        win[k][i] = from_cache && i < nc ? io_traits<IO>::load(cache + i * H + k) : 0.0f;
+        if (from_cache && i < nc) u.e[i] = cache[i * H + k];
+      win[k] = u.r;
+    }
     // the first H rows, with the window sliding over them; after them the
     // window holds the samples before row min(len, H)
 #pragma unroll
     for (int r = 0; r < H; ++r) {
       if (r < len) {
-        float v[V], y[V];
-        load_cols<IO, V, UNIT>(x + (sp.begin + r) * a.sx[0], a.sx[1], nc, v);
+        float y[V];
+        const Row<IO, V> v = load_cols<IO, V, UNIT>(x + (sp.begin + r) * a.sx[0], a.sx[1], nc);
         filter(v, y);
         store_cols<IO, V, UNIT>(out + (sp.begin + r) * a.so[0], a.so[1], nc, y);
         slide(v);
@@ -148,13 +180,16 @@ __global__ __launch_bounds__(64 * kWaves) void conv_prompts_kernel(ConvPromptsAr
     if (len > H) {
 #pragma unroll
       for (int k = 0; k < H; ++k)
-        load_cols<IO, V, UNIT>(x + (sp.end - H + k) * a.sx[0], a.sx[1], nc, win[k]);
+        win[k] = load_cols<IO, V, UNIT>(x + (sp.end - H + k) * a.sx[0], a.sx[1], nc);
     }
 #pragma unroll
-    for (int k = 0; k < H; ++k)
+    for (int k = 0; k < H; ++k) {
+      Loose u;
+      u.r = win[k];
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i < nc) io_traits<IO>::store(cache + i * H + k, win[k][i]);
+        if (i < nc) cache[i * H + k] = u.e[i];
+    }
   }
 }
 

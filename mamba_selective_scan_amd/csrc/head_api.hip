@@ -304,7 +304,7 @@ size_t mss_head_scan_step_workspace_size(const mss_head_step_args* a, mss_status
   const mss_status st = check_step_shape(a);
   if (status != nullptr) *status = st;
   if (st != MSS_OK) return 0;
-  return static_cast<size_t>(a->rows * (a->heads * a->headdim + 2 * a->groups * a->dstate) * 4);
+  return static_cast<size_t>(a->rows * 2 * a->groups * a->dstate * 4);  // filtered B and C
 }
 
 mss_status mss_head_scan_step(const mss_head_step_args* a, void* stream) {
@@ -329,7 +329,7 @@ mss_status mss_head_scan_step(const mss_head_step_args* a, void* stream) {
       !aligned(a->bias, 4) || !aligned(a->D, 4) || !aligned(a->dt_bias, 4) || !aligned(a->slots, 4) ||
       !aligned(a->workspace, 256))
     return MSS_ERR_MISALIGNED;
-  const size_t need = static_cast<size_t>(R * chans * 4);
+  const size_t need = static_cast<size_t>(R * 2 * G * N * 4);
   if (a->workspace == nullptr || a->workspace_bytes < need) return MSS_ERR_WORKSPACE_TOO_SMALL;
   const Extent ins[] = {extent_of(a->xbc, xs, a->xbc_stride, 2, es), extent_of(a->dt_raw, ds, a->dt_stride, 2, es),
                         extent_of(a->z, os, a->z_stride, 3, es), extent_of(a->weight, ws, a->weight_stride, 2, 4),

@@ -72,7 +72,7 @@ struct HeadStepArgs {
   float* state;
   void* window;
   void* out;
-  float* u;  // workspace [rows][channels]: the conv's output
+  float* u;  // workspace [rows][2 G N]: the filtered B and C
 };
 
 struct NormArgs {

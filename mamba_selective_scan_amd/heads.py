@@ -26,10 +26,32 @@ import ctypes
 
 import torch
 
-from . import _ACTIVATIONS, _conv_weight, _launch, _lib, _need_gpu, _workspace
+from . import _ACTIVATIONS, _conv_weight, _lib, _need_gpu, _workspace
 
 _IO = {torch.float32: _lib.MSS_F32, torch.bfloat16: _lib.MSS_BF16}
 _QUANT = {None: _lib.MSS_QUANT_NONE, "row": _lib.MSS_QUANT_ROW, "block": _lib.MSS_QUANT_BLOCK}
+
+
+_conv_args = _lib.packer(_lib.ConvPromptsArgs)
+_scan_args = _lib.packer(_lib.HeadScanArgs)
+_step_args = _lib.packer(_lib.HeadStepArgs)
+_norm_args = _lib.packer(_lib.NormArgs)
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _launch(fn, args, device):
+    """Call a library entry point on torch's current stream of ``device``, with
+    ``device`` current (as the package's own launches, whose stream lookup costs
+    more than the rest of a small call)."""
+    index = device.index
+    if index == _current_device():
+        code = fn(ctypes.byref(args), _current_stream(index))
+    else:
+        with torch.cuda.device(device):
+            code = fn(ctypes.byref(args), _current_stream(index))
+    if code:
+        _lib.check(code)
 
 
 def _io(t):
@@ -53,11 +75,11 @@ def _like(t, name, shape, dtype, device):
 
 
 def _vector(t, name, n, dtype, device):
-    """A contiguous vector's address, or None."""
+    """A contiguous vector's address, or 0 for None."""
     if t is None:
-        return None
+        return 0
     _like(t, name, (n,), dtype, device)
-    if not t.is_contiguous():
+    if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -71,28 +93,30 @@ def _cache(t, name, inner, dtype, device):
         raise ValueError(f"{name} must have shape [slots, {', '.join(map(str, inner))}], got "
                          f"{tuple(t.shape)}")
     _like(t, name, (t.shape[0], *inner), dtype, device)
-    step = 0 if 0 in inner else 1  # an empty entry has any strides
-    for size, stride in zip(reversed(inner), reversed(t.stride()[1:])):
-        if size > 1 and step > 0 and stride != step:
-            raise ValueError(f"each entry of {name} must be contiguous")
-        step *= size
+    if not t.is_contiguous() and not t[0].is_contiguous():
+        raise ValueError(f"each entry of {name} must be contiguous")
     return t.shape[0], t.data_ptr(), t.stride(0)
 
 
-def _prompts(a, cu_seqlens, slots, resume, device):
+def _prompts(cu_seqlens, slots, resume, device):
+    """Number of prompts, and the addresses of the three vectors."""
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be a vector of at least 2 offsets")
     n = cu_seqlens.shape[0] - 1
-    a.seqs = n
-    a.cu_seqlens = _vector(cu_seqlens, "cu_seqlens", n + 1, torch.int32, device)
-    a.slots = _vector(slots, "slots", n, torch.int32, device)
-    a.resume = _vector(resume, "resume", n, torch.int32, device)
+    return (n, _vector(cu_seqlens, "cu_seqlens", n + 1, torch.int32, device),
+            _vector(slots, "slots", n, torch.int32, device),
+            _vector(resume, "resume", n, torch.int32, device))
 
 
 def _out(out, shape, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
     return _like(out, "out", shape, dtype, device)
+
+
+def _optional(t):
+    """Address and strides of a 3-d tensor, or zeros for None."""
+    return (0, 0, 0, 0) if t is None else (t.data_ptr(), *t.stride())
 
 
 def _give_workspace(a, need, workspace, device):
@@ -124,18 +148,12 @@ def causal_conv1d_prompts(x, weight, bias=None, *, cu_seqlens, window, slots=Non
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be 'silu' or None, got {activation!r}")
     out = _out(out, x.shape, x.dtype, dev)
-    a = _lib.ConvPromptsArgs()
-    a.struct_size = ctypes.sizeof(a)
-    a.io_dtype = _io(x)
-    a.tokens, a.dim, a.width = tokens, dim, width
-    a.x, a.x_stride[:] = x.data_ptr(), x.stride()
-    a.weight, a.weight_stride[:] = weight.data_ptr(), weight.stride()
-    a.bias = _vector(bias, "bias", dim, torch.float32, dev)
-    _prompts(a, cu_seqlens, slots, resume, dev)
-    a.cache_slots, a.window, a.window_stride = _cache(window, "window", (dim, width - 1), x.dtype,
-                                                      dev)
-    a.out, a.out_stride[:] = out.data_ptr(), out.stride()
-    a.activation = _ACTIVATIONS[activation]
+    n, *prompts = _prompts(cu_seqlens, slots, resume, dev)
+    cache_slots, *cache = _cache(window, "window", (dim, width - 1), x.dtype, dev)
+    a = _conv_args(_io(x), tokens, dim, width, n, cache_slots,
+                   x.data_ptr(), *x.stride(), weight.data_ptr(), *weight.stride(),
+                   _vector(bias, "bias", dim, torch.float32, dev), *prompts, *cache,
+                   out.data_ptr(), *out.stride(), _ACTIVATIONS[activation], 0)
     _launch(_lib.lib().mss_causal_conv1d_prompts, a, dev)
     return out
 
@@ -165,25 +183,17 @@ def head_scan_prompts(x, dt_raw, A_log, B, C, D=None, z=None, dt_bias=None, *, c
     _like(dt_raw, "dt_raw", (tokens, heads), dt, dev)
     groups, dstate = B.shape[1:]
     out = _out(out, x.shape, dt, dev)
-    a = _lib.HeadScanArgs()
-    a.struct_size = ctypes.sizeof(a)
-    a.io_dtype = _io(x)
-    a.tokens, a.heads, a.headdim, a.dstate, a.groups = tokens, heads, headdim, dstate, groups
-    a.x, a.x_stride[:] = x.data_ptr(), x.stride()
-    a.dt_raw, a.dt_stride[:] = dt_raw.data_ptr(), dt_raw.stride()
-    a.A_log = _vector(A_log, "A_log", heads, torch.float32, dev)
-    a.B, a.B_stride[:] = B.data_ptr(), B.stride()
-    a.C, a.C_stride[:] = C.data_ptr(), C.stride()
-    a.D = _vector(D, "D", heads, torch.float32, dev)
     if z is not None:
         _like(z, "z", x.shape, dt, dev)
-        a.z, a.z_stride[:] = z.data_ptr(), z.stride()
-    a.dt_bias = _vector(dt_bias, "dt_bias", heads, torch.float32, dev)
-    _prompts(a, cu_seqlens, slots, resume, dev)
-    a.cache_slots, a.state, a.state_stride = _cache(state, "state", (heads, headdim, dstate),
-                                                    torch.float32, dev)
-    a.out, a.out_stride[:] = out.data_ptr(), out.stride()
-    a.delta_softplus = 1 if delta_softplus else 0
+    n, *prompts = _prompts(cu_seqlens, slots, resume, dev)
+    cache_slots, *cache = _cache(state, "state", (heads, headdim, dstate), torch.float32, dev)
+    a = _scan_args(_io(x), tokens, heads, headdim, dstate, groups, n, cache_slots,
+                   x.data_ptr(), *x.stride(), dt_raw.data_ptr(), *dt_raw.stride(),
+                   _vector(A_log, "A_log", heads, torch.float32, dev),
+                   B.data_ptr(), *B.stride(), C.data_ptr(), *C.stride(),
+                   _vector(D, "D", heads, torch.float32, dev), *_optional(z),
+                   _vector(dt_bias, "dt_bias", heads, torch.float32, dev), *prompts, *cache,
+                   out.data_ptr(), *out.stride(), 1 if delta_softplus else 0, 0, 0, 0)
     lib = _lib.lib()
     st = ctypes.c_int(0)
     need = lib.mss_head_scan_prompts_workspace_size(ctypes.byref(a), ctypes.byref(st))
@@ -220,29 +230,22 @@ def head_scan_step(state, window, xbc, dt_raw, A_log, weight, bias=None, D=None,
     weight = _conv_weight(weight, chans, dev)
     width = weight.shape[1]
     out = _out(out, (rows, heads, headdim), dt, dev)
-    a = _lib.HeadStepArgs()
-    a.struct_size = ctypes.sizeof(a)
-    a.io_dtype = _io(xbc)
-    a.rows, a.heads, a.headdim, a.dstate, a.groups = rows, heads, headdim, dstate, groups
-    a.width = width
-    a.cache_slots, a.state, a.state_stride = _cache(state, "state", (heads, headdim, dstate),
-                                                    torch.float32, dev)
-    slots_w, a.window, a.window_stride = _cache(window, "window", (chans, width - 1), dt, dev)
-    if slots_w != a.cache_slots:
-        raise ValueError(f"window has {slots_w} slots, state {a.cache_slots}")
-    a.xbc, a.xbc_stride[:] = xbc.data_ptr(), xbc.stride()
-    a.dt_raw, a.dt_stride[:] = dt_raw.data_ptr(), dt_raw.stride()
-    a.A_log = _vector(A_log, "A_log", heads, torch.float32, dev)
-    a.weight, a.weight_stride[:] = weight.data_ptr(), weight.stride()
-    a.bias = _vector(bias, "bias", chans, torch.float32, dev)
-    a.D = _vector(D, "D", heads, torch.float32, dev)
     if z is not None:
         _like(z, "z", (rows, heads, headdim), dt, dev)
-        a.z, a.z_stride[:] = z.data_ptr(), z.stride()
-    a.dt_bias = _vector(dt_bias, "dt_bias", heads, torch.float32, dev)
-    a.slots = _vector(slots, "slots", rows, torch.int32, dev)
-    a.out, a.out_stride[:] = out.data_ptr(), out.stride()
-    a.delta_softplus = 1 if delta_softplus else 0
+    cache_slots, *states = _cache(state, "state", (heads, headdim, dstate), torch.float32, dev)
+    window_slots, *windows = _cache(window, "window", (chans, width - 1), dt, dev)
+    if window_slots != cache_slots:
+        raise ValueError(f"window has {window_slots} slots, state {cache_slots}")
+    a = _step_args(_io(xbc), rows, heads, headdim, dstate, groups, width, cache_slots,
+                   *states, *windows, xbc.data_ptr(), *xbc.stride(),
+                   dt_raw.data_ptr(), *dt_raw.stride(),
+                   _vector(A_log, "A_log", heads, torch.float32, dev),
+                   weight.data_ptr(), *weight.stride(),
+                   _vector(bias, "bias", chans, torch.float32, dev),
+                   _vector(D, "D", heads, torch.float32, dev), *_optional(z),
+                   _vector(dt_bias, "dt_bias", heads, torch.float32, dev),
+                   _vector(slots, "slots", rows, torch.int32, dev),
+                   out.data_ptr(), *out.stride(), 1 if delta_softplus else 0, 0, 0, 0)
     lib = _lib.lib()
     st = ctypes.c_int(0)
     need = lib.mss_head_scan_step_workspace_size(ctypes.byref(a), ctypes.byref(st))
@@ -278,16 +281,9 @@ def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=
         raise ValueError(f"quant must be None, 'row' or 'block', got {quant!r}")
     dev, shape = x.device, x.shape
     rows, dim = shape
-    a = _lib.NormArgs()
-    a.struct_size = ctypes.sizeof(a)
-    a.io_dtype = a.residual_dtype = _io(x)
-    a.quant = _QUANT[quant]
-    a.rows, a.dim, a.eps = rows, dim, eps
-    a.x, a.x_stride = _rows(x, "x", shape, x.dtype, dev)
-    a.weight = _vector(weight, "weight", dim, torch.float32, dev)
+    _like(x, "x", shape, x.dtype, dev)
     out = _out(out, shape, x.dtype if quant is None else torch.float8_e4m3fn, dev)
-    a.out, a.out_stride = _rows(out, "out", shape, out.dtype, dev)
-    left = (out,)
+    left, scales, res, res_type = (out,), 0, (0, 0, 0, 0), _io(x)
     if quant is not None:
         if quant == "block" and dim % _lib.MSS_SCALE_BLOCK:
             raise ValueError(f"quant 'block' needs a multiple of {_lib.MSS_SCALE_BLOCK} columns, got {dim}")
@@ -296,19 +292,21 @@ def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=
             scale = torch.empty(want, dtype=torch.float32, device=dev)
         elif not _like(scale, "scale", want, torch.float32, dev).is_contiguous():
             raise ValueError("scale must be contiguous")
-        a.scale = scale.data_ptr()
-        left += (scale,)
+        scales = scale.data_ptr()
+        left = (out, scale)
     elif scale is not None:
         raise ValueError("scale is given without quant")
     if residual is not None:
-        a.residual_dtype = _io(residual)
-        a.residual, a.residual_stride = _rows(residual, "residual", shape, residual.dtype, dev)
+        res_type = _io(residual)
+        res = _rows(residual, "residual", shape, residual.dtype, dev)
         if residual_out is None:
             residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
-        a.residual_out, a.residual_out_stride = _rows(residual_out, "residual_out", shape,
-                                                      residual.dtype, dev)
+        res += _rows(residual_out, "residual_out", shape, residual.dtype, dev)
         left += (residual_out,)
     elif residual_out is not None:
         raise ValueError("residual_out is given without residual")
+    a = _norm_args(_io(x), res_type, _QUANT[quant], rows, dim, *_rows(x, "x", shape, x.dtype, dev),
+                   *res[:2], _vector(weight, "weight", dim, torch.float32, dev),
+                   *_rows(out, "out", shape, out.dtype, dev), scales, *res[2:], eps, 0)
     _launch(_lib.lib().mss_rms_norm, a, dev)
     return left if len(left) > 1 else out

@@ -153,7 +153,7 @@ def test_other_refusals():
     refused("norm", "MSS_ERR_BAD_STRUCT", quant=3)
     refused("norm", "MSS_ERR_UNSUPPORTED_DTYPE", residual_dtype=5)
     refused("step", "MSS_ERR_WORKSPACE_TOO_SMALL", workspace=None)
-    refused("step", "MSS_ERR_WORKSPACE_TOO_SMALL", workspace_bytes=3 * 768 * 4 - 1)
+    refused("step", "MSS_ERR_WORKSPACE_TOO_SMALL", workspace_bytes=3 * 512 * 4 - 1)
     # views between which nothing overlaps but whose ranges interleave are
     # refused as well: the check is on ranges
     refused("norm", "MSS_ERR_ALIASING", out=fake(0) + 512, x_stride=1024, out_stride=2048)
@@ -161,7 +161,7 @@ def test_other_refusals():
 
 def test_workspace_sizes():
     lib, st = _lib.lib(), ctypes.c_int(0)
-    assert lib.mss_head_scan_step_workspace_size(ctypes.byref(step()), ctypes.byref(st)) == 3 * 768 * 4
+    assert lib.mss_head_scan_step_workspace_size(ctypes.byref(step()), ctypes.byref(st)) == 3 * 512 * 4
     assert st.value == 0
     assert lib.mss_head_scan_step_workspace_size(ctypes.byref(put(step(), rows=0)), ctypes.byref(st)) == 0
     assert st.value == _lib.STATUS_CODE["MSS_ERR_BAD_SHAPE"]
