@@ -594,6 +594,13 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     }
     if (not_finite<IO>(odd)) lds.odd[par] = 1;
     const IO raw = fetch_dt(t + Q);
+    // the next chunk's rows: in the sums, which have registers to spare, a whole
+    // chunk ahead; in the walk, once the outputs have left theirs.  (Past the end:
+    // zeros; under a condition the old values would stay live until here.)
+    if constexpr (AGG) {
+      step_end();
+      fetch(t + Q);
+    }
     __syncthreads();
     walk = uniform(lds.odd[par]) != 0;
     if (threadIdx.x == 0) lds.odd[par ^ 1] = 0;
@@ -766,10 +773,10 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     }
 
     // ---- the next chunk's rows and time steps
-    fetch(t + Q);  // (past the end: zeros; under a condition the old values would stay live until here)
+    if constexpr (!AGG) fetch(t + Q);
     step_end();
     const float dec = decay;
-    times(t + Q, raw, par ^ 1);
+    if constexpr (!AGG) times(t + Q, raw, par ^ 1);
     step_end();
 
     // ---- the state
@@ -818,6 +825,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
         step_end();
       }
     }
+    if constexpr (AGG) times(t + Q, raw, par ^ 1);
     zw += Q * a.sz[0];
     ow += Q * a.so[0];
     __syncthreads();
@@ -865,7 +873,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       }
       state_in(true);
     }
-    fetch(t + Q);
+    if constexpr (!AGG) fetch(t + Q);
     times(t + Q, fetch_dt(t + Q), par ^ 1);
     zw += Q * a.sz[0];
     ow += Q * a.so[0];

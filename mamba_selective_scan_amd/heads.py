@@ -74,6 +74,21 @@ def _like(t, name, shape, dtype, device):
     return t
 
 
+def _gpu(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _need_gpu(t, name)  # (raises, saying what it got)
+    return t.device
+
+
+def _weight(weight, dim, device):
+    """A conv weight as [dim, W] fp32."""
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    if weight.dim() != 2:
+        return _conv_weight(weight, dim, device)
+    return _like(weight, "weight", (dim, weight.shape[1]), torch.float32, device)
+
+
 def _vector(t, name, n, dtype, device):
     """A contiguous vector's address, or 0 for None."""
     if t is None:
@@ -139,11 +154,11 @@ def causal_conv1d_prompts(x, weight, bias=None, *, cu_seqlens, window, slots=Non
     samples of each sequence, read for prompts that resume and left updated.
     Returns out [T, D]; without ``out``, rows of no prompt are undefined.
     """
-    _need_gpu(x, "x")
+    dev = _gpu(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must have 2 dimensions, got shape {tuple(x.shape)}")
-    dev, (tokens, dim) = x.device, x.shape
-    weight = _conv_weight(weight, dim, dev)
+    tokens, dim = x.shape
+    weight = _weight(weight, dim, dev)
     width = weight.shape[1]
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be 'silu' or None, got {activation!r}")
@@ -172,10 +187,10 @@ def head_scan_prompts(x, dt_raw, A_log, B, C, D=None, z=None, dt_bias=None, *, c
     undefined.  ``workspace`` (uint8) may be supplied to avoid its allocation;
     calls that may overlap in time need one each.
     """
-    _need_gpu(x, "x")
+    dev = _gpu(x, "x")
     if x.dim() != 3:
         raise ValueError(f"x must have 3 dimensions, got shape {tuple(x.shape)}")
-    dev, dt, (tokens, heads, headdim) = x.device, x.dtype, x.shape
+    dt, (tokens, heads, headdim) = x.dtype, x.shape
     if not isinstance(B, torch.Tensor) or B.dim() != 3 or B.shape[0] != tokens:
         raise ValueError(f"B must have shape [{tokens}, groups, dstate]")
     _like(B, "B", B.shape, dt, dev)
@@ -215,11 +230,11 @@ def head_scan_step(state, window, xbc, dt_raw, A_log, weight, bias=None, D=None,
     dt_bias [H] fp32; z [rows, H, P] or None.  Returns out [rows, H, P];
     without ``out``, skipped rows are undefined.
     """
-    _need_gpu(state, "state")
-    _need_gpu(xbc, "xbc")
+    dev = _gpu(state, "state")
+    _gpu(xbc, "xbc")
     if state.dim() != 4 or xbc.dim() != 2:
         raise ValueError("state must be [slots, H, P, N] and xbc [rows, channels]")
-    dev, dt, (rows, chans) = state.device, xbc.dtype, xbc.shape
+    dt, (rows, chans) = xbc.dtype, xbc.shape
     heads, headdim, dstate = state.shape[1:]
     groups, rest = divmod(chans - heads * headdim, 2 * max(dstate, 1))
     if rest or groups < 1:
@@ -227,7 +242,7 @@ def head_scan_step(state, window, xbc, dt_raw, A_log, weight, bias=None, D=None,
                          f"{dstate}")
     _like(xbc, "xbc", xbc.shape, dt, dev)
     _like(dt_raw, "dt_raw", (rows, heads), dt, dev)
-    weight = _conv_weight(weight, chans, dev)
+    weight = _weight(weight, chans, dev)
     width = weight.shape[1]
     out = _out(out, (rows, heads, headdim), dt, dev)
     if z is not None:
@@ -274,12 +289,12 @@ def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=
     [R, D / 128].  With a residual, r in the residual's dtype is returned last;
     ``residual_out`` may be ``residual`` itself, which is then updated in place.
     """
-    _need_gpu(x, "x")
+    dev = _gpu(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x must have 2 dimensions, got shape {tuple(x.shape)}")
     if quant not in _QUANT:
         raise ValueError(f"quant must be None, 'row' or 'block', got {quant!r}")
-    dev, shape = x.device, x.shape
+    shape = x.shape
     rows, dim = shape
     _like(x, "x", shape, x.dtype, dev)
     out = _out(out, shape, x.dtype if quant is None else torch.float8_e4m3fn, dev)
