@@ -561,8 +561,8 @@ typedef struct mss_head_scan_args {
     const int32_t *cu_seqlens;   /* [seqs + 1]                                           */
     const int32_t *slots;        /* [seqs]                                               */
     const int32_t *resume;       /* [seqs]                                               */
-    float *state;                /* [slot][h][p][n] fp32, each slot contiguous, 16-byte  */
-    int64_t state_stride;        /* aligned; elements from slot to slot                  */
+    float *state;                /* [slot][h][p][n] fp32, each slot contiguous           */
+    int64_t state_stride;        /* elements from slot to slot                           */
     void *out;                   /* [t,h,p], unit stride in p (NULL iff tokens == 0)     */
     int64_t out_stride[3];
     int32_t delta_softplus;      /* nonzero: delta = softplus(dt_raw + dt_bias)          */
@@ -586,8 +586,8 @@ typedef struct mss_head_step_args {
     int64_t width;               /* conv taps, 1..MSS_MAX_CONV_WIDTH                     */
     int64_t cache_slots;
 
-    float *state;                /* [slot][h][p][n] fp32, each slot contiguous, 16-byte  */
-    int64_t state_stride;        /* aligned; elements from slot to slot                  */
+    float *state;                /* [slot][h][p][n] fp32, each slot contiguous           */
+    int64_t state_stride;        /* elements from slot to slot                           */
     void *window;                /* [slot][c][width-1] io_dtype, c over the H P + 2 G N  */
     int64_t window_stride;       /* channels, each slot contiguous (NULL iff width == 1) */
     const void *xbc;             /* [b,c] new samples: x [H][P], then B [G][N], C [G][N] */
@@ -607,8 +607,6 @@ typedef struct mss_head_step_args {
     int64_t out_stride[3];
     int32_t delta_softplus;
     int32_t reserved0;           /* must be 0                                            */
-    void *workspace;             /* device scratch, 256-byte aligned, of at least        */
-    size_t workspace_bytes;      /* mss_head_scan_step_workspace_size bytes              */
 } mss_head_step_args;
 
 /* Output of mss_rms_norm. */
@@ -658,11 +656,9 @@ size_t mss_head_scan_prompts_workspace_size(const mss_head_scan_args *args, mss_
  * its own until the call has run: two calls that may overlap in time need two. */
 mss_status mss_head_scan_prompts(const mss_head_scan_args *args, void *stream);
 
-/* Bytes of device workspace mss_head_scan_step needs (from the sizes alone). */
-size_t mss_head_scan_step_workspace_size(const mss_head_step_args *args, mss_status *status);
-
 /* One token a row through conv and head-wise scan (see the top of this file).
- * state and window are updated in place; out must not overlap any input. */
+ * state and window are updated in place; out must not overlap any input.  No
+ * workspace. */
 mss_status mss_head_scan_step(const mss_head_step_args *args, void *stream);
 
 /* Root-mean-square norm with the residual's addition (see the top of this

@@ -51,8 +51,7 @@ EXPORTS = ("mss_abi_version", "mss_status_string", "mss_selective_scan_workspace
            "mss_selective_scan_bwd", "mss_selective_scan_fwd_complex",
            "mss_selective_scan_fwd_noalloc", "mss_selective_scan_fwd_complex_workspace_size",
            "mss_causal_conv1d_prompts", "mss_head_scan_prompts",
-           "mss_head_scan_prompts_workspace_size", "mss_head_scan_step",
-           "mss_head_scan_step_workspace_size", "mss_rms_norm")
+           "mss_head_scan_prompts_workspace_size", "mss_head_scan_step", "mss_rms_norm")
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -265,7 +264,6 @@ class HeadStepArgs(ctypes.Structure):
         ("slots", _vp),
         ("out", _vp), ("out_stride", _i64 * 3),
         ("delta_softplus", _i32), ("reserved0", _i32),
-        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -349,9 +347,6 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.mss_head_scan_prompts_workspace_size.restype = ctypes.c_size_t
     lib.mss_head_scan_prompts.argtypes = [ctypes.POINTER(HeadScanArgs), _vp]
     lib.mss_head_scan_prompts.restype = ctypes.c_int
-    lib.mss_head_scan_step_workspace_size.argtypes = [ctypes.POINTER(HeadStepArgs),
-                                                      ctypes.POINTER(ctypes.c_int)]
-    lib.mss_head_scan_step_workspace_size.restype = ctypes.c_size_t
     lib.mss_head_scan_step.argtypes = [ctypes.POINTER(HeadStepArgs), _vp]
     lib.mss_head_scan_step.restype = ctypes.c_int
     lib.mss_rms_norm.argtypes = [ctypes.POINTER(NormArgs), _vp]

@@ -230,7 +230,7 @@ mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
     return MSS_ERR_BAD_STRIDE;
   if (!aligned(a->x, es) || !aligned(a->dt_raw, es) || !aligned(a->B, es) || !aligned(a->C, es) ||
       !aligned(a->z, es) || !aligned(a->out, es) || !aligned(a->A_log, 4) || !aligned(a->D, 4) ||
-      !aligned(a->dt_bias, 4) || !aligned(a->state, 16) || !aligned(a->cu_seqlens, 4) ||
+      !aligned(a->dt_bias, 4) || !aligned(a->state, 4) || !aligned(a->cu_seqlens, 4) ||
       !aligned(a->slots, 4) || !aligned(a->resume, 4) || !aligned(a->workspace, 256))
     return MSS_ERR_MISALIGNED;
   const bool any = T > 0;
@@ -300,13 +300,6 @@ mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
   return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
 }
 
-size_t mss_head_scan_step_workspace_size(const mss_head_step_args* a, mss_status* status) {
-  const mss_status st = check_step_shape(a);
-  if (status != nullptr) *status = st;
-  if (st != MSS_OK) return 0;
-  return static_cast<size_t>(a->rows * 2 * a->groups * a->dstate * 4);  // filtered B and C
-}
-
 mss_status mss_head_scan_step(const mss_head_step_args* a, void* stream) {
   const mss_status shape = check_step_shape(a);
   if (shape != MSS_OK) return shape;
@@ -324,13 +317,10 @@ mss_status mss_head_scan_step(const mss_head_step_args* a, void* stream) {
   if (!cache_stride_ok(a->cache_slots, H * P * N, a->state_stride) ||
       (W > 1 && !cache_stride_ok(a->cache_slots, chans * (W - 1), a->window_stride)))
     return MSS_ERR_BAD_STRIDE;
-  if (!aligned(a->state, 16) || !aligned(a->window, es) || !aligned(a->xbc, es) || !aligned(a->dt_raw, es) ||
+  if (!aligned(a->state, 4) || !aligned(a->window, es) || !aligned(a->xbc, es) || !aligned(a->dt_raw, es) ||
       !aligned(a->z, es) || !aligned(a->out, es) || !aligned(a->A_log, 4) || !aligned(a->weight, 4) ||
-      !aligned(a->bias, 4) || !aligned(a->D, 4) || !aligned(a->dt_bias, 4) || !aligned(a->slots, 4) ||
-      !aligned(a->workspace, 256))
+      !aligned(a->bias, 4) || !aligned(a->D, 4) || !aligned(a->dt_bias, 4) || !aligned(a->slots, 4))
     return MSS_ERR_MISALIGNED;
-  const size_t need = static_cast<size_t>(R * 2 * G * N * 4);
-  if (a->workspace == nullptr || a->workspace_bytes < need) return MSS_ERR_WORKSPACE_TOO_SMALL;
   const Extent ins[] = {extent_of(a->xbc, xs, a->xbc_stride, 2, es), extent_of(a->dt_raw, ds, a->dt_stride, 2, es),
                         extent_of(a->z, os, a->z_stride, 3, es), extent_of(a->weight, ws, a->weight_stride, 2, 4),
                         vec(a->A_log, H, 4), vec(a->bias, chans, 4), vec(a->D, H, 4), vec(a->dt_bias, H, 4),
@@ -338,9 +328,8 @@ mss_status mss_head_scan_step(const mss_head_step_args* a, void* stream) {
   const Extent outs[] = {extent_of(a->out, os, a->out_stride, 3, es),
                          cache_extent(a->state, a->cache_slots, H * P * N, a->state_stride, 4),
                          W > 1 ? cache_extent(a->window, a->cache_slots, chans * (W - 1), a->window_stride, es)
-                               : Extent{},
-                         vec(a->workspace, static_cast<int64_t>(need), 1)};
-  for (int i = 0; i < 4; ++i) {
+                               : Extent{}};
+  for (int i = 0; i < 3; ++i) {
     if (any_overlap(outs[i], ins)) return MSS_ERR_ALIASING;
     for (int j = 0; j < i; ++j)
       if (overlaps(outs[i], outs[j])) return MSS_ERR_ALIASING;
@@ -374,7 +363,6 @@ mss_status mss_head_scan_step(const mss_head_step_args* a, void* stream) {
   k.state = a->state;
   k.window = a->window;
   k.out = a->out;
-  k.u = static_cast<float*>(a->workspace);
   const hipError_t e = mss::launch_head_step(k, a->io_dtype == MSS_BF16, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
 }

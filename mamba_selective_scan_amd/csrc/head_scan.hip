@@ -34,8 +34,9 @@
 // segment adds to a zero state, one composes the states entering the segments
 // (and the state the prompt leaves), and the walk then runs all segments at once.
 //
-// A chunk that holds an infinity or a NaN in x or B is walked token by token
-// (0 times it would reach tokens before it, and splitting loses an infinity).
+// A chunk that holds an infinity or a NaN in x, B or C is walked token by token
+// (0 times one in x would reach tokens before it, splitting loses an infinity, and
+// infinities of both signs would meet in a sum that the recurrence does not form).
 #include "mss_head.hpp"
 
 namespace mss {
@@ -547,8 +548,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       const float dn = static_cast<float>(sum - (Q == 64 && lane >= 32 ? n1 : n0)), df = static_cast<float>(sum - far);
       // far factors that are used: rows from 32 on, columns before
       const float grow = lane < 32 ? -df : df;
-      const float worst = Q == 64 ? fmaxf(fabsf(dn), grow) : lane < Q ? fabsf(dn) : 0.0f;
-      steep = __ballot(!(worst <= kSteep)) != 0;
+      // (a NaN counts as steep: the factors would carry it to tokens before it)
+      steep = __ballot((Q == 64 || lane < Q) && (!(fabsf(dn) <= kSteep) || !(Q == 32 || grow <= kSteep))) != 0;
       const float hi = static_cast<float>(sum);
       if (Q == 64 || lane < Q) {
         m.enter[lane] = long_decay(hi);
@@ -584,7 +585,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
     for (int i = 0; i < kLoadBC; ++i) {
       *reinterpret_cast<u32x4*>(lds.b + wB + i * kRowsBC * BC::kRow) = pb[i];
-      odd = top_exponents<IO>(pb[i], odd);
+      if constexpr (AGG) odd = top_exponents<IO>(pb[i], odd);
       if constexpr (!AGG) *reinterpret_cast<u32x4*>(lds.c + wB + i * kRowsBC * BC::kRow) = pcc[i];
     }
 #pragma unroll
@@ -602,9 +603,11 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       fetch(t + Q);
     }
     __syncthreads();
-    walk = uniform(lds.odd[par]) != 0;
     if (threadIdx.x == 0) lds.odd[par ^ 1] = 0;
-    if (walk) break;
+    if constexpr (AGG) {
+      walk = uniform(lds.odd[par]) != 0;
+      if (walk) break;
+    }
     const auto& m = lds.time[par][wave];
 
     f32x4 y[AGG ? 1 : Q / 16][2];
@@ -650,6 +653,13 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
           for (int tp = 0; tp < 2; ++tp) y[it][tp] = mma(sb[tp], cf[it], q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
       }
+      // an infinity or a NaN in B or C is one in C B^T
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(acc[k][r]) & 0x7f800000u);
+      if (top == 0x7f800000u) lds.odd[par] = 1;
       // piece (ks, it) is number it (ks = 0) or it + 2
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
@@ -658,6 +668,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       }
       step_end();
       __syncthreads();
+      walk = uniform(lds.odd[par]) != 0;
+      if (walk) break;
     }
 
     if constexpr (!AGG) {

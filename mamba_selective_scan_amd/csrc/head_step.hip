@@ -7,46 +7,64 @@
 //   out   = (sum_n C[n] S[n] + D x) * silu(z)
 //
 // Bound by the states, read and written once (8 P N bytes a head; everything
-// else is two orders smaller).  Two launches.  The first filters the channels of
-// B and C, whose windows are read by all heads of a group and may only slide
-// once, and leaves them in fp32.  The second has a workgroup for each tile of a
-// head's columns: it starts the loads of the tile's states, filters the tile's x
-// channels (it alone reads their windows) while they are on their way, and walks
-// the states.
+// else is two orders smaller).  A workgroup has a tile of one head's columns: it
+// starts the loads of the tile's states, filters the tile's x channels and its
+// group's B and C while they are on their way, and walks the states.  The windows
+// of x slide there, where they have their only reader; those of B and C, which
+// every head of the group reads, in a second small launch.  (Filtering B and C
+// once for all heads, in a launch before, took a workspace and the same time.)
 #include "mss_head.hpp"
 
 namespace mss {
 namespace {
 
-// The conv of one channel: its window and new sample through the taps and SiLU;
-// the window slides.
+// One channel's window followed by its new sample, at the end of `line`.
 template <typename IO>
-__device__ inline float conv_step(const HeadStepArgs& a, int b, int slot, int c) {
+__device__ inline void conv_line(const HeadStepArgs& a, int b, int slot, int c, IO (&line)[4]) {
   const int H = a.width - 1;
-  IO* st = static_cast<IO*>(a.window) + slot * a.swin + static_cast<int64_t>(c) * H;
-  IO line[4];  // window and sample, at the end of the four
+  const IO* st = static_cast<const IO*>(a.window) + slot * a.swin + static_cast<int64_t>(c) * H;
 #pragma unroll
   for (int k = 0; k < 3; ++k)
     if (k >= 3 - H) line[k] = st[k - (3 - H)];
   line[3] = static_cast<const IO*>(a.xbc)[b * a.sx[0] + c * a.sx[1]];
+}
+template <typename IO>
+__device__ inline float conv_filter(const HeadStepArgs& a, int c, const IO (&line)[4]) {
+  const int H = a.width - 1;
   float acc = a.bias != nullptr ? a.bias[c] : 0.0f;
+  if (H == 3 && a.sw[1] == 1) {  // taps that lie together, as layers hold them
+    float w[4];
+    vecio<float, 4>::load(a.weight + c * a.sw[0], w);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k >= 3 - H) acc = fmaf(a.weight[c * a.sw[0] + (k - (3 - H)) * a.sw[1]], io_traits<IO>::load(&line[k]), acc);
+    for (int k = 0; k < 4; ++k) acc = fmaf(w[k], io_traits<IO>::load(&line[k]), acc);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k >= 3 - H) acc = fmaf(a.weight[c * a.sw[0] + (k - (3 - H)) * a.sw[1]], io_traits<IO>::load(&line[k]), acc);
+  }
+  return silu(acc);
+}
+template <typename IO>
+__device__ inline void conv_slide(const HeadStepArgs& a, int slot, int c, const IO (&line)[4]) {
+  const int H = a.width - 1;
+  IO* st = static_cast<IO*>(a.window) + slot * a.swin + static_cast<int64_t>(c) * H;
 #pragma unroll
   for (int k = 0; k < 3; ++k)
     if (k >= 3 - H) st[k - (3 - H)] = line[k + 1];
-  return silu(acc);
 }
 
+// Slides the windows of B and C.
 template <typename IO>
-__global__ __launch_bounds__(256) void head_step_conv_kernel(HeadStepArgs a, int bc) {
+__global__ __launch_bounds__(256) void head_step_slide_kernel(HeadStepArgs a, int bc) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<int64_t>(a.rows) * bc) return;
   const int b = static_cast<int>(i / bc);
   const int slot = slot_of(a.slots, a.cache_slots, b);
   if (slot < 0) return;
-  a.u[i] = conv_step<IO>(a, b, slot, a.heads * a.headdim + static_cast<int>(i % bc));
+  const int c = a.heads * a.headdim + static_cast<int>(i % bc);
+  IO line[4];
+  conv_line(a, b, slot, c, line);
+  conv_slide(a, slot, c, line);
 }
 
 // Sum over groups of LPR adjacent lanes, left in every lane of the group: quad
@@ -75,6 +93,7 @@ __global__ __launch_bounds__(256) void head_step_kernel(HeadStepArgs a, int ptil
   constexpr int RP = 256 / LPR;  // columns per pass
   constexpr int kCols = RP * NP;
   __shared__ float xs[kCols], ys[kCols];
+  __shared__ __attribute__((aligned(16))) float bc[2][kMaxHeadState];  // the group's B and C
   int64_t id = blockIdx.x;
   const int tile = static_cast<int>(id % ptiles);
   id /= ptiles;
@@ -93,17 +112,34 @@ __global__ __launch_bounds__(256) void head_step_kernel(HeadStepArgs a, int ptil
   for (int k = 0; k < NP; ++k)
     load_part<float, 4>(st + static_cast<int64_t>(k) * RP * a.dstate, pl + k * RP < cols ? nn : 0, s[k]);
   const int g = h / (a.heads / a.groups);
-  const float* u = a.u + static_cast<int64_t>(b) * 2 * a.groups * a.dstate;
-  float bn[4], cn[4];
-  load_part<float, 4>(u + g * a.dstate + n0, nn, bn);
-  load_part<float, 4>(u + (a.groups + g) * a.dstate + n0, nn, cn);
   const float xr = io_traits<IO>::load(static_cast<const IO*>(a.dt) + b * a.sdt[0] + h * a.sdt[1]) +
                    (a.dt_bias != nullptr ? a.dt_bias[h] : 0.0f);
   const float dl = a.softplus ? softplus(xr) : xr;
   const float decay = fast_exp2(dl * (-expf(a.A_log[h]) * kLog2e));
-  for (int p = threadIdx.x; p < cols; p += 256)
-    xs[p] = conv_step<IO>(a, b, slot, h * a.headdim + tile * kCols + p);
+  // a channel of B or C (2 N <= 256 of them) and the first of x a thread, with
+  // both on their way before either is filtered
+  const int k = threadIdx.x, which = k >= a.dstate ? 1 : 0;
+  const int cb = a.heads * a.headdim + (which * a.groups + g) * a.dstate + k - which * a.dstate;
+  const int cx = h * a.headdim + tile * kCols + k;
+  IO lb[4], lx[4];
+  if (k < 2 * a.dstate) conv_line(a, b, slot, cb, lb);
+  if (k < cols) conv_line(a, b, slot, cx, lx);
+  if (k < 2 * a.dstate) bc[which][k - which * a.dstate] = conv_filter(a, cb, lb);
+  if (k < cols) {
+    xs[k] = conv_filter(a, cx, lx);
+    conv_slide(a, slot, cx, lx);
+  }
+  if constexpr (kCols > 256) {
+    for (int p = k + 256; p < cols; p += 256) {
+      conv_line(a, b, slot, cx + p - k, lx);
+      xs[p] = conv_filter(a, cx + p - k, lx);
+      conv_slide(a, slot, cx + p - k, lx);
+    }
+  }
   __syncthreads();
+  float bn[4], cn[4];
+  load_part<float, 4>(&bc[0][min(n0, kMaxHeadState - 4)], nn, bn);
+  load_part<float, 4>(&bc[1][min(n0, kMaxHeadState - 4)], nn, cn);
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const int p = pl + k * RP;
@@ -149,15 +185,16 @@ hipError_t launch_lpr(const HeadStepArgs& a, hipStream_t stream) {
 
 template <typename IO>
 hipError_t launch_t(const HeadStepArgs& a, hipStream_t stream) {
+  hipError_t e;
+  if (a.dstate <= 16) e = launch_lpr<IO, 4>(a, stream);
+  else if (a.dstate <= 32) e = launch_lpr<IO, 8>(a, stream);
+  else if (a.dstate <= 64) e = launch_lpr<IO, 16>(a, stream);
+  else e = launch_lpr<IO, 32>(a, stream);
+  if (e != hipSuccess || a.width == 1) return e;
   const int bc = 2 * a.groups * a.dstate;
   const int64_t n = static_cast<int64_t>(a.rows) * bc;
-  head_step_conv_kernel<IO><<<dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream>>>(a, bc);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (a.dstate <= 16) return launch_lpr<IO, 4>(a, stream);
-  if (a.dstate <= 32) return launch_lpr<IO, 8>(a, stream);
-  if (a.dstate <= 64) return launch_lpr<IO, 16>(a, stream);
-  return launch_lpr<IO, 32>(a, stream);
+  head_step_slide_kernel<IO><<<dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream>>>(a, bc);
+  return hipGetLastError();
 }
 
 }  // namespace

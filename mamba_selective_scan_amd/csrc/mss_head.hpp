@@ -72,7 +72,6 @@ struct HeadStepArgs {
   float* state;
   void* window;
   void* out;
-  float* u;  // workspace [rows][2 G N]: the filtered B and C
 };
 
 struct NormArgs {

@@ -219,7 +219,7 @@ def head_scan_prompts(x, dt_raw, A_log, B, C, D=None, z=None, dt_bias=None, *, c
 
 
 def head_scan_step(state, window, xbc, dt_raw, A_log, weight, bias=None, D=None, z=None,
-                   dt_bias=None, *, slots=None, delta_softplus=True, out=None, workspace=None):
+                   dt_bias=None, *, slots=None, delta_softplus=True, out=None):
     """One token a row: the conv step with SiLU over all channels, then one step
     of the head-wise scan, ordered on torch's current stream.
 
@@ -260,13 +260,8 @@ def head_scan_step(state, window, xbc, dt_raw, A_log, weight, bias=None, D=None,
                    _vector(D, "D", heads, torch.float32, dev), *_optional(z),
                    _vector(dt_bias, "dt_bias", heads, torch.float32, dev),
                    _vector(slots, "slots", rows, torch.int32, dev),
-                   out.data_ptr(), *out.stride(), 1 if delta_softplus else 0, 0, 0, 0)
-    lib = _lib.lib()
-    st = ctypes.c_int(0)
-    need = lib.mss_head_scan_step_workspace_size(ctypes.byref(a), ctypes.byref(st))
-    _lib.check(st.value)
-    _give_workspace(a, need, workspace, dev)
-    _launch(lib.mss_head_scan_step, a, dev)
+                   out.data_ptr(), *out.stride(), 1 if delta_softplus else 0, 0)
+    _launch(_lib.lib().mss_head_scan_step, a, dev)
     return out
 
 

@@ -65,7 +65,7 @@ def step():
                window_stride=768 * 3, xbc=fake(2), xbc_stride=(768, 1), dt_raw=fake(3), dt_stride=(4, 1),
                A_log=fake(4), weight=fake(5), weight_stride=(4, 1), bias=fake(6), D=fake(7), z=fake(8),
                z_stride=(256, 64, 1), dt_bias=fake(9), slots=fake(10), out=fake(11), out_stride=(256, 64, 1),
-               delta_softplus=1, workspace=fake(12), workspace_bytes=1 << 30)
+               delta_softplus=1)
 
 
 def norm():
@@ -107,14 +107,14 @@ STRIDE = {
 }
 MISALIGNED = {
     "conv": [("x", 1), ("weight", 2), ("window", 1), ("cu_seqlens", 2), ("slots", 1), ("out", 1)],
-    "scan": [("x", 1), ("state", 8), ("cu_seqlens", 2), ("A_log", 2), ("workspace", 16), ("dt_bias", 1)],
-    "step": [("state", 4), ("window", 1), ("slots", 2), ("workspace", 128), ("xbc", 1)],
+    "scan": [("x", 1), ("state", 2), ("cu_seqlens", 2), ("A_log", 2), ("workspace", 16), ("dt_bias", 1)],
+    "step": [("state", 1), ("window", 1), ("slots", 2), ("bias", 2), ("xbc", 1)],
     "norm": [("x", 1), ("residual", 2), ("scale", 2), ("weight", 1)],
 }
 ALIAS = {
     "conv": [("out", 0), ("window", 7), ("out", 4), ("window", 1)],
     "scan": [("out", 0), ("out", 11), ("state", 6), ("out", 3), ("state", 10)],
-    "step": [("out", 2), ("out", 0), ("workspace", 0), ("window", 0), ("window", 8), ("workspace", 11)],
+    "step": [("out", 2), ("out", 0), ("window", 0), ("window", 8), ("state", 5), ("out", 10)],
     "norm": [("out", 0), ("scale", 3), ("residual_out", 0), ("residual_out", 3), ("scale", 1)],
 }
 
@@ -152,21 +152,32 @@ def test_other_refusals():
     refused("conv", "MSS_ERR_BAD_STRUCT", activation=7)
     refused("norm", "MSS_ERR_BAD_STRUCT", quant=3)
     refused("norm", "MSS_ERR_UNSUPPORTED_DTYPE", residual_dtype=5)
-    refused("step", "MSS_ERR_WORKSPACE_TOO_SMALL", workspace=None)
-    refused("step", "MSS_ERR_WORKSPACE_TOO_SMALL", workspace_bytes=3 * 512 * 4 - 1)
+    # 600 tokens of 4 heads are cut over time, and need room for the states between
+    refused("scan", "MSS_ERR_WORKSPACE_TOO_SMALL", tokens=600, workspace=None)
+    refused("scan", "MSS_ERR_WORKSPACE_TOO_SMALL", tokens=600, workspace_bytes=1 << 16)
+    refused("scan", "MSS_ERR_ALIASING", tokens=600, workspace=fake(11))
+    refused("scan", "MSS_ERR_ALIASING", tokens=600, workspace=fake(12))
     # views between which nothing overlaps but whose ranges interleave are
     # refused as well: the check is on ranges
     refused("norm", "MSS_ERR_ALIASING", out=fake(0) + 512, x_stride=1024, out_stride=2048)
 
 
 def test_workspace_sizes():
+    """From the sizes alone: none for a call of up to eight chunks, room for every
+    segment's state and decay otherwise."""
     lib, st = _lib.lib(), ctypes.c_int(0)
-    assert lib.mss_head_scan_step_workspace_size(ctypes.byref(step()), ctypes.byref(st)) == 3 * 512 * 4
-    assert st.value == 0
-    assert lib.mss_head_scan_step_workspace_size(ctypes.byref(put(step(), rows=0)), ctypes.byref(st)) == 0
-    assert st.value == _lib.STATUS_CODE["MSS_ERR_BAD_SHAPE"]
-    lib.mss_head_scan_prompts_workspace_size(ctypes.byref(put(scan(), dstate=0)), ctypes.byref(st))
-    assert st.value == _lib.STATUS_CODE["MSS_ERR_UNSUPPORTED_DSTATE"]
+
+    def size(**kw):
+        return lib.mss_head_scan_prompts_workspace_size(ctypes.byref(put(scan(), **kw)), ctypes.byref(st))
+
+    assert size() == 0 and st.value == 0
+    assert size(tokens=512) == 0
+    states = 4 * 64 * 128 * 4
+    for tokens in (513, 32768, 1 << 20):
+        # a cut prompt has segments of at least four chunks, but for its last
+        need = size(tokens=tokens)
+        assert states <= need <= (2 * tokens // 256) * (states + 16) + 256 and st.value == 0
+    assert size(dstate=0) == 0 and st.value == _lib.STATUS_CODE["MSS_ERR_UNSUPPORTED_DSTATE"]
 
 
 class _NoCalls:

@@ -182,7 +182,8 @@ def test_scan_is_causal_past_nan_and_infinity(mss, lens, at, io):
     args = lambda: (v["x"], v["dt_raw"], v["A_log"], v["B"], v["C"], v["D"], v["z"], v["dt_bias"])  # noqa: E731
     clean = mss.head_scan_prompts(*args(), cu_seqlens=c["cu"], state=c["state"].clone(), slots=c["slots"])
     for name, index, value in [("x", (at, 1, 3), float("nan")), ("x", (at, 1, 3), float("inf")),
-                               ("B", (at, 0, 5), float("-inf"))]:
+                               ("B", (at, 0, 5), float("-inf")), ("C", (at, 0, 5), float("inf")),
+                               ("dt_raw", (at, 0), float("nan"))]:
         kept = v[name].clone()
         v[name][index] = value
         state = c["state"].clone()
@@ -245,6 +246,41 @@ def test_scan_views(mss, io):
     out = randn(g, t, heads, headdim + 1, dtype=DT[io])[:, :, 1:]
     c["state"] = randn(g, 4, 3, heads, headdim, dstate)[:, 1]
     scan_check(mss, f"scan views {io}", v, c, out=out)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_caches_at_odd_addresses(mss, io):
+    """Entries of an odd number of elements, with others between them: states and
+    windows at any element."""
+    g = gen(17)
+    heads, headdim, dstate, groups = 3, 5, 7, 3
+    v, c = scan_inputs(g, (70, 9), heads, headdim, dstate, groups, io)
+    c["state"] = randn(g, 4, 3, heads, headdim, dstate)[:, 1]
+    scan_check(mss, f"scan odd entries {io}", v, c)
+    chans = heads * headdim + 2 * groups * dstate
+    state, window = c["state"], randn(g, 4, 3, chans, 3, dtype=DT[io])[:, 1]
+    xbc, dt_raw = randn(g, 2, chans, dtype=DT[io]), randn(g, 2, heads, dtype=DT[io])
+    weight = randn(g, chans, 4)
+    want, ws, ww, mag, smag = ref.step(state, window, xbc, dt_raw, v["A_log"], weight, None, None, None, None,
+                                       groups, c["slots"])
+    got = mss.head_scan_step(state, window, xbc, dt_raw, v["A_log"], weight, slots=c["slots"])
+    k = 1.21 * (2.2 * 12 + dstate + 8) * E
+    ref.within(f"step odd entries {io} out", got, want, k * mag + ref.HALF[DT[io]] * want.abs() * 1.01)
+    ref.within(f"step odd entries {io} state", state, ws, k * smag)
+    assert torch.equal(ref.d(window), ww)
+
+
+def test_offsets_outside_the_rules(mss):
+    """cu_seqlens that runs backwards, starts late or ends past the rows: results
+    of no meaning, rows and entries in their places."""
+    v, c = scan_inputs(gen(18), (400, 300, 500), 2, 64, 64, 1, "bf16")
+    x, w = randn(gen(18), 1200, 40), randn(gen(18), 40, 4)
+    for cu in ((0, 1200, 0, 1200), (-7, 700, 300, 5000), (5000, 5000, 5000, 5000), (30, 40, 1100, 1150)):
+        out = mss.head_scan_prompts(v["x"], v["dt_raw"], v["A_log"], v["B"], v["C"], cu_seqlens=ints(*cu),
+                                    state=c["state"], slots=c["slots"])
+        u = mss.causal_conv1d_prompts(x, w, cu_seqlens=ints(*cu), window=randn(gen(18), 5, 40, 3))
+        torch.cuda.synchronize()
+        assert out.shape == v["x"].shape and u.shape == x.shape
 
 
 def test_scan_skips_and_keeps(mss):
