@@ -533,7 +533,9 @@ typedef struct mss_conv_prompts_args {
     int32_t reserved0;           /* must be 0                                            */
 } mss_conv_prompts_args;
 
-/* Arguments of mss_head_scan_prompts.  Set struct_size = sizeof(mss_head_scan_args). */
+/* Arguments of mss_head_scan_prompts.  Set struct_size = sizeof(mss_head_scan_args).
+ * Token strides of x, B, C, z and out above 2^31 / 260 elements are refused
+ * (MSS_ERR_BAD_STRIDE): a tile of 64 tokens is addressed with 32 bits. */
 typedef struct mss_head_scan_args {
     uint32_t struct_size;
     int32_t io_dtype;            /* mss_dtype of x, dt_raw, z, B, C, out                 */

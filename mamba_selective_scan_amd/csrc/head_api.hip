@@ -221,8 +221,8 @@ mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
     return MSS_ERR_BAD_STRIDE;
   // 64 rows of a tile are addressed with 32-bit byte offsets
   constexpr int64_t kMaxRow = (int64_t{1} << 31) / (65 * 4);
-  if (a->x_stride[0] > kMaxRow || a->B_stride[0] > kMaxRow || a->C_stride[0] > kMaxRow ||
-      (a->z != nullptr && a->z_stride[0] > kMaxRow) || a->out_stride[0] > kMaxRow)
+  if (T > 1 && (a->x_stride[0] > kMaxRow || a->B_stride[0] > kMaxRow || a->C_stride[0] > kMaxRow ||
+                (a->z != nullptr && a->z_stride[0] > kMaxRow) || a->out_stride[0] > kMaxRow))
     return MSS_ERR_BAD_STRIDE;
   const int64_t xs[3] = {T, H, P}, ds[2] = {T, H}, bs[3] = {T, G, N};
   if (T > 0 && !non_overlapping(xs, a->out_stride, 3)) return MSS_ERR_BAD_STRIDE;
@@ -261,7 +261,8 @@ mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
   // and before the next one
   const int64_t V = 16 / es;
   auto vectors = [&](const void* p, const int64_t* st, int64_t outer, int64_t inner) {
-    return aligned(p, 16) && st[0] % V == 0 && st[0] >= inner && (outer == 1 || st[1] % V == 0) && inner % V == 0;
+    return aligned(p, 16) && st[0] % V == 0 && st[0] >= inner && st[0] <= kMaxRow &&
+           (outer == 1 || st[1] % V == 0) && inner % V == 0;
   };
   // 8 columns at a time leave the kernel, whatever the type
   k.vec = any && P % 8 == 0 && vectors(a->x, a->x_stride, H, P) && vectors(a->B, a->B_stride, G, N) &&

@@ -34,6 +34,18 @@
 // segment adds to a zero state, one composes the states entering the segments
 // (and the state the prompt leaves), and the walk then runs all segments at once.
 //
+// What bounds it: instructions.  A chunk of 64 tokens costs a wave 152 MFMAs of 16
+// cycles and 1200 VALU instructions (states of 128; counted); with two waves a SIMD
+// (two workgroups of 80 KB of LDS and 225 registers a CU) the SIMDs issue in 63% of
+// their cycles, and the waits between a chunk's products take most of the rest.
+// 80 heads of 64 x 128, 8 x 4096 tokens in bf16: 549 us, 157 TFLOP/s of the 4 P N a
+// token that the recurrence needs; 24 heads, one prompt of 32768: 199 us (walk 132,
+// sums 67, states between 15 in a profile); 200 tokens of 24 heads: 28 us, four
+// chunks one after the other.  Measured and not kept: three waves a SIMD for the
+// sums (same time); two parts for the addends of states that only outputs read (one
+// long prompt 4% faster, a short one 4% slower); steps left to the compiler's
+// schedule, without the barriers between them (4% at most).
+//
 // A chunk that holds an infinity or a NaN in x, B or C is walked token by token
 // (0 times one in x would reach tokens before it, splitting loses an infinity, and
 // infinities of both signs would meet in a sum that the recurrence does not form).

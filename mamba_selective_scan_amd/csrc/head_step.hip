@@ -13,6 +13,9 @@
 // of x slide there, where they have their only reader; those of B and C, which
 // every head of the group reads, in a second small launch.  (Filtering B and C
 // once for all heads, in a launch before, took a workspace and the same time.)
+// 128 rows of 80 heads of 64 x 128 in bf16: 139 us for the two, 4.8 TB/s, where a
+// copy reaches 5.1; one row of 24 heads: 6.6 us, bound by the two launches and the
+// chain from the windows to the outputs.
 #include "mss_head.hpp"
 
 namespace mss {
@@ -171,7 +174,12 @@ template <typename IO, int LPR>
 hipError_t launch_lpr(const HeadStepArgs& a, hipStream_t stream) {
   constexpr int RP = 256 / LPR;
   const int passes = (a.headdim + RP - 1) / RP;
-  const int np = passes >= 8 ? 8 : passes >= 4 ? 4 : passes >= 2 ? 2 : 1;
+  int np = passes >= 8 ? 8 : passes >= 4 ? 4 : passes >= 2 ? 2 : 1;
+  // fewer workgroups than CUs: smaller tiles, so that the states come through more
+  // of them (one row of 24 heads of 64 x 128 in a graph: 6.6 us, 7.5 us at eight
+  // columns a thread); more workgroups than that only filter B and C more often
+  // (8 rows of 80 heads: 10.9 us at 640 workgroups, 11.3 us at 1280)
+  while (np > 1 && static_cast<int64_t>(a.rows) * a.heads * ((passes + np - 1) / np) < 256) np /= 2;
   const int ptiles = (passes + np - 1) / np;
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.rows) * a.heads * ptiles)), block(256);
   switch (np) {

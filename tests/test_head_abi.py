@@ -99,7 +99,9 @@ STRIDE = {
              dict(weight_stride=(-4, 1))],
     "scan": [dict(x_stride=(256, 64, 2)), dict(out_stride=(256, 63, 1)), dict(z_stride=(256, 1, 64)),
              dict(B_stride=(256, 1, 2)), dict(C_stride=(256, -128, 1)), dict(state_stride=4 * 64 * 128 - 4),
-             dict(dt_stride=(-4, 1))],
+             dict(dt_stride=(-4, 1)), dict(x_stride=((1 << 31) // 260 + 1, 64, 1)),
+             dict(B_stride=(1 << 24, 128, 1)), dict(C_stride=(1 << 24, 128, 1)),
+             dict(z_stride=(1 << 24, 64, 1)), dict(out_stride=(1 << 24, 64, 1))],
     "step": [dict(xbc_stride=(-1, 1)), dict(out_stride=(255, 64, 1)), dict(state_stride=100),
              dict(window_stride=768), dict(z_stride=(1, -1, 1))],
     "norm": [dict(x_stride=-1), dict(out_stride=255), dict(residual_out_stride=100),

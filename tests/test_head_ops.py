@@ -249,6 +249,16 @@ def test_scan_views(mss, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_one_token_has_any_row_stride(mss, io):
+    """The token stride of a single token means nothing, however large."""
+    v, c = scan_inputs(gen(21), (1,), 2, 64, 64, 1, io)
+    for name in ("x", "B", "C", "z"):
+        shape = v[name].shape
+        v[name] = v[name].as_strided(shape, (1 << 24, shape[2], 1))
+    scan_check(mss, f"scan one token {io}", v, c)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_caches_at_odd_addresses(mss, io):
     """Entries of an odd number of elements, with others between them: states and
     windows at any element."""
