@@ -72,20 +72,29 @@ mss_status check_scan_shape(const mss_head_scan_args* a) {
   return check_head_shape(a->heads, a->headdim, a->dstate, a->groups);
 }
 
-// How a head-wise scan is cut over time: prompts longer than seg_len run as
-// segments, so that a few long prompts still fill the card.  From the sizes
-// alone: the prompts' lengths stay on the device.
+// How a head-wise scan is cut over time and over columns: prompts longer than
+// seg_len run as segments, so that a few long prompts still fill the card, and
+// tiles of 16 columns take the place of 32 while there are too few of those.
+// From the sizes alone: the prompts' lengths stay on the device.
 //
 // One long prompt wants as many segments as workgroups can run at once and not
 // one more (24 heads of 64 x 128, 32768 tokens in bf16: 191 us at 480 workgroups
-// of 512, 234 us at 516).  Segments shorter than four chunks spend more on the
-// states between them than they gain (one prompt of 4096: 61 us at 256 tokens,
-// 80 us at 64); a call of up to eight chunks is not cut at all (200 tokens:
-// 29 us whole, 35 us in segments of 64).  Longer than kSegMax, a batch of equal
-// prompts does not care (8 x 4096 tokens of 80 heads: 528 us whole, 535 us at
-// 1024) while one of unequal prompts would wait for its longest (24 prompts,
-// 32768 tokens: 571 us at 1024, 622 us at 2560).
+// of 512, 234 us at 516; a prompt's last segment counts as half a one).  A cut
+// call makes three passes: it takes more than five chunks to be worth it (320
+// tokens: 25.9 us whole, 28.3 us cut; 512: 38 and 30), on the average of the
+// prompts, as the lengths are not known here; then segments may be as short as
+// two chunks (2048 tokens: 43 us at 128 tokens a segment, 57 us at 256).  Longer
+// than kSegMax, a batch of equal prompts does not care (8 x 4096 tokens of 80
+// heads: 528 us whole, 535 us at 1024) while one of unequal prompts would wait for
+// its longest (24 prompts, 32768 tokens: 571 us at 1024, 622 us at 2560).
+//
+// Tiles of 16 columns do a chunk in two thirds of the time but form its decays
+// twice: for calls that leave a quarter of the workgroup slots empty at 32 (200
+// tokens of 24 heads: 21.8 us, 27.9 us at 32; 1000 tokens of 80 heads: 49 and 54;
+// 2000 tokens of 80 heads, over that line: 74 and 69) and still run at once (8 x 200
+// tokens of 80 heads, which do not: 55 and 49).
 struct HeadScanPlan {
+  bool narrow = false;
   int64_t ptiles, tiles, seg_len = 0, cut_slots = 0, cut_prompts = 0;
   size_t parts = 0, workspace = 0;
 };
@@ -94,16 +103,24 @@ constexpr int64_t kSegMax = 1024;
 
 HeadScanPlan head_scan_plan(const mss_head_scan_args* a) {
   HeadScanPlan p;
-  p.ptiles = (a->headdim + 31) / 32;
-  p.tiles = a->groups * ((a->heads / a->groups * p.ptiles + 3) / 4);
   const bool f32 = a->io_dtype == MSS_F32;
   const int64_t chunk = f32 ? 32 : 64;
   // workgroups a CU holds (by LDS and registers): three of the small fp32 kernels
   const int64_t slots = kCus * (f32 && a->dstate <= 64 ? 3 : 2);
-  const int64_t want = std::max<int64_t>(1, slots / p.tiles);
-  int64_t seg = ((a->tokens + want - 1) / want + chunk - 1) / chunk * chunk;
-  seg = std::clamp(seg, 4 * chunk, kSegMax);
-  if (a->tokens > 8 * chunk) {
+  int64_t seg = 0;
+  // the tiles of `cols` columns and their segments; returns the workgroups
+  auto tile = [&](int64_t cols) {
+    p.ptiles = (a->headdim + cols - 1) / cols;
+    p.tiles = a->groups * ((a->heads / a->groups * p.ptiles + 3) / 4);
+    const int64_t room = slots / p.tiles;
+    const int64_t want = std::max<int64_t>({1, room / 2, room - a->seqs / 2});
+    seg = ((a->tokens + want - 1) / want + chunk - 1) / chunk * chunk;
+    seg = std::clamp(seg, (a->tokens > 5 * chunk * a->seqs ? 2 : 5) * chunk, kSegMax);
+    return std::max(a->seqs, a->tokens / seg + a->seqs / 2) * p.tiles;
+  };
+  p.narrow = tile(32) < slots / 4 * 3 && tile(16) <= slots;
+  if (!p.narrow) tile(32);
+  if (a->tokens > seg) {
     // a cut prompt has more than seg tokens, so at most 2 len / seg segments
     p.seg_len = seg;
     p.cut_slots = 2 * a->tokens / seg;
@@ -268,7 +285,8 @@ mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
   k.vec = any && P % 8 == 0 && vectors(a->x, a->x_stride, H, P) && vectors(a->B, a->B_stride, G, N) &&
           vectors(a->C, a->C_stride, G, N) && vectors(a->out, a->out_stride, H, P) &&
           (a->z == nullptr || vectors(a->z, a->z_stride, H, P));
-  k.ptiles = static_cast<int>(plan.ptiles);
+  k.narrow = k.vec && plan.narrow;
+  k.ptiles = static_cast<int>(plan.narrow && !k.vec ? (P + 31) / 32 : plan.ptiles);
   k.seg_len = static_cast<int>(plan.seg_len);
   k.cut_slots = static_cast<int>(plan.cut_slots);
   k.cut_prompts = static_cast<int>(plan.cut_prompts);

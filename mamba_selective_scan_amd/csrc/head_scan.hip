@@ -8,7 +8,8 @@
 // which are matrix products: C B^T (shared by the heads of a group), its decayed
 // lower triangle with x, C with the entering state, and x with B.
 //
-// A wave walks one head's tile of 32 columns p chunk by chunk, with the state in
+// A wave walks one head's tile of 32 columns p (16 in calls with few tiles) chunk
+// by chunk, with the state in
 // MFMA accumulators; a workgroup's four waves are tiles of one group, which
 // share the chunk's B and C in LDS and form C B^T together.  Every product is
 // laid out so that one product's accumulators are the next one's operand:
@@ -38,9 +39,9 @@
 // cycles and 1200 VALU instructions (states of 128; counted); with two waves a SIMD
 // (two workgroups of 80 KB of LDS and 225 registers a CU) the SIMDs issue in 63% of
 // their cycles, and the waits between a chunk's products take most of the rest.
-// 80 heads of 64 x 128, 8 x 4096 tokens in bf16: 549 us, 157 TFLOP/s of the 4 P N a
-// token that the recurrence needs; 24 heads, one prompt of 32768: 199 us (walk 132,
-// sums 67, states between 15 in a profile); 200 tokens of 24 heads: 28 us, four
+// 80 heads of 64 x 128, 8 x 4096 tokens in bf16: 538 us, 160 TFLOP/s of the 4 P N a
+// token that the recurrence needs; 24 heads, one prompt of 32768: 193 us (walk 132,
+// sums 67, states between 15 in a profile); 200 tokens of 24 heads: 22 us, four
 // chunks one after the other.  Measured and not kept: three waves a SIMD for the
 // sums (same time); two parts for the addends of states that only outputs read (one
 // long prompt 4% faster, a short one 4% slower); steps left to the compiler's
@@ -55,7 +56,7 @@ namespace mss {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kCols = 32;  // columns p of a wave's tile
+constexpr int kCols = 32;  // columns of x in LDS; a wave's tile of columns p is these or the first 16
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -149,6 +150,11 @@ struct Tile {
     if constexpr (sizeof(IO) == 2) return offset(8 * g + ((c >> 2) & 1) + ((c >> 1) & 4), c & 3);
     return offset(8 * g, 2 * (c >> 2)) + 4 * (c & 3);
   }
+  // (of a tile of 16 columns: the lane's column is c)
+  __device__ static inline int lane_col16(int g, int c) {
+    if constexpr (sizeof(IO) == 2) return offset(8 * g + ((c >> 2) & 1) + ((c >> 1) & 4), (c & 3) >> 1) + 8 * (c & 1);
+    return offset(8 * g, c >> 2) + 4 * (c & 3);
+  }
   __device__ static inline Frag<IO> col(const char* t, int lane, int ks, int q, int half) {
     Frag<IO> f;
     if constexpr (sizeof(IO) == 2) {
@@ -201,10 +207,12 @@ __device__ inline u32x4 buf_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// 8 elements as they lie in memory (16 or 32 bytes), as fp32, and back.
-template <typename IO>
-struct Raw8 {
-  u32x4 v[sizeof(IO) / 2];
+// E (4 or 8) elements as they lie in memory, as fp32, and back.
+template <typename IO, int E>
+struct Raw {
+  static constexpr int kWords = E * static_cast<int>(sizeof(IO)) / 4, kW = kWords < 4 ? kWords : 4, kV = kWords / kW;
+  typedef uint32_t vec __attribute__((ext_vector_type(kW)));
+  vec v[kV];
   __device__ inline float get(int e) const {
     if constexpr (sizeof(IO) == 2)
       return __uint_as_float(e & 1 ? v[0][e / 2] & 0xffff0000u : v[0][e / 2] << 16);
@@ -214,10 +222,28 @@ struct Raw8 {
   __device__ inline void set(const float* f) {
     if constexpr (sizeof(IO) == 2) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[0][i] = bf16x2_bits(f[2 * i], f[2 * i + 1]);
+      for (int i = 0; i < E / 2; ++i) v[0][i] = bf16x2_bits(f[2 * i], f[2 * i + 1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i / 4][i & 3] = __float_as_uint(f[i]);
+      for (int i = 0; i < E; ++i) v[i / 4][i & 3] = __float_as_uint(f[i]);
+    }
+  }
+  __device__ inline void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      if constexpr (kW == 4)
+        v[i] = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16 * i, 0, 0));
+      else
+        v[i] = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    }
+  }
+  __device__ inline void store(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      if constexpr (kW == 4)
+        __builtin_amdgcn_raw_buffer_store_b128(v[i], r, off + 16 * i, 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b64(v[i], r, off, 0, 0);
     }
   }
 };
@@ -386,7 +412,8 @@ struct Shape {
 
 // AGG: only what a segment adds to a zero state, and its decay.  VEC: rows are
 // whole 16-byte vectors (else element by element at their ends).
-template <typename IO, int NP, int Q, bool AGG, bool VEC>
+// NT: accumulator tiles over a wave's columns, 16 each.
+template <typename IO, int NP, int Q, int NT, bool AGG, bool VEC>
 __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   using S = Shape<IO, NP, Q>;
   using BC = typename S::BC;
@@ -396,8 +423,10 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   constexpr int kK = NP / 32;                          // K-steps over the states
   constexpr int kT = Q / 32;                           // K-steps over the tokens
   constexpr int kLoadBC = Q * BC::kChunks / 256;       // 16-byte loads a thread
-  constexpr int kLoadX = Q * X::kChunks / 64;          // 16-byte loads a lane
-  constexpr int kRowsBC = 256 / BC::kChunks, kRowsX = 64 / X::kChunks;  // rows between them
+  constexpr int kChunksX = NT * kES;                   // 16-byte chunks of a row of x
+  constexpr int kLoadX = Q * kChunksX / 64;            // 16-byte loads a lane
+  constexpr int kRowsBC = 256 / BC::kChunks, kRowsX = 64 / kChunksX;  // rows between them
+  constexpr int kOut = 4 * NT;                         // columns of a token that a lane writes
   using Lds = std::conditional_t<AGG, typename S::Sum, typename S::Walk>;
   __shared__ __attribute__((aligned(16))) Lds lds;
 
@@ -432,25 +461,27 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 
   const bool on = job < jobs;
   const int h = grp * (a.heads / a.groups) + (on ? job / a.ptiles : 0);
-  const int p0 = (on ? job % a.ptiles : 0) * kCols;
+  const int p0 = (on ? job % a.ptiles : 0) * 16 * NT;
   const int pc = on ? a.headdim - p0 : 0;              // this tile's columns
   const int64_t hp = static_cast<int64_t>(h) * a.headdim + p0;
   float* cache = a.state + slot * a.sstate + hp * a.dstate;
   float* part = cut ? a.parts + (static_cast<int64_t>(w.index) * a.heads * a.headdim + hp) * a.dstate : nullptr;
 
-  // the state: tile [n = 32 q + 8 g + 4 tn + r][p = 8 (c / 4) + c % 4 + 4 tp]
-  f32x4 st[kK][2][2];
+  // the state: tile [n = 32 q + 8 g + 4 tn + r][p = 8 (c / 4) + c % 4 + 4 tp], or p = c
+  f32x4 st[kK][2][NT];
+  auto column = [](int th) { return NT == 2 ? 8 * ((th >> 2) & 3) + (th & 3) : th & 15; };
+  auto lane_colx = [](int g, int c) { return NT == 2 ? X::lane_col(g, c) : X::lane_col16(g, c); };
   // where this tile's state lies in memory: what a cut prompt's segment enters
   // with or adds, or the prompt's cache entry
   float* home = cut ? part : cache;
   auto state_in = [&](bool from) __attribute__((always_inline)) {
     const int th = thread_anew(), n0 = 8 * ((th >> 4) & 3), N = anew(a.dstate);
-    const float* at = home + static_cast<int64_t>(8 * ((th >> 2) & 3) + (th & 3)) * N + n0;
-    const int ps = pc - 8 * ((th >> 2) & 3) - (th & 3);
+    const float* at = home + static_cast<int64_t>(column(th)) * N + n0;
+    const int ps = pc - column(th);
 #pragma unroll
     for (int q = 0; q < kK; ++q)
 #pragma unroll
-      for (int tp = 0; tp < 2; ++tp) {
+      for (int tp = 0; tp < NT; ++tp) {
         float v[8] = {};
         if (from) load_part<float, 8>(at + 4 * tp * N + 32 * q, 4 * tp < ps ? N - n0 - 32 * q : 0, v);
 #pragma unroll
@@ -460,12 +491,12 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   };
   auto state_out = [&]() __attribute__((always_inline)) {
     const int th = thread_anew(), n0 = 8 * ((th >> 4) & 3), N = anew(a.dstate);
-    float* at = home + static_cast<int64_t>(8 * ((th >> 2) & 3) + (th & 3)) * N + n0;
-    const int ps = pc - 8 * ((th >> 2) & 3) - (th & 3);
+    float* at = home + static_cast<int64_t>(column(th)) * N + n0;
+    const int ps = pc - column(th);
 #pragma unroll
     for (int q = 0; q < kK; ++q)
 #pragma unroll
-      for (int tp = 0; tp < 2; ++tp) {
+      for (int tp = 0; tp < NT; ++tp) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = st[q][e >> 2][tp][e & 3];
@@ -492,7 +523,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     const int th = thread_anew();
     // this thread's chunks of B and C, and this lane's of x: row and column of the first
     const int rb = th / BC::kChunks, nb = th % BC::kChunks * kE;
-    const int rx = (th & 63) / X::kChunks, nx = (th & 63) % X::kChunks * kE;
+    const int rx = (th & 63) / kChunksX, nx = (th & 63) % kChunksX * kE;
     if constexpr (VEC) {
       // byte offsets from the chunk's first row (a tile spans less than 2 GiB)
       const int eX = static_cast<int>(a.sx[0]) * kES, eB = static_cast<int>(a.sB[0]) * kES;
@@ -593,7 +624,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     uint32_t odd = 0;
     const int th = thread_anew();
     const int wB = BC::offset(th / BC::kChunks, th % BC::kChunks);
-    const int wX = X::offset((th & 63) / X::kChunks, (th & 63) % X::kChunks);
+    const int wX = X::offset((th & 63) / kChunksX, (th & 63) % kChunksX);
 #pragma unroll
     for (int i = 0; i < kLoadBC; ++i) {
       *reinterpret_cast<u32x4*>(lds.b + wB + i * kRowsBC * BC::kRow) = pb[i];
@@ -622,7 +653,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     }
     const auto& m = lds.time[par][wave];
 
-    f32x4 y[AGG ? 1 : Q / 16][2];
+    f32x4 y[AGG ? 1 : Q / 16][NT];
     if constexpr (!AGG) {
       const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, lane = th & 63;
       const int lrow = BC::lane_row(c, g);
@@ -638,7 +669,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       // ---- S C^T: the state's fragments each serve every tile of tokens
 #pragma unroll
       for (int q = 0; q < kK; ++q) {
-        Frag<IO> sb[2], cf[Q / 16];
+        Frag<IO> sb[NT], cf[Q / 16];
 #pragma unroll
         for (int it = 0; it < Q / 16; ++it) cf[it] = BC::row(lds.c, lrow, 16 * it, q);
         const Frag<IO> b = BC::row(lds.b, lju, 0, q);
@@ -657,13 +688,13 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
           acc[0] = mma(b, wave >= 2 ? cf[1] : cf[0], q == 0 ? f32x4{0, 0, 0, 0} : acc[0]);
         }
 #pragma unroll
-        for (int tp = 0; tp < 2; ++tp)
+        for (int tp = 0; tp < NT; ++tp)
 #pragma unroll
           for (int e = 0; e < 8; e += 2) sb[tp].set2(e, st[q][e >> 2][tp][e & 3], st[q][e >> 2][tp][(e & 3) + 1]);
 #pragma unroll
         for (int it = 0; it < Q / 16; ++it)
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp) y[it][tp] = mma(sb[tp], cf[it], q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
+          for (int tp = 0; tp < NT; ++tp) y[it][tp] = mma(sb[tp], cf[it], q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
       }
       // an infinity or a NaN in B or C is one in C B^T
       uint32_t top = 0;
@@ -687,31 +718,30 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     if constexpr (!AGG) {
       {
         const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, lane = th & 63;
-        const int lx = X::lane_row(c, g), lxc = X::lane_col(g, c);
+        const int lxc = lane_colx(g, c);
+        const int lx = X::offset(c, kOut * g / kE) + kOut * g % kE * kES;  // columns kOut g of token c
         // the gate, on its way while the chunk's own tokens are added
-        Raw8<IO> z[VEC ? Q / 16 : 1];
+        Raw<IO, kOut> z[VEC ? Q / 16 : 1];
         if constexpr (VEC) {
           const int eZ = static_cast<int>(a.sz[0]) * kES;
           const auto rZ = rows_of(zw, gate ? min(end - t, Q) : 0, eZ);
-          uint32_t o = 8 * g < pc ? c * eZ + 8 * g * kES : kOffNone;
+          uint32_t o = kOut * g < pc ? c * eZ + kOut * g * kES : kOffNone;
 #pragma unroll
-          for (int it = 0; it < Q / 16; ++it, o += 16 * eZ)
-#pragma unroll
-            for (int v = 0; v < kES / 2; ++v) z[it].v[v] = buf_load16(rZ, o + 16 * v);
+          for (int it = 0; it < Q / 16; ++it, o += 16 * eZ) z[it].load(rZ, o);
         }
 #pragma unroll
         for (int it = 0; it < Q / 16; ++it) {
           const float ei = m.enter[16 * it + c];
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp) y[it][tp] *= ei;
+          for (int tp = 0; tp < NT; ++tp) y[it][tp] *= ei;
         }
         step_end();
         // the chunk's own tokens
 #pragma unroll
         for (int ks = 0; ks < kT; ++ks) {
-          Frag<IO> xt[2];
+          Frag<IO> xt[NT];
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
+          for (int tp = 0; tp < NT; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
           constexpr int kIt = Q / 16;
           Frag<IO> w[kIt];
           float row[kIt];
@@ -746,50 +776,51 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2) w[it].set2(e, v[e], v[e + 1]);
           }
-          f32x4 u[kIt][2];
+          f32x4 u[kIt][NT];
 #pragma unroll
           for (int it = 2 * ks; it < kIt; ++it)
 #pragma unroll
-            for (int tp = 0; tp < 2; ++tp) u[it][tp] = mma(xt[tp], w[it], f32x4{0, 0, 0, 0});
+            for (int tp = 0; tp < NT; ++tp) u[it][tp] = mma(xt[tp], w[it], f32x4{0, 0, 0, 0});
 #pragma unroll
           for (int it = 2 * ks; it < kIt; ++it)
 #pragma unroll
-            for (int tp = 0; tp < 2; ++tp)
+            for (int tp = 0; tp < NT; ++tp)
 #pragma unroll
               for (int r = 0; r < 4; ++r) y[it][tp][r] = fmaf(row[it], u[it][tp][r], y[it][tp][r]);
           step_end();
         }
         const int eO = static_cast<int>(a.so[0]) * kES;
         const auto rO = rows_of(ow, min(end - t, Q), eO);
-        uint32_t to = 8 * g < pc ? c * eO + 8 * g * kES : kOffNone;
+        uint32_t to = kOut * g < pc ? c * eO + kOut * g * kES : kOffNone;
 #pragma unroll
         for (int it = 0; it < Q / 16; ++it) {
           const int i = 16 * it + c;
-          // ---- skip, gate, out: lane holds token i, columns 8 g .. 8 g + 7
-          const Frag<IO> xi = X::row(lds.x[wave], lx, 16 * it, 0);
-          float o[8];
+          // ---- skip, gate, out: lane holds token i, columns kOut g .. kOut g + kOut - 1
+          Raw<IO, kOut> xi;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf(skip, xi.get(e), y[it][e >> 2][e & 3]);
+          for (int k = 0; k < xi.kV; ++k)
+            xi.v[k] = *reinterpret_cast<const typename Raw<IO, kOut>::vec*>(lds.x[wave] + (lx ^ 16 * k) + 16 * it * X::kRow);
+          float o[kOut];
+#pragma unroll
+          for (int e = 0; e < kOut; ++e) o[e] = fmaf(skip, xi.get(e), y[it][e >> 2][e & 3]);
           if constexpr (VEC) {
             if (gate) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= silu(z[it].get(e));
+              for (int e = 0; e < kOut; ++e) o[e] *= silu(z[it].get(e));
             }
-            Raw8<IO> u;
+            Raw<IO, kOut> u;
             u.set(o);
-#pragma unroll
-            for (int k = 0; k < kES / 2; ++k)
-              __builtin_amdgcn_raw_buffer_store_b128(u.v[k], rO, to + 16 * k, 0, 0);
+            u.store(rO, to);
             to += 16 * eO;
           } else {
-            const int n = t + i < end ? pc - 8 * g : 0;
+            const int n = t + i < end ? pc - kOut * g : 0;
             if (gate) {
-              float zz[8];
-              load_part<IO, 8>(zw + i * a.sz[0] + 8 * g, n, zz);
+              float zz[kOut];
+              load_part<IO, kOut>(zw + i * a.sz[0] + kOut * g, n, zz);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= silu(zz[e]);
+              for (int e = 0; e < kOut; ++e) o[e] *= silu(zz[e]);
             }
-            store_part<IO, 8>(ow + i * a.so[0] + 8 * g, n, o);
+            store_part<IO, kOut>(ow + i * a.so[0] + kOut * g, n, o);
           }
           step_end();
         }
@@ -806,23 +837,23 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     // ---- the state
     {
       const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4;
-      const int lcol = BC::lane_col(g, c), lxc = X::lane_col(g, c);
+      const int lcol = BC::lane_col(g, c), lxc = lane_colx(g, c);
 #pragma unroll
       for (int q = 0; q < kK; ++q)
 #pragma unroll
         for (int tn = 0; tn < 2; ++tn)
 #pragma unroll
-          for (int tp = 0; tp < 2; ++tp) st[q][tn][tp] *= dec;
+          for (int tp = 0; tp < NT; ++tp) st[q][tn][tp] *= dec;
 #pragma unroll
       for (int ks = 0; ks < kT; ++ks) {
         constexpr int kParts = sizeof(IO) == 2 ? 3 : 1;
-        Frag<IO> xt[2], v[2][kParts];
+        Frag<IO> xt[NT], v[NT][kParts];
 #pragma unroll
-        for (int tp = 0; tp < 2; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
+        for (int tp = 0; tp < NT; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
         const float* left = m.left + 32 * ks + 8 * g;
         const f32x4 l0 = *reinterpret_cast<const f32x4*>(left), l1 = *reinterpret_cast<const f32x4*>(left + 4);
 #pragma unroll
-        for (int tp = 0; tp < 2; ++tp)
+        for (int tp = 0; tp < NT; ++tp)
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             float r0 = xt[tp].get(e) * (tok(e) < 4 ? l0[tok(e) & 3] : l1[tok(e) & 3]);
@@ -844,7 +875,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
             for (int tn = 0; tn < 2; ++tn)
 #pragma unroll
-              for (int tp = 0; tp < 2; ++tp) st[q][tn][tp] = mma(bt[tn], v[tp][k], st[q][tn][tp]);
+              for (int tp = 0; tp < NT; ++tp) st[q][tn][tp] = mma(bt[tn], v[tp][k], st[q][tn][tp]);
         }
         step_end();
       }
@@ -860,12 +891,12 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       // ---- token by token, the state in memory: nothing of this may take
       // registers from the products
       state_out();
-      const int th = thread_anew(), c = th & 15, g = (th & 63) >> 4, N = anew(a.dstate);
+      const int th = thread_anew(), g = (th & 63) >> 4, N = anew(a.dstate);
 #pragma unroll 1
       for (int i = 0; i < Q && t + i < end; ++i) {
         const float dti = m.delta[i], e = fast_exp2(dti * rate);
 #pragma unroll 1
-        for (int p = 8 * (c >> 2) + (c & 3), tp = 0; tp < 2; ++tp, p += 4) {
+        for (int p = column(th), tp = 0; tp < NT; ++tp, p += 4) {
           const float x = io_traits<IO>::load(reinterpret_cast<const IO*>(lds.x[wave] + X::offset(i, p / kE)) + p % kE);
           float y = 0.0f;
 #pragma unroll 1
@@ -955,23 +986,24 @@ __global__ __launch_bounds__(256) void head_scan_carry_kernel(HeadScanArgs a, in
   }
 }
 
-template <typename IO, int NP, int Q, bool VEC>
+template <typename IO, int NP, int Q, int NT, bool VEC>
 hipError_t launch_v(const HeadScanArgs& a, hipStream_t stream) {
   const int64_t tiles = static_cast<int64_t>(a.groups) * ((a.heads / a.groups * a.ptiles + kWaves - 1) / kWaves);
   if (a.cut_slots > 0) {
-    head_scan_kernel<IO, NP, Q, true, VEC><<<dim3(static_cast<unsigned>(a.cut_slots * tiles)), 256, 0, stream>>>(a);
+    head_scan_kernel<IO, NP, Q, NT, true, VEC><<<dim3(static_cast<unsigned>(a.cut_slots * tiles)), 256, 0, stream>>>(a);
     const int64_t blocks = (static_cast<int64_t>(a.heads) * a.headdim * a.dstate + 1023) / 1024;
     head_scan_carry_kernel<<<dim3(static_cast<unsigned>(blocks * a.cut_prompts)), 256, 0, stream>>>(
         a, static_cast<int>(blocks));
   }
-  head_scan_kernel<IO, NP, Q, false, VEC>
+  head_scan_kernel<IO, NP, Q, NT, false, VEC>
       <<<dim3(static_cast<unsigned>((a.cut_slots + a.q.seqs) * tiles)), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <typename IO, int NP, int Q>
 hipError_t launch_n(const HeadScanArgs& a, hipStream_t stream) {
-  return a.vec ? launch_v<IO, NP, Q, true>(a, stream) : launch_v<IO, NP, Q, false>(a, stream);
+  if (!a.vec) return launch_v<IO, NP, Q, 2, false>(a, stream);
+  return a.narrow ? launch_v<IO, NP, Q, 1, true>(a, stream) : launch_v<IO, NP, Q, 2, true>(a, stream);
 }
 
 // Chunks of 64 tokens in bf16 and 32 in fp32, whose tiles are twice as wide.

@@ -49,7 +49,8 @@ struct HeadScanArgs {
   float* state;
   void* out;
   int vec;          // rows of x, B, C, z and out are whole aligned 16-byte vectors
-  int ptiles;       // 32-column tiles of a head
+  int narrow;       // tiles of 16 columns (vec only), not 32
+  int ptiles;       // tiles of a head
   int seg_len;      // longer prompts are cut into segments of at most this many tokens (0: none is)
   int cut_slots;    // room for the segments of all cut prompts
   int cut_prompts;  // at most this many prompts are cut

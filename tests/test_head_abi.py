@@ -165,7 +165,7 @@ def test_other_refusals():
 
 
 def test_workspace_sizes():
-    """From the sizes alone: none for a call of up to eight chunks, room for every
+    """From the sizes alone: none for a call of up to five chunks, room for every
     segment's state and decay otherwise."""
     lib, st = _lib.lib(), ctypes.c_int(0)
 
@@ -173,12 +173,16 @@ def test_workspace_sizes():
         return lib.mss_head_scan_prompts_workspace_size(ctypes.byref(put(scan(), **kw)), ctypes.byref(st))
 
     assert size() == 0 and st.value == 0
-    assert size(tokens=512) == 0
+    assert size(tokens=320) == 0 and size(tokens=320, seqs=1) == 0
+    assert size(tokens=160, io_dtype=0) == 0
     states = 4 * 64 * 128 * 4
-    for tokens in (513, 32768, 1 << 20):
-        # a cut prompt has segments of at least four chunks, but for its last
-        need = size(tokens=tokens)
-        assert states <= need <= (2 * tokens // 256) * (states + 16) + 256 and st.value == 0
+    for tokens in (321, 513, 32768, 1 << 20):
+        # a cut prompt has segments of at least two chunks, but for its last; of
+        # five where the prompts are shorter than that on the average
+        for seqs in (1, 3):
+            least = 128 if tokens > 320 * seqs else 320
+            need = size(tokens=tokens, seqs=seqs)
+            assert states <= need <= (2 * tokens // least) * (states + 16) + 256 and st.value == 0
     assert size(dstate=0) == 0 and st.value == _lib.STATUS_CODE["MSS_ERR_UNSUPPORTED_DSTATE"]
 
 

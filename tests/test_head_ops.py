@@ -172,7 +172,8 @@ def test_scan_cut_over_time(mss, lens, heads, headdim, dstate, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
-@pytest.mark.parametrize("lens,at", [((100,), 37), ((700, 40), 300)])
+@pytest.mark.parametrize("lens,at", [((100,), 37), ((700, 40), 300), ((100,) + (0,) * 600, 37),
+                                     ((700, 40) + (0,) * 600, 300)], ids=lambda v: str(v)[:12])
 def test_scan_is_causal_past_nan_and_infinity(mss, lens, at, io):
     """What follows an infinity or a NaN in x or B is what the recurrence gives;
     what comes before it is as without it."""
@@ -207,6 +208,48 @@ def test_scan_is_causal_past_nan_and_infinity(mss, lens, at, io):
 def test_scan_shapes(mss, heads, headdim, dstate, groups, io):
     v, c = scan_inputs(gen(2), (70, 1, 131), heads, headdim, dstate, groups, io)
     scan_check(mss, f"scan H={heads} P={headdim} N={dstate} G={groups} {io}", v, c)
+
+
+def crowd(lens, heads, headdim, groups):
+    """With so many empty prompts that the call's workgroups, four tiles of 32
+    columns each, fill the card: it keeps those tiles, where a small call takes
+    tiles of 16."""
+    tiles = groups * -(-heads // groups * -(-headdim // 32) // 4)
+    return (*lens, *(0,) * (768 // tiles))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [(70, 1, 131), (64, 200)], ids=str)
+@pytest.mark.parametrize("heads,headdim,dstate,groups",
+                         [(4, 48, 64, 4), (7, 64, 16, 7), (9, 32, 128, 3), (8, 96, 24, 2), (6, 64, 128, 2),
+                          (3, 40, 32, 1), (5, 8, 8, 1)])
+def test_scan_many_prompts(mss, heads, headdim, dstate, groups, lens, io):
+    v, c = scan_inputs(gen(22), crowd(lens, heads, headdim, groups), heads, headdim, dstate, groups, io, extra=2)
+    scan_check(mss, f"scan crowd H={heads} P={headdim} N={dstate} G={groups} {io}", v, c)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,headdim,dstate,lens", [(3, 64, 128, (1500, 3, 700, 0, 257)), (1, 32, 64, (1025, 321))],
+                         ids=str)
+def test_scan_many_prompts_cut_over_time(mss, heads, headdim, dstate, lens, io):
+    v, c = scan_inputs(gen(23), crowd(lens, heads, headdim, 1), heads, headdim, dstate, 1, io, rates=(-2.0, 2.0))
+    scan_check(mss, f"scan crowd cut {io}", v, c)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_scan_many_prompts_fast_decay(mss, io):
+    v, c = scan_inputs(gen(24), crowd((150, 64), 6, 32, 1), 6, 32, 32, 1, io, rates=(-12.0, 6.0))
+    scan_check(mss, f"scan crowd decays {io}", v, c)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("headdim,dstate", [(8, 8), (16, 16), (24, 40), (72, 128), (80, 64)])
+def test_scan_small_tiles(mss, headdim, dstate, io):
+    """Columns that end inside a tile of 16, whole and cut over time."""
+    v, c = scan_inputs(gen(25), (70, 330, 2), 2, headdim, dstate, 1, io)
+    scan_check(mss, f"scan tiles P={headdim} N={dstate} {io}", v, c)
+    v, c = scan_inputs(gen(25), (400,), 2, headdim, dstate, 1, io)
+    scan_check(mss, f"scan tiles cut P={headdim} N={dstate} {io}", v, c)
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
