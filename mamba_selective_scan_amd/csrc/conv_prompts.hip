@@ -13,7 +13,7 @@
 // prompt leaves, belong to a job of their own (one per prompt and channel
 // vector, in the same launch), so a window has one reader, which is also its
 // writer, however many waves share the prompt.  5376 channels x 32768 rows in
-// bf16, 24 prompts: 156 us, 4.5 TB/s, where a copy reaches 5.1 (165 us with
+// bf16, 24 prompts: 155 us, 4.5 TB/s, where a copy reaches 5.1 (165 us with
 // four rows ahead; runs of 16 or 64 rows: 169 and 163 us).
 #include "mss_head.hpp"
 
