@@ -145,6 +145,13 @@ struct vecio<float, V> {
     for (int i = 0; i < V; ++i) q[i] = v[i];
     *reinterpret_cast<raw*>(p) = q;
   }
+  // past the caches
+  __device__ static inline void store_past(float* p, const float* v) {
+    raw q;
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = v[i];
+    __builtin_nontemporal_store(q, reinterpret_cast<raw*>(p));
+  }
 };
 template <int V>
 struct vecio<bf16_t, V> {
@@ -175,10 +182,13 @@ __device__ inline void load_part(const IO* p, int n, float* v) {
     for (int i = 0; i < V; ++i) v[i] = i < n ? io_traits<IO>::load(p + i) : 0.0f;
   }
 }
-template <typename IO, int V>
+template <typename IO, int V, bool PAST = false>
 __device__ inline void store_part(IO* p, int n, const float* v) {
   if (n >= V) {
-    vecio<IO, V>::store(p, v);
+    if constexpr (PAST)
+      vecio<IO, V>::store_past(p, v);
+    else
+      vecio<IO, V>::store(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
