@@ -504,7 +504,10 @@ mss_status mss_causal_conv1d_update(const mss_conv_step_args *args, void *stream
  * entry; 0: from zero, whatever the entry holds.  An empty prompt leaves its
  * entry as it was (resume) or zero.  Two prompts of one call must not share a
  * slot; entries of other slots are left as they were.  Values of cu_seqlens
- * outside these rules give wrong results, never an access out of bounds. */
+ * outside these rules give wrong results, never an access out of bounds.
+ *
+ * Operations 7 to 10 refuse sizes whose launch would pass 2^32 threads
+ * (MSS_ERR_BAD_SHAPE). */
 
 /* Arguments of mss_causal_conv1d_prompts.  Set struct_size = sizeof(mss_conv_prompts_args). */
 typedef struct mss_conv_prompts_args {

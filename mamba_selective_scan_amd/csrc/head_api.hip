@@ -21,6 +21,8 @@ using mss::overlaps;
 using mss::strides_nonneg;
 
 constexpr int64_t kMaxInt = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;  // of a launch
+constexpr int64_t kMaxGroups = kMaxThreads / 256;        // workgroups of 256
 constexpr int64_t kMaxTokens = int64_t{1} << 30;
 constexpr int64_t kMaxSeqs = int64_t{1} << 20;
 constexpr int64_t kMaxNormDim = 32768;
@@ -142,7 +144,10 @@ mss_status check_step_shape(const mss_head_step_args* a) {
   const mss_status st = check_head_shape(a->heads, a->headdim, a->dstate, a->groups);
   if (st != MSS_OK) return st;
   const int64_t chans = a->heads * a->headdim + 2 * a->groups * a->dstate;
-  if (chans > kMaxInt || a->rows > kMaxInt / chans || a->rows * a->heads > kMaxInt / ((a->headdim + 7) / 8))
+  // (a workgroup's columns are 64 or more, or at least half of the head's, once
+  // there are 256 workgroups)
+  if (chans > kMaxInt || a->rows > kMaxInt / chans ||
+      a->rows * a->heads > kMaxGroups / (2 * ((a->headdim + 63) / 64)))
     return MSS_ERR_BAD_SHAPE;
   return MSS_OK;
 }
@@ -166,6 +171,10 @@ mss_status mss_causal_conv1d_prompts(const mss_conv_prompts_args* a, void* strea
     return MSS_ERR_BAD_SHAPE;
   if (a->activation != MSS_ACT_NONE && a->activation != MSS_ACT_SILU) return MSS_ERR_BAD_STRUCT;
   const int64_t T = a->tokens, W = a->width, es = elem(a->io_dtype);
+  const int64_t colgroups = (a->dim + 1024 / es - 1) / (1024 / es);  // a wave's 16 bytes a lane
+  const int64_t run = std::clamp(T * colgroups / kConvWaves, kConvShortRun, kConvRun);
+  const int64_t nruns = (T + run - 1) / run;
+  if ((nruns + a->seqs) * colgroups > 4 * kMaxGroups) return MSS_ERR_BAD_SHAPE;
   if (a->weight == nullptr || a->cu_seqlens == nullptr || (W > 1 && a->window == nullptr) ||
       (T > 0 && (a->x == nullptr || a->out == nullptr)))
     return MSS_ERR_NULL_POINTER;
@@ -199,11 +208,9 @@ mss_status mss_causal_conv1d_prompts(const mss_conv_prompts_args* a, void* strea
     k.sw[i] = a->weight_stride[i];
   }
   k.swin = a->window_stride;
-  const int64_t lane_cols = 16 / es;
-  k.colgroups = static_cast<int>((a->dim + 64 * lane_cols - 1) / (64 * lane_cols));
-  k.run = static_cast<int>(std::clamp(T * k.colgroups / kConvWaves, kConvShortRun, kConvRun));
-  k.nruns = (T + k.run - 1) / k.run;
-  if ((k.nruns + a->seqs) * k.colgroups > 4 * kMaxInt) return MSS_ERR_BAD_SHAPE;
+  k.colgroups = static_cast<int>(colgroups);
+  k.run = static_cast<int>(run);
+  k.nruns = nruns;
   k.x = a->x;
   k.weight = a->weight;
   k.bias = a->bias;
@@ -223,6 +230,10 @@ mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
   const mss_status shape = check_scan_shape(a);
   if (shape != MSS_OK) return shape;
   const int64_t T = a->tokens, H = a->heads, P = a->headdim, N = a->dstate, G = a->groups;
+  const HeadScanPlan plan = head_scan_plan(a);
+  if ((a->seqs + plan.cut_slots) * plan.tiles > kMaxGroups ||
+      plan.cut_prompts * ((H * P * N + 1023) / 1024) > kMaxGroups)
+    return MSS_ERR_BAD_SHAPE;
   const int64_t es = elem(a->io_dtype);
   if (a->A_log == nullptr || a->cu_seqlens == nullptr || a->state == nullptr ||
       (T > 0 && (a->x == nullptr || a->dt_raw == nullptr || a->B == nullptr || a->C == nullptr ||
@@ -263,10 +274,6 @@ mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
   const Extent eo = any ? extent_of(a->out, xs, a->out_stride, 3, es) : none;
   const Extent es_ = cache_extent(a->state, a->cache_slots, H * P * N, a->state_stride, 4);
   if (any_overlap(eo, ins) || any_overlap(es_, ins) || overlaps(eo, es_)) return MSS_ERR_ALIASING;
-  const HeadScanPlan plan = head_scan_plan(a);
-  if ((a->seqs + plan.cut_slots) * plan.tiles > kMaxInt ||
-      plan.cut_prompts * ((H * P * N + 1023) / 1024) > kMaxInt)
-    return MSS_ERR_BAD_SHAPE;
   if (plan.workspace > 0) {
     if (a->workspace == nullptr || a->workspace_bytes < plan.workspace) return MSS_ERR_WORKSPACE_TOO_SMALL;
     const Extent ew = vec(a->workspace, static_cast<int64_t>(plan.workspace), 1);
@@ -393,7 +400,8 @@ mss_status mss_rms_norm(const mss_norm_args* a, void* stream) {
     return MSS_ERR_BAD_STRUCT;
   const int64_t R = a->rows, D = a->dim;
   if (R < 1 || R > kMaxInt || D < 1 || D > kMaxNormDim ||
-      (a->quant == MSS_QUANT_BLOCK && D % MSS_SCALE_BLOCK != 0) || !(a->eps >= 0.0f))
+      (a->quant == MSS_QUANT_BLOCK && D % MSS_SCALE_BLOCK != 0) || !(a->eps >= 0.0f) ||
+      R > kMaxThreads / (D <= 2048 ? 64 : D <= 8192 ? 256 : 1024) - 3)
     return MSS_ERR_BAD_SHAPE;
   if (a->x == nullptr || a->weight == nullptr || a->out == nullptr ||
       (a->quant != MSS_QUANT_NONE && a->scale == nullptr))

@@ -81,12 +81,13 @@ CALLS = {"conv": (conv, "mss_causal_conv1d_prompts"), "scan": (scan, "mss_head_s
 STRUCT = [dict(struct_size=8), dict(reserved0=1)]
 SHAPE = {
     "conv": [dict(tokens=-1), dict(tokens=(1 << 30) + 1), dict(dim=0), dict(width=0), dict(width=5), dict(seqs=0),
-             dict(seqs=(1 << 20) + 1), dict(cache_slots=0)],
+             dict(seqs=(1 << 20) + 1), dict(cache_slots=0), dict(tokens=1 << 30, dim=1 << 15, x_stride=(1 << 15, 1))],
     "scan": [dict(tokens=-1), dict(heads=0), dict(headdim=0), dict(groups=0), dict(groups=3), dict(groups=8),
-             dict(seqs=0), dict(cache_slots=0), dict(heads=1 << 40), dict(heads=1 << 29)],
+             dict(seqs=0), dict(cache_slots=0), dict(heads=1 << 40), dict(heads=1 << 29), dict(tokens=0, heads=96, seqs=1 << 20, headdim=64)],
     "step": [dict(rows=0), dict(heads=0), dict(headdim=0), dict(groups=3), dict(width=5), dict(cache_slots=0),
-             dict(rows=1 << 30)],
-    "norm": [dict(rows=0), dict(dim=0), dict(dim=130), dict(dim=32768 + 128), dict(eps=-1.0), dict(eps=float("nan"))],
+             dict(rows=1 << 30), dict(rows=1 << 22)],
+    "norm": [dict(rows=0), dict(dim=0), dict(dim=130), dict(dim=32768 + 128), dict(eps=-1.0), dict(eps=float("nan")),
+             dict(rows=1 << 26), dict(rows=1 << 24, dim=4096), dict(rows=1 << 22, dim=16384)],
 }
 NULL = {
     "conv": ["x", "weight", "cu_seqlens", "window", "out"],
