@@ -36,6 +36,7 @@ _conv_args = _lib.packer(_lib.ConvPromptsArgs)
 _scan_args = _lib.packer(_lib.HeadScanArgs)
 _step_args = _lib.packer(_lib.HeadStepArgs)
 _norm_args = _lib.packer(_lib.NormArgs)
+_Tensor = torch.Tensor
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -63,11 +64,11 @@ def _io(t):
 
 def _like(t, name, shape, dtype, device):
     """``t`` if it has this shape, dtype and device."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -75,18 +76,19 @@ def _like(t, name, shape, dtype, device):
 
 
 def _gpu(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         _need_gpu(t, name)  # (raises, saying what it got)
     return t.device
 
 
 def _weight(weight, dim, device):
     """A conv weight as [dim, W] fp32."""
-    if not isinstance(weight, torch.Tensor):
+    if not isinstance(weight, _Tensor):
         raise TypeError("weight must be a torch.Tensor")
-    if weight.dim() != 2:
+    shape = weight.shape
+    if len(shape) != 2:
         return _conv_weight(weight, dim, device)
-    return _like(weight, "weight", (dim, weight.shape[1]), torch.float32, device)
+    return _like(weight, "weight", (dim, shape[1]), torch.float32, device)
 
 
 def _vector(t, name, n, dtype, device):
@@ -94,7 +96,7 @@ def _vector(t, name, n, dtype, device):
     if t is None:
         return 0
     _like(t, name, (n,), dtype, device)
-    if n > 1 and t.stride(0) != 1:
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -102,20 +104,21 @@ def _vector(t, name, n, dtype, device):
 def _cache(t, name, inner, dtype, device):
     """A cache [slots, *inner] whose entries are contiguous, at any distance
     from slot to slot: its slot count, address and slot stride."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != len(inner) + 1 or t.shape[0] < 1:
+    shape = t.shape
+    if len(shape) != len(inner) + 1 or shape[0] < 1:
         raise ValueError(f"{name} must have shape [slots, {', '.join(map(str, inner))}], got "
-                         f"{tuple(t.shape)}")
-    _like(t, name, (t.shape[0], *inner), dtype, device)
+                         f"{tuple(shape)}")
+    _like(t, name, (shape[0], *inner), dtype, device)
     if not t.is_contiguous() and not t[0].is_contiguous():
         raise ValueError(f"each entry of {name} must be contiguous")
-    return t.shape[0], t.data_ptr(), t.stride(0)
+    return shape[0], t.data_ptr(), t.stride()[0]
 
 
 def _prompts(cu_seqlens, slots, resume, device):
     """Number of prompts, and the addresses of the three vectors."""
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+    if not isinstance(cu_seqlens, _Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be a vector of at least 2 offsets")
     n = cu_seqlens.shape[0] - 1
     return (n, _vector(cu_seqlens, "cu_seqlens", n + 1, torch.int32, device),
@@ -192,7 +195,7 @@ def head_scan_prompts(x, dt_raw, A_log, B, C, D=None, z=None, dt_bias=None, *, c
     if x.dim() != 3:
         raise ValueError(f"x must have 3 dimensions, got shape {tuple(x.shape)}")
     dt, (tokens, heads, headdim) = x.dtype, x.shape
-    if not isinstance(B, torch.Tensor) or B.dim() != 3 or B.shape[0] != tokens:
+    if not isinstance(B, _Tensor) or B.dim() != 3 or B.shape[0] != tokens:
         raise ValueError(f"B must have shape [{tokens}, groups, dstate]")
     _like(B, "B", B.shape, dt, dev)
     _like(C, "C", B.shape, dt, dev)
@@ -270,10 +273,12 @@ def head_scan_step(state, window, xbc, dt_raw, A_log, weight, bias=None, D=None,
 
 
 def _rows(t, name, shape, dtype, device):
+    """A matrix's address and the distance of its rows."""
     _like(t, name, shape, dtype, device)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.stride()
+    if cols != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit stride in its columns")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), rows
 
 
 def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=None,
@@ -295,7 +300,6 @@ def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=
         raise ValueError(f"quant must be None, 'row' or 'block', got {quant!r}")
     shape = x.shape
     rows, dim = shape
-    _like(x, "x", shape, x.dtype, dev)
     out = _out(out, x, x.dtype if quant is None else torch.float8_e4m3fn, dev)
     left, scales, res, res_type = (out,), 0, (0, 0, 0, 0), _io(x)
     if quant is not None:
@@ -311,6 +315,8 @@ def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=
     elif scale is not None:
         raise ValueError("scale is given without quant")
     if residual is not None:
+        if not isinstance(residual, _Tensor):
+            raise TypeError("residual must be a torch.Tensor")
         res_type = _io(residual)
         res = _rows(residual, "residual", shape, residual.dtype, dev)
         if residual_out is None:
