@@ -652,7 +652,7 @@ typedef struct mss_norm_args {
 mss_status mss_causal_conv1d_prompts(const mss_conv_prompts_args *args, void *stream);
 
 /* Bytes of device workspace mss_head_scan_prompts needs.  Depends only on the
- * sizes, not on the prompts' lengths.  Returns 0 and sets *status on invalid
+ * sizes, not on the prompts' lengths.  Returns 0 and sets *status (if not NULL) on invalid
  * sizes. */
 size_t mss_head_scan_prompts_workspace_size(const mss_head_scan_args *args, mss_status *status);
 

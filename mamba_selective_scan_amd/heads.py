@@ -214,10 +214,8 @@ def head_scan_prompts(x, dt_raw, A_log, B, C, D=None, z=None, dt_bias=None, *, c
                    _vector(dt_bias, "dt_bias", heads, torch.float32, dev), *prompts, *cache,
                    out.data_ptr(), *out.stride(), 1 if delta_softplus else 0, 0, 0, 0)
     lib = _lib.lib()
-    st = ctypes.c_int(0)
-    need = lib.mss_head_scan_prompts_workspace_size(ctypes.byref(a), ctypes.byref(st))
-    _lib.check(st.value)
-    _give_workspace(a, need, workspace, dev)
+    # (0 for sizes that the launch refuses)
+    _give_workspace(a, lib.mss_head_scan_prompts_workspace_size(ctypes.byref(a), None), workspace, dev)
     _launch(lib.mss_head_scan_prompts, a, dev)
     return out
 
