@@ -49,7 +49,8 @@
 //
 // A chunk that holds an infinity or a NaN in x, B or C is walked token by token
 // (0 times one in x would reach tokens before it, splitting loses an infinity, and
-// infinities of both signs would meet in a sum that the recurrence does not form).
+// infinities of both signs would meet in a sum that the recurrence does not form),
+// and so is one with values of 2^kLargeExponent or more in x or C B^T.
 #include "mss_head.hpp"
 
 namespace mss {
@@ -249,7 +250,7 @@ struct Raw {
 };
 
 // Largest exponent fields seen: 0x7f80 in one of the halves (the whole, in
-// fp32) tells an infinity or a NaN.
+// fp32) tells an infinity or a NaN, 2^e is field 127 + e.
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 template <typename IO>
 __device__ inline uint32_t top_exponents(u32x4 v, uint32_t top) {
@@ -264,8 +265,9 @@ __device__ inline uint32_t top_exponents(u32x4 v, uint32_t top) {
   return top;
 }
 template <typename IO>
-__device__ inline bool not_finite(uint32_t top) {
-  return sizeof(IO) == 2 ? (top >> 16) == 0x7f80u || (top & 0xffffu) == 0x7f80u : top == 0x7f800000u;
+__device__ inline bool reaches(uint32_t top, int exponent) {
+  const uint32_t field = static_cast<uint32_t>(127 + exponent) << 7;
+  return (top >> 16) >= field || (sizeof(IO) == 2 && (top & 0xffffu) >= field);
 }
 
 // Sums over the lanes up to each one, in 64 bits: rotations within the 16-lane
@@ -352,8 +354,16 @@ __device__ inline Where find_cut(const HeadScanArgs& a, int at, bool by_prompt) 
 // 32 ks + 15 where the piece meets the diagonal (near), at token 31 for the
 // pieces past the first 32 tokens (far).  The near factors may exceed 1, by as
 // much as 16 tokens decay; a chunk where one passes 2^kSteep takes each
-// exponential by itself.
-constexpr float kSteep = 100.0f;
+// exponential by itself.  The two factors are multiplied with each other before
+// anything else (one of them alone, next to large inputs, would pass the largest
+// fp32, next to small ones the smallest): what the inputs meet is the decay.  A
+// time step below 2^-kSteep, whose column factor could leave the normal range,
+// makes a chunk steep as well.
+constexpr float kSteep = 60.0f;
+// From here on a value of x, or of C B^T, takes the token-by-token walk, as an
+// infinity does: with decays of at most 1 and time steps below 2^20 no product
+// that the chunked form makes of the values below overflows by itself.
+constexpr int kLargeExponent = 60;
 // Values that are formed anew at each place that uses them.  The walk's loop
 // needs nearly every register for its tiles: addresses kept across it would push
 // them out to memory, and each of their reloads would wait for every load in
@@ -399,7 +409,7 @@ struct Shape {
     char x[kWaves][Q * kCols * sizeof(IO)];
     f32x4 s[kUnits * 2][64];
     Times<Q> time[2][kWaves];
-    int odd[2];  // a chunk holds something not finite
+    int odd[2];  // a chunk holds something large or not finite
   };
   struct Sum {
     char b[Q * NP * sizeof(IO)];
@@ -592,7 +602,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       // far factors that are used: rows from 32 on, columns before
       const float grow = lane < 32 ? -df : df;
       // (a NaN counts as steep: the factors would carry it to tokens before it)
-      steep = __ballot((Q == 64 || lane < Q) && (!(fabsf(dn) <= kSteep) || !(Q == 32 || grow <= kSteep))) != 0;
+      const bool tiny = dl != 0.0f && !(fabsf(dl) >= fast_exp2(-kSteep));
+      steep = __ballot((Q == 64 || lane < Q) && (tiny || !(fabsf(dn) <= kSteep) || !(Q == 32 || grow <= kSteep))) != 0;
       const float hi = static_cast<float>(sum);
       if (Q == 64 || lane < Q) {
         m.enter[lane] = long_decay(hi);
@@ -636,7 +647,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       *reinterpret_cast<u32x4*>(lds.x[wave] + wX + i * kRowsX * X::kRow) = px[i];
       odd = top_exponents<IO>(px[i], odd);
     }
-    if (not_finite<IO>(odd)) lds.odd[par] = 1;
+    if (reaches<IO>(odd, kLargeExponent)) lds.odd[par] = 1;
     const IO raw = fetch_dt(t + Q);
     // the next chunk's rows: in the sums, which have registers to spare, a whole
     // chunk ahead; in the walk, once the outputs have left theirs.  (Past the end:
@@ -696,13 +707,13 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
           for (int tp = 0; tp < NT; ++tp) y[it][tp] = mma(sb[tp], cf[it], q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
       }
-      // an infinity or a NaN in B or C is one in C B^T
+      // (an infinity or a NaN in B or C is one in C B^T)
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < kPer; ++k)
 #pragma unroll
         for (int r = 0; r < 4; ++r) top = max(top, __float_as_uint(acc[k][r]) & 0x7f800000u);
-      if (top == 0x7f800000u) lds.odd[par] = 1;
+      if (reaches<float>(top, kLargeExponent)) lds.odd[par] = 1;
       // piece (ks, it) is number it (ks = 0) or it + 2
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
@@ -744,7 +755,6 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
           for (int tp = 0; tp < NT; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
           constexpr int kIt = Q / 16;
           Frag<IO> w[kIt];
-          float row[kIt];
 #pragma unroll
           for (int it = 2 * ks; it < kIt; ++it) {
             const int i = 16 * it + c;
@@ -753,14 +763,13 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
             const f32x4 s0 = lds.s[2 * unit][lane], s1 = lds.s[2 * unit + 1][lane];
             const int below = 16 * (it & 1) + c - 8 * g;  // token slots up to this one are summed
             float v[8];
-            row[it] = 1.0f;
             if (!steep) {
-              row[it] = far ? m.row_far[i] : m.row_near[i];
+              const float row = far ? m.row_far[i] : m.row_near[i];
               const float* col = (far ? m.col_far : m.col_near) + 32 * ks + 8 * g;
               const f32x4 c0 = *reinterpret_cast<const f32x4*>(col), c1 = *reinterpret_cast<const f32x4*>(col + 4);
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                v[e] = (e < 4 ? s0[e & 3] : s1[e & 3]) * (tok(e) < 4 ? c0[tok(e) & 3] : c1[tok(e) & 3]);
+                v[e] = (e < 4 ? s0[e & 3] : s1[e & 3]) * (row * (tok(e) < 4 ? c0[tok(e) & 3] : c1[tok(e) & 3]));
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -776,17 +785,10 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2) w[it].set2(e, v[e], v[e + 1]);
           }
-          f32x4 u[kIt][NT];
 #pragma unroll
           for (int it = 2 * ks; it < kIt; ++it)
 #pragma unroll
-            for (int tp = 0; tp < NT; ++tp) u[it][tp] = mma(xt[tp], w[it], f32x4{0, 0, 0, 0});
-#pragma unroll
-          for (int it = 2 * ks; it < kIt; ++it)
-#pragma unroll
-            for (int tp = 0; tp < NT; ++tp)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) y[it][tp][r] = fmaf(row[it], u[it][tp][r], y[it][tp][r]);
+            for (int tp = 0; tp < NT; ++tp) y[it][tp] = mma(xt[tp], w[it], y[it][tp]);
           step_end();
         }
         const int eO = static_cast<int>(a.so[0]) * kES;
