@@ -24,9 +24,10 @@
 // transposing read meet each LDS bank twice, with rows' 16-byte chunks swizzled
 // by the row number (a plain order would meet them four times).
 //
-// bf16 inputs enter the products as they are.  What is rounded to bf16 besides:
-// the decayed C B^T and the entering state where they make y (one rounding of
-// each term, the size of y's own).  The state itself stays in fp32: its addends
+// bf16 inputs enter the products as they are.  The decayed C B^T and the entering
+// state are split into two bf16 parts where they make y: each term is off by
+// 2^-16 at most, far below y's own rounding (one part alone, in 545 us where this
+// takes 598 on the batch below, left 1.9e-3 of y in place of its rounding's 1.66e-3).  The state itself stays in fp32: its addends
 // delta e^(..) x are split into three bf16 parts (24 bits), so states are
 // as exact as an fp32 sum.  fp32 inputs use the fp32 matrix instruction, with
 // nothing rounded.  The sums c are taken in 64 bits and kept as two floats.
@@ -437,6 +438,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   constexpr int kLoadX = Q * kChunksX / 64;            // 16-byte loads a lane
   constexpr int kRowsBC = 256 / BC::kChunks, kRowsX = 64 / kChunksX;  // rows between them
   constexpr int kOut = 4 * NT;                         // columns of a token that a lane writes
+  constexpr int kParts = sizeof(IO) == 2 ? 2 : 1;      // of an fp32 operand of the outputs
+  constexpr int kAddParts = sizeof(IO) == 2 ? 3 : 1;   // of one of the state's addends
   using Lds = std::conditional_t<AGG, typename S::Sum, typename S::Walk>;
   __shared__ __attribute__((aligned(16))) Lds lds;
 
@@ -479,6 +482,9 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 
   // the state: tile [n = 32 q + 8 g + 4 tn + r][p = 8 (c / 4) + c % 4 + 4 tp], or p = c
   f32x4 st[kK][2][NT];
+  // an infinite state has no second part; one that would round to an infinite
+  // first part is walked token by token
+  bool split = true, huge = false;
   auto column = [](int th) { return NT == 2 ? 8 * ((th >> 2) & 3) + (th & 3) : th & 15; };
   auto lane_colx = [](int g, int c) { return NT == 2 ? X::lane_col(g, c) : X::lane_col16(g, c); };
   // where this tile's state lies in memory: what a cut prompt's segment enters
@@ -488,6 +494,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
     const int th = thread_anew(), n0 = 8 * ((th >> 4) & 3), N = anew(a.dstate);
     const float* at = home + static_cast<int64_t>(column(th)) * N + n0;
     const int ps = pc - column(th);
+    bool over = false, near = false;
 #pragma unroll
     for (int q = 0; q < kK; ++q)
 #pragma unroll
@@ -495,9 +502,17 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
         float v[8] = {};
         if (from) load_part<float, 8>(at + 4 * tp * N + 32 * q, 4 * tp < ps ? N - n0 - 32 * q : 0, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) st[q][e >> 2][tp][e & 3] = v[e];
+        for (int e = 0; e < 8; ++e) {
+          st[q][e >> 2][tp][e & 3] = v[e];
+          over |= !(fabsf(v[e]) < INFINITY);
+          near |= fabsf(v[e]) >= 0x1p127f && fabsf(v[e]) < INFINITY;
+        }
         step_end();
       }
+    if constexpr (kParts > 1 && !AGG) {
+      split = __ballot(over) == 0;
+      huge = __ballot(near) != 0;
+    }
   };
   auto state_out = [&]() __attribute__((always_inline)) {
     const int th = thread_anew(), n0 = 8 * ((th >> 4) & 3), N = anew(a.dstate);
@@ -647,7 +662,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       *reinterpret_cast<u32x4*>(lds.x[wave] + wX + i * kRowsX * X::kRow) = px[i];
       odd = top_exponents<IO>(px[i], odd);
     }
-    if (reaches<IO>(odd, kLargeExponent)) lds.odd[par] = 1;
+    if (reaches<IO>(odd, kLargeExponent) || huge) lds.odd[par] = 1;
     const IO raw = fetch_dt(t + Q);
     // the next chunk's rows: in the sums, which have registers to spare, a whole
     // chunk ahead; in the walk, once the outputs have left theirs.  (Past the end:
@@ -706,6 +721,18 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
         for (int it = 0; it < Q / 16; ++it)
 #pragma unroll
           for (int tp = 0; tp < NT; ++tp) y[it][tp] = mma(sb[tp], cf[it], q == 0 ? f32x4{0, 0, 0, 0} : y[it][tp]);
+        if (kParts > 1 && split) {
+          Frag<IO> rest[NT];
+#pragma unroll
+          for (int tp = 0; tp < NT; ++tp)
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+              rest[tp].set2(e, sb[tp].more(e, st[q][e >> 2][tp][e & 3]), sb[tp].more(e + 1, st[q][e >> 2][tp][(e & 3) + 1]));
+#pragma unroll
+          for (int it = 0; it < Q / 16; ++it)
+#pragma unroll
+            for (int tp = 0; tp < NT; ++tp) y[it][tp] = mma(rest[tp], cf[it], y[it][tp]);
+        }
       }
       // (an infinity or a NaN in B or C is one in C B^T)
       uint32_t top = 0;
@@ -754,7 +781,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
           for (int tp = 0; tp < NT; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
           constexpr int kIt = Q / 16;
-          Frag<IO> w[kIt];
+          Frag<IO> w[kIt][kParts];
 #pragma unroll
           for (int it = 2 * ks; it < kIt; ++it) {
             const int i = 16 * it + c;
@@ -783,12 +810,17 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
               for (int e = 0; e < 8; ++e) v[e] = tok(e) <= below ? v[e] : 0.0f;
             }
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) w[it].set2(e, v[e], v[e + 1]);
+            for (int e = 0; e < 8; e += 2) {
+              w[it][0].set2(e, v[e], v[e + 1]);
+              if constexpr (kParts > 1) w[it][1].set2(e, w[it][0].more(e, v[e]), w[it][0].more(e + 1, v[e + 1]));
+            }
           }
 #pragma unroll
-          for (int it = 2 * ks; it < kIt; ++it)
+          for (int k = 0; k < kParts; ++k)
 #pragma unroll
-            for (int tp = 0; tp < NT; ++tp) y[it][tp] = mma(xt[tp], w[it], y[it][tp]);
+            for (int it = 2 * ks; it < kIt; ++it)
+#pragma unroll
+              for (int tp = 0; tp < NT; ++tp) y[it][tp] = mma(xt[tp], w[it][k], y[it][tp]);
           step_end();
         }
         const int eO = static_cast<int>(a.so[0]) * kES;
@@ -848,8 +880,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
           for (int tp = 0; tp < NT; ++tp) st[q][tn][tp] *= dec;
 #pragma unroll
       for (int ks = 0; ks < kT; ++ks) {
-        constexpr int kParts = sizeof(IO) == 2 ? 3 : 1;
-        Frag<IO> xt[NT], v[NT][kParts];
+        Frag<IO> xt[NT], v[NT][kAddParts];
 #pragma unroll
         for (int tp = 0; tp < NT; ++tp) xt[tp] = X::col(lds.x[wave], lxc, ks, 0, tp);
         const float* left = m.left + 32 * ks + 8 * g;
@@ -861,7 +892,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
             float r0 = xt[tp].get(e) * (tok(e) < 4 ? l0[tok(e) & 3] : l1[tok(e) & 3]);
             float r1 = xt[tp].get(e + 1) * (tok(e + 1) < 4 ? l0[tok(e + 1) & 3] : l1[tok(e + 1) & 3]);
 #pragma unroll
-            for (int k = 0; k < kParts; ++k) {
+            for (int k = 0; k < kAddParts; ++k) {
               v[tp][k].set2(e, r0, r1);
               r0 = v[tp][k].more(e, r0);
               r1 = v[tp][k].more(e + 1, r1);
@@ -873,7 +904,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
 #pragma unroll
           for (int tn = 0; tn < 2; ++tn) bt[tn] = BC::col(lds.b, lcol, ks, q, tn);
 #pragma unroll
-          for (int k = kParts - 1; k >= 0; --k)
+          for (int k = kAddParts - 1; k >= 0; --k)
 #pragma unroll
             for (int tn = 0; tn < 2; ++tn)
 #pragma unroll

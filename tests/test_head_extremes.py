@@ -61,3 +61,44 @@ def test_scan_tiny_time_steps_among_fast_decay(mss, io):  # noqa: F811
         v["dt_raw"][at] = dt
         v["x"][at + 1:at + 3] = 0
     scan_check(mss, f"scan of tiny steps {io}", v, c, softplus=False)
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["tiles16", "tiles32"])
+@pytest.mark.parametrize("lens,heads,headdim,dstate", [((130, 1, 64), 3, 64, 128), ((700, 9), 2, 40, 24),
+                                                       ((70,), 3, 33, 20)], ids=str)
+def test_scan_bf16_outputs_are_rounded_once(mss, lens, heads, headdim, dstate, wide):  # noqa: F811
+    """bf16 outputs are off by their own rounding and 2^-16 of the terms they are a
+    sum of, however much those cancel: an operand kept as two bf16 parts is off by
+    2^-8 of 2^-8."""
+    v, c = scan_inputs(gen(35), crowd(lens, heads, headdim, 1) if wide else lens, heads, headdim, dstate, 1, "bf16")
+    args = tuple(v.values())
+    want, _ = ref.scan_prompts(*args, c["cu"], c["state"], c["slots"], c["resume"])
+    mag, _ = ref.scan_prompts(*args, c["cu"], c["state"], c["slots"], c["resume"], absolute=True)
+    got = mss.head_scan_prompts(*args, cu_seqlens=c["cu"], state=c["state"], slots=c["slots"], resume=c["resume"])
+    torch.cuda.synchronize()
+    k = (2 * max(lens) + dstate + 8) * 2.0 ** -24
+    ref.within(f"scan rounded once {lens} {wide}", got, want, (k + 2.0 ** -16) * mag + 2.0 ** -8 * 1.01 * want.abs())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [(150, 9), (700, 40)], ids=str)
+def test_scan_from_infinite_states(mss, lens, io):  # noqa: F811
+    """Infinite and huge entries of a cached state reach the outputs as they are."""
+    v, c = scan_inputs(gen(36), lens, 2, 40, 24, 1, io, rates=(-6.0, -5.0))
+    c["resume"] = torch.ones(2, dtype=torch.int32, device="cuda")
+    c["state"][:, 0, 3, 5] = float("inf")
+    c["state"][:, 0, 7, 5] = float("-inf")
+    c["state"][:, 1, 9, 2] = 3.4e38
+    v["B"].abs_()
+    v["C"].fill_(0.5)
+    v["x"].abs_()
+    state = c["state"].clone()
+    want, wstate = ref.scan_prompts(*v.values(), c["cu"], c["state"], c["slots"], c["resume"])
+    got = mss.head_scan_prompts(*v.values(), cu_seqlens=c["cu"], state=state, slots=c["slots"], resume=c["resume"])
+    torch.cuda.synchronize()
+    assert torch.isinf(want).any()
+    # (an output past its type's range is an infinity)
+    for what, x, y in (("out", ref.d(got), want.to(got.dtype)), ("state", ref.d(state), wstate)):
+        for test in (torch.isnan, torch.isposinf, torch.isneginf):
+            wrong = int((test(x) != test(y)).sum())
+            assert wrong == 0, f"{wrong} values of {what} differ in {test.__name__}"
