@@ -51,7 +51,8 @@
 // A chunk that holds an infinity or a NaN in x, B or C is walked token by token
 // (0 times one in x would reach tokens before it, splitting loses an infinity, and
 // infinities of both signs would meet in a sum that the recurrence does not form),
-// and so is one with values of 2^kLargeExponent or more in x or C B^T.
+// and so is one with values of 2^kLargeExponent or more in x or C B^T, or with time
+// steps or a rate whose sums or exponentials pass fp32.
 #include "mss_head.hpp"
 
 namespace mss {
@@ -362,9 +363,15 @@ __device__ inline Where find_cut(const HeadScanArgs& a, int at, bool by_prompt) 
 // makes a chunk steep as well.
 constexpr float kSteep = 60.0f;
 // From here on a value of x, or of C B^T, takes the token-by-token walk, as an
-// infinity does: with decays of at most 1 and time steps below 2^20 no product
-// that the chunked form makes of the values below overflows by itself.
+// infinity does: below it, and with the time steps and growth below, no product
+// that the chunked form makes overflows by itself.
 constexpr int kLargeExponent = 60;
+// A chunk is walked token by token where a time step lies past kLargeStep (or is
+// not finite: the sums over the tokens would be, and differences of those NaN), a
+// token grows the state by more than 2^kGrowth (2^32 over a chunk), or a decay
+// rate overflows.
+constexpr float kLargeStep = 0x1p20f;
+constexpr float kGrowth = 0.5f;
 // Values that are formed anew at each place that uses them.  The walk's loop
 // needs nearly every register for its tiles: addresses kept across it would push
 // them out to memory, and each of their reloads would wait for every load in
@@ -410,7 +417,7 @@ struct Shape {
     char x[kWaves][Q * kCols * sizeof(IO)];
     f32x4 s[kUnits * 2][64];
     Times<Q> time[2][kWaves];
-    int odd[2];  // a chunk holds something large or not finite
+    int odd[2];  // a chunk is walked token by token
   };
   struct Sum {
     char b[Q * NP * sizeof(IO)];
@@ -593,14 +600,16 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
   };
   double total = 0.0;   // the segment's decay (AGG)
   float decay = 1.0f;   // of the chunk that times() last formed
-  bool steep = false;
+  bool steep = false, wild = false;  // of that chunk
   auto times = [&](int t, IO raw, int par) __attribute__((always_inline)) {
     const int lane = thread_anew() & 63;
     float dl = io_traits<IO>::load(&raw) + bias;
     const float sp = softplus(dl);
     dl = a.softplus ? sp : dl;
     dl = lane < Q && t + lane < end ? dl : 0.0f;
-    const double sum = lane_sums(static_cast<double>(dl * rate));
+    const float power = dl * rate;
+    wild = __ballot(!(fabsf(dl) <= kLargeStep && power <= kGrowth && power > -INFINITY)) != 0;
+    const double sum = lane_sums(static_cast<double>(power));
     const double last = lane_value(sum, Q - 1);
     decay = long_decay(static_cast<float>(last));
     if (AGG) total += last;
@@ -616,9 +625,8 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       const float dn = static_cast<float>(sum - (Q == 64 && lane >= 32 ? n1 : n0)), df = static_cast<float>(sum - far);
       // far factors that are used: rows from 32 on, columns before
       const float grow = lane < 32 ? -df : df;
-      // (a NaN counts as steep: the factors would carry it to tokens before it)
-      const bool tiny = dl != 0.0f && !(fabsf(dl) >= fast_exp2(-kSteep));
-      steep = __ballot((Q == 64 || lane < Q) && (tiny || !(fabsf(dn) <= kSteep) || !(Q == 32 || grow <= kSteep))) != 0;
+      const bool tiny = dl != 0.0f && fabsf(dl) < fast_exp2(-kSteep);
+      steep = __ballot((Q == 64 || lane < Q) && (tiny || fabsf(dn) > kSteep || (Q == 64 && grow > kSteep))) != 0;
       const float hi = static_cast<float>(sum);
       if (Q == 64 || lane < Q) {
         m.enter[lane] = long_decay(hi);
@@ -662,7 +670,7 @@ __global__ __launch_bounds__(256, 2) void head_scan_kernel(HeadScanArgs a) {
       *reinterpret_cast<u32x4*>(lds.x[wave] + wX + i * kRowsX * X::kRow) = px[i];
       odd = top_exponents<IO>(px[i], odd);
     }
-    if (reaches<IO>(odd, kLargeExponent) || huge) lds.odd[par] = 1;
+    if (reaches<IO>(odd, kLargeExponent) || huge || wild) lds.odd[par] = 1;
     const IO raw = fetch_dt(t + Q);
     // the next chunk's rows: in the sums, which have registers to spare, a whole
     // chunk ahead; in the walk, once the outputs have left theirs.  (Past the end:
@@ -1013,7 +1021,7 @@ __global__ __launch_bounds__(256) void head_scan_carry_kernel(HeadScanArgs a, in
       if (k0 + k < nseg) {
         store_part<float, 4>(part + (k0 + k) * all, n, s);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = fmaf(d[k][e], s[e], v[k][e]);
+        for (int e = 0; e < 4; ++e) s[e] = s[e] == 0.0f ? v[k][e] : fmaf(d[k][e], s[e], v[k][e]);  // (d may be infinite)
       }
     }
   }

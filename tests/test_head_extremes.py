@@ -102,3 +102,53 @@ def test_scan_from_infinite_states(mss, lens, io):  # noqa: F811
         for test in (torch.isnan, torch.isposinf, torch.isneginf):
             wrong = int((test(x) != test(y)).sum())
             assert wrong == 0, f"{wrong} values of {what} differ in {test.__name__}"
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,at", [((100,), 37), ((700, 40), 300), ((100,) + (0,) * 600, 37),
+                                     ((700, 40) + (0,) * 600, 300)], ids=lambda v: str(v)[:12])
+def test_scan_past_an_infinite_time_step(mss, lens, at, io):  # noqa: F811
+    """An infinite time step makes the states infinite, not NaN, and tokens before
+    it as they are without it."""
+    v, c = scan_inputs(gen(32), lens, 2, 40, 24, 1, io)
+    c["resume"] = None
+    v["D"] = None
+    clean = mss.head_scan_prompts(*v.values(), cu_seqlens=c["cu"], state=c["state"].clone(), slots=c["slots"])
+    v["dt_raw"][at, 0] = float("inf")
+    state = c["state"].clone()
+    got = mss.head_scan_prompts(*v.values(), cu_seqlens=c["cu"], state=state, slots=c["slots"])
+    want, wstate = ref.scan_prompts(*v.values(), c["cu"], c["state"], c["slots"])
+    torch.cuda.synchronize()
+    got, state, clean = ref.d(got), ref.d(state), ref.d(clean)
+    assert torch.isinf(wstate[int(c["slots"][0]), 0]).all()
+    for what, x, y in (("out", got, want), ("state", state, wstate)):
+        for test in (torch.isnan, torch.isposinf, torch.isneginf):
+            wrong = int((test(x) != test(y)).sum())
+            assert wrong == 0, f"{wrong} values of {what} differ in {test.__name__}"
+    # the same sums, a chunk's in another order
+    ref.within("before", got[:at], clean[:at], 2.0 ** -6 * clean[:at].abs().amax((0, 2), True))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [(64, 20), (700,), (64, 20) + (0,) * 600], ids=lambda v: str(v)[:12])
+def test_scan_growth_from_nothing(mss, lens, io):  # noqa: F811
+    """Negative time steps, whose decays pass the largest fp32 over a chunk, and no
+    input but in the last tokens: a zero state stays zero until then."""
+    v, c = scan_inputs(gen(33), lens, 2, 40, 24, 1, io)
+    c["resume"] = None
+    v["A_log"].zero_()
+    v["dt_raw"].fill_(-3.0)
+    v["dt_bias"] = None
+    end = lens[0]
+    v["x"][:end - 4] = 0
+    scan_check(mss, f"scan of growth {io}", v, c, softplus=False)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_scan_rate_past_fp32(mss, io):  # noqa: F811
+    """A decay rate that overflows fp32 leaves each token by itself, as it does in
+    the step."""
+    v, c = scan_inputs(gen(34), (70, 9), 2, 40, 24, 1, io)
+    c["resume"] = None
+    v["A_log"] = torch.tensor([100.0, 0.5], device="cuda")
+    scan_check(mss, f"scan of a rate past fp32 {io}", v, c)
