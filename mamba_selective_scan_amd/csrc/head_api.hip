@@ -123,10 +123,11 @@ HeadScanPlan head_scan_plan(const mss_head_scan_args* a) {
   p.narrow = tile(32) < slots / 4 * 3 && tile(16) <= slots;
   if (!p.narrow) tile(32);
   if (a->tokens > seg) {
-    // a cut prompt has more than seg tokens, so at most 2 len / seg segments
+    // a cut prompt has more than seg tokens, so at most 2 len / seg segments, and
+    // less than len / seg + 1
     p.seg_len = seg;
-    p.cut_slots = 2 * a->tokens / seg;
     p.cut_prompts = std::min(a->seqs, a->tokens / seg);
+    p.cut_slots = std::min(2 * a->tokens / seg, a->tokens / seg + p.cut_prompts);
     const size_t states = static_cast<size_t>(a->heads * a->headdim * a->dstate) * 4;
     p.parts = (p.cut_slots * states + 255) / 256 * 256;
     p.workspace = p.parts + static_cast<size_t>(p.cut_slots * a->heads) * 4;

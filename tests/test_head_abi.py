@@ -255,3 +255,13 @@ def test_bad_tensors_are_refused_before_launch(monkeypatch):
             (dict(residual_out=z(5, 256)), ValueError, "residual_out"),
             (dict(quant="row", out=z(5, 256)), TypeError, "out")]:
         bad(err, match, mss.rms_norm, **{**norm, **change})
+
+
+def test_workspace_holds_what_prompts_can_be_cut_into():
+    """A cut prompt has less than one segment more than its tokens fill: 8 prompts
+    in 32768 tokens make at most 40 segments of 1024, one makes at most 40 of 832."""
+    lib = _lib.lib()
+    for heads, seqs, segments in ((80, 8, 40), (24, 1, 40)):
+        a = put(scan(), tokens=32768, heads=heads, groups=1, seqs=seqs)
+        need = lib.mss_head_scan_prompts_workspace_size(ctypes.byref(a), None)
+        assert 0 < need <= segments * (heads * 64 * 128 * 4 + heads * 4) + 256
