@@ -64,16 +64,6 @@ mss_status check_head_shape(int64_t heads, int64_t headdim, int64_t dstate, int6
   return MSS_OK;
 }
 
-mss_status check_scan_shape(const mss_head_scan_args* a) {
-  if (a == nullptr || a->struct_size != sizeof(mss_head_scan_args) || a->reserved0 != 0)
-    return MSS_ERR_BAD_STRUCT;
-  if (bad_dtype(a->io_dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
-  if (a->tokens < 0 || a->tokens > kMaxTokens || a->seqs < 1 || a->seqs > kMaxSeqs ||
-      a->cache_slots < 1 || a->cache_slots > kMaxInt)
-    return MSS_ERR_BAD_SHAPE;
-  return check_head_shape(a->heads, a->headdim, a->dstate, a->groups);
-}
-
 // How a head-wise scan is cut over time and over columns: prompts longer than
 // seg_len run as segments, so that a few long prompts still fill the card, and
 // tiles of 16 columns take the place of 32 while there are too few of those.
@@ -133,6 +123,23 @@ HeadScanPlan head_scan_plan(const mss_head_scan_args* a) {
     p.workspace = p.parts + static_cast<size_t>(p.cut_slots * a->heads) * 4;
   }
   return p;
+}
+
+// The scan's sizes, and how it runs.
+mss_status check_scan_shape(const mss_head_scan_args* a, HeadScanPlan* plan) {
+  if (a == nullptr || a->struct_size != sizeof(mss_head_scan_args) || a->reserved0 != 0)
+    return MSS_ERR_BAD_STRUCT;
+  if (bad_dtype(a->io_dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
+  if (a->tokens < 0 || a->tokens > kMaxTokens || a->seqs < 1 || a->seqs > kMaxSeqs ||
+      a->cache_slots < 1 || a->cache_slots > kMaxInt)
+    return MSS_ERR_BAD_SHAPE;
+  const mss_status st = check_head_shape(a->heads, a->headdim, a->dstate, a->groups);
+  if (st != MSS_OK) return st;
+  *plan = head_scan_plan(a);
+  if ((a->seqs + plan->cut_slots) * plan->tiles > kMaxGroups ||
+      plan->cut_prompts * ((a->heads * a->headdim * a->dstate + 1023) / 1024) > kMaxGroups)
+    return MSS_ERR_BAD_SHAPE;
+  return MSS_OK;
 }
 
 mss_status check_step_shape(const mss_head_step_args* a) {
@@ -222,19 +229,17 @@ mss_status mss_causal_conv1d_prompts(const mss_conv_prompts_args* a, void* strea
 }
 
 size_t mss_head_scan_prompts_workspace_size(const mss_head_scan_args* a, mss_status* status) {
-  const mss_status st = check_scan_shape(a);
+  HeadScanPlan plan;
+  const mss_status st = check_scan_shape(a, &plan);
   if (status != nullptr) *status = st;
-  return st == MSS_OK ? head_scan_plan(a).workspace : 0;
+  return st == MSS_OK ? plan.workspace : 0;
 }
 
 mss_status mss_head_scan_prompts(const mss_head_scan_args* a, void* stream) {
-  const mss_status shape = check_scan_shape(a);
+  HeadScanPlan plan;
+  const mss_status shape = check_scan_shape(a, &plan);
   if (shape != MSS_OK) return shape;
   const int64_t T = a->tokens, H = a->heads, P = a->headdim, N = a->dstate, G = a->groups;
-  const HeadScanPlan plan = head_scan_plan(a);
-  if ((a->seqs + plan.cut_slots) * plan.tiles > kMaxGroups ||
-      plan.cut_prompts * ((H * P * N + 1023) / 1024) > kMaxGroups)
-    return MSS_ERR_BAD_SHAPE;
   const int64_t es = elem(a->io_dtype);
   if (a->A_log == nullptr || a->cu_seqlens == nullptr || a->state == nullptr ||
       (T > 0 && (a->x == nullptr || a->dt_raw == nullptr || a->B == nullptr || a->C == nullptr ||

@@ -265,3 +265,14 @@ def test_workspace_holds_what_prompts_can_be_cut_into():
         a = put(scan(), tokens=32768, heads=heads, groups=1, seqs=seqs)
         need = lib.mss_head_scan_prompts_workspace_size(ctypes.byref(a), None)
         assert 0 < need <= segments * (heads * 64 * 128 * 4 + heads * 4) + 256
+
+
+def test_workspace_size_of_sizes_that_the_launch_refuses():
+    """No size, and the launch's status, where the segments would pass 2^32 threads:
+    a binding allocates nothing before the refusal."""
+    lib, st = _lib.lib(), ctypes.c_int(0)
+    a = put(scan(), tokens=1 << 30, heads=4096, groups=1, x_stride=(1 << 18, 64, 1), z_stride=(1 << 18, 64, 1),
+            out_stride=(1 << 18, 64, 1))
+    assert lib.mss_head_scan_prompts_workspace_size(ctypes.byref(a), ctypes.byref(st)) == 0
+    assert st.value == _lib.STATUS_CODE["MSS_ERR_BAD_SHAPE"]
+    assert lib.mss_head_scan_prompts(ctypes.byref(a), None) == st.value
