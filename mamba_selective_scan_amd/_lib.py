@@ -284,7 +284,7 @@ class NormArgs(ctypes.Structure):
 
 def packer(cls):
     """A function that makes a ``cls`` from its fields' values in order, without
-    struct_size (arrays flattened, None for a null pointer): one call of struct
+    struct_size (arrays flattened, 0 for a null pointer): one call of struct
     instead of a store through ctypes for each field."""
     codes = {ctypes.c_uint32: "I", _i32: "i", _i64: "q", _vp: "P", ctypes.c_size_t: "N",
              ctypes.c_float: "f"}

@@ -33,8 +33,8 @@
 // nothing rounded.  The sums c are taken in 64 bits and kept as two floats.
 //
 // A prompt longer than a.seg_len is cut into segments: one pass forms what each
-// segment adds to a zero state, one composes the states entering the segments
-// (and the state the prompt leaves), and the walk then runs all segments at once.
+// segment adds to a zero state, one composes the states entering the segments, and
+// the walk then runs all segments at once: the last one's writes the cache entry.
 //
 // What bounds it: instructions.  A chunk of 64 tokens costs a wave 152 MFMAs of 16
 // cycles and 1200 VALU instructions (states of 128; counted); with two waves a SIMD
