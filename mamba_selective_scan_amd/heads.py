@@ -16,8 +16,8 @@ behind the last prompt are.  No two prompts or rows of a call may share a slot.
 ``resume`` (int32, on the device; None means 0 for all) tells which prompts
 start from their cache entries; the others start from zero.
 
-The values of cu_seqlens, slots and resume stay on the device: nothing here
-synchronises.  These operations update caches in place and have no gradients.
+Calls of no tokens or no rows are fine: they give empty outputs.  The values of
+cu_seqlens, slots and resume stay on the device: nothing here synchronises.  These operations update caches in place and have no gradients.
 """
 
 from __future__ import annotations
@@ -266,7 +266,8 @@ def head_scan_step(state, window, xbc, dt_raw, A_log, weight, bias=None, D=None,
                    _vector(dt_bias, "dt_bias", heads, torch.float32, dev),
                    _vector(slots, "slots", rows, torch.int32, dev),
                    out.data_ptr(), *out.stride(), 1 if delta_softplus else 0, 0)
-    _launch(_lib.lib().mss_head_scan_step, a, dev)
+    if rows:
+        _launch(_lib.lib().mss_head_scan_step, a, dev)
     return out
 
 
@@ -326,5 +327,6 @@ def rms_norm(x, weight, *, residual=None, eps=1e-5, quant=None, out=None, scale=
     a = _norm_args(_io(x), res_type, _QUANT[quant], rows, dim, *_rows(x, "x", shape, x.dtype, dev),
                    *res[:2], _vector(weight, "weight", dim, torch.float32, dev),
                    *_rows(out, "out", shape, out.dtype, dev), scales, *res[2:], eps, 0)
-    _launch(_lib.lib().mss_rms_norm, a, dev)
+    if rows:
+        _launch(_lib.lib().mss_rms_norm, a, dev)
     return left if len(left) > 1 else out

@@ -1,6 +1,7 @@
-"""The head-wise scan at magnitudes, time steps and decays far from those of a
-trained layer: what the recurrence gives in 64 bits is what the chunked form has
-to give, within the bounds of test_head_ops.
+"""The head-wise operations at their edges: magnitudes, time steps and decays far
+from those of a trained layer (what the recurrence gives in 64 bits is what the
+chunked form has to give, within the bounds of test_head_ops), calls of no rows,
+offsets outside the rules.
 """
 
 import math
@@ -9,7 +10,7 @@ import pytest
 import torch
 
 import head_ref as ref
-from test_head_ops import crowd, gen, mss, offsets, randn, scan_check, scan_inputs  # noqa: F401
+from test_head_ops import DT, crowd, gen, ints, mss, randn, scan_check, scan_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +153,26 @@ def test_scan_rate_past_fp32(mss, io):  # noqa: F811
     c["resume"] = None
     v["A_log"] = torch.tensor([100.0, 0.5], device="cuda")
     scan_check(mss, f"scan of a rate past fp32 {io}", v, c)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_no_rows(mss, io):  # noqa: F811
+    """A step and a norm of no rows, as a server's empty batch makes them, next to
+    a conv and a scan of no tokens: empty outputs, caches as they were."""
+    g, dt = gen(26), DT[io]
+    state, window = randn(g, 3, 2, 8, 16), randn(g, 3, 48, 3, dtype=dt)
+    kept = state.clone(), window.clone()
+    v = dict(A_log=randn(g, 2), weight=randn(g, 48, 4), bias=randn(g, 48), D=randn(g, 2))
+    y = mss.head_scan_step(state, window, randn(g, 0, 48, dtype=dt), randn(g, 0, 2, dtype=dt), *v.values(),
+                           randn(g, 0, 2, 8, dtype=dt), slots=ints())
+    assert y.shape == (0, 2, 8) and y.dtype is dt
+    assert torch.equal(state, kept[0]) and torch.equal(window, kept[1])
+    x, w = randn(g, 0, 256, dtype=dt), randn(g, 256)
+    assert mss.rms_norm(x, w).shape == (0, 256)
+    for quant, cols in (("row", 1), ("block", 2)):
+        q, scale, left = mss.rms_norm(x, w, residual=randn(g, 0, 256), quant=quant)
+        assert q.shape == (0, 256) and q.dtype is torch.float8_e4m3fn
+        assert scale.shape == (0, cols) and left.shape == (0, 256)
+    with pytest.raises(ValueError, match="weight"):
+        mss.rms_norm(x, w[:255])
+    torch.cuda.synchronize()
