@@ -4,6 +4,7 @@ chunked form has to give, within the bounds of test_head_ops), calls of no rows,
 offsets outside the rules.
 """
 
+import ctypes
 import math
 
 import pytest
@@ -176,3 +177,44 @@ def test_no_rows(mss, io):  # noqa: F811
     with pytest.raises(ValueError, match="weight"):
         mss.rms_norm(x, w[:255])
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("off", [1024, 1023], ids=["vectors", "elements"])
+def test_offsets_outside_the_rules_stay_in_their_buffers(mss, off, io):  # noqa: F811
+    """cu_seqlens that runs backwards, starts late or ends past the rows: what lies
+    around the outputs, caches and workspace, the entries of no prompt and the
+    inputs are as they were."""
+    from mamba_selective_scan_amd import _lib
+    heads, headdim, dstate, tokens, dim, dt = 2, 64, 64, 1200, 40, DT[io]
+    v, c = scan_inputs(gen(37), (400, 300, 500), heads, headdim, dstate, 1, io)
+    x, w = randn(gen(38), tokens, dim, dtype=dt), randn(gen(38), dim, 4)
+    slots = ints(4, 0, 2)
+    a = _lib.HeadScanArgs(struct_size=ctypes.sizeof(_lib.HeadScanArgs), io_dtype=_lib.MSS_F32 if io == "f32" else
+                          _lib.MSS_BF16, tokens=tokens, heads=heads, headdim=headdim, dstate=dstate, groups=1, seqs=3,
+                          cache_slots=6)
+    need = _lib.lib().mss_head_scan_prompts_workspace_size(ctypes.byref(a), None)
+    assert need > 0
+    kept = [t.clone() for t in (*v.values(), x, w)]
+
+    def between(*shape, dtype):
+        """A tensor inside a larger one of sevens."""
+        n = math.prod(shape)
+        whole = torch.full((n + 2 * off,), 7, dtype=dtype, device="cuda")
+        return whole, whole[off:off + n].view(shape)
+
+    for cu in ((0, 1200, 0, 1200), (-7, 700, 300, 5000), (5000, 5000, 5000, 5000), (30, 40, 1100, 1150),
+               (1200, 0, 1200, 0), (-(1 << 31), (1 << 31) - 1, -(1 << 31), (1 << 31) - 1)):
+        held = [between(tokens, heads, headdim, dtype=dt), between(6, heads, headdim, dstate, dtype=torch.float32),
+                between(tokens, dim, dtype=dt), between(6, dim, 3, dtype=dt)]
+        work = torch.full((need + 4096,), 7, dtype=torch.uint8, device="cuda")
+        out, state, u, window = (inner for _, inner in held)
+        mss.head_scan_prompts(*v.values(), cu_seqlens=ints(*cu), state=state, slots=slots, out=out, workspace=work)
+        mss.causal_conv1d_prompts(x, w, cu_seqlens=ints(*cu), window=window, slots=slots, out=u)
+        torch.cuda.synchronize()
+        for whole, _ in held:
+            assert (whole[:off] == 7).all() and (whole[-off:] == 7).all(), cu
+        assert (work[need:] == 7).all(), cu
+        for cache in (state, window):
+            assert (cache[1] == 7).all() and (cache[3] == 7).all() and (cache[5] == 7).all(), cu
+        assert all(torch.equal(a, b) for a, b in zip(kept, (*v.values(), x, w))), cu
