@@ -218,3 +218,31 @@ def test_offsets_outside_the_rules_stay_in_their_buffers(mss, off, io):  # noqa:
         for cache in (state, window):
             assert (cache[1] == 7).all() and (cache[3] == 7).all() and (cache[5] == 7).all(), cu
         assert all(torch.equal(a, b) for a, b in zip(kept, (*v.values(), x, w))), cu
+
+
+@pytest.mark.parametrize("quant", [None, "row", "block"])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [256, 4096, 9088])
+def test_norm_of_rows_whose_squares_leave_fp32(mss, dim, io, quant):  # noqa: F811
+    """Rows so large that their squares pass fp32, and, without eps, so small that
+    they vanish, next to ordinary ones: the norm is what it is for any row."""
+    dt, E = DT[io], 2.0 ** -24
+    x = randn(gen(39), 6, dim)
+    for row, size in enumerate((1e19, 1.0, 1e36, 1e-20, 1e-36)):
+        x[row] *= size
+    x[5] = 3e38
+    x, weight = x.to(dt), randn(gen(40), dim)
+    y, _ = ref.rms_norm(x, weight, eps=0.0)
+    got = mss.rms_norm(x, weight, eps=0.0, quant=quant)
+    torch.cuda.synchronize()
+    k = (dim + 8) * E  # the mean square's sum, then a few roundings
+    if quant is None:
+        ref.within(f"norm {dim} {io}", got, y, (k + ref.HALF[dt] * 1.01) * y.abs())
+        return
+    q, scale = got
+    wide = 128 if quant == "block" else dim
+    want = y.unflatten(1, (-1, wide)).abs().amax(2) / 448
+    ref.within(f"norm {dim} {io} {quant} scale", scale.reshape(want.shape), want, 2 * (k + 4 * E) * want)
+    s = ref.d(scale).reshape(want.shape).repeat_interleave(wide, 1)
+    bound = torch.maximum(2.0 ** -4 * y.abs(), 2.0 ** -10 * s) * 1.001
+    ref.within(f"norm {dim} {io} {quant} values", ref.d(q.float()) * s, y, bound)
