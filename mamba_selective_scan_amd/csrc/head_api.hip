@@ -70,21 +70,21 @@ mss_status check_head_shape(int64_t heads, int64_t headdim, int64_t dstate, int6
 // From the sizes alone: the prompts' lengths stay on the device.
 //
 // One long prompt wants as many segments as workgroups can run at once and not
-// one more (24 heads of 64 x 128, 32768 tokens in bf16: 191 us at 480 workgroups
-// of 512, 234 us at 516; a prompt's last segment counts as half a one).  A cut
+// one more (24 heads of 64 x 128, 32768 tokens in bf16: 220 us at 480 workgroups
+// of 512, 249 us at 516; a prompt's last segment counts as half a one).  A cut
 // call makes three passes: it takes more than five chunks to be worth it (320
-// tokens: 25.9 us whole, 28.3 us cut; 512: 38 and 30), on the average of the
+// tokens: 32.1 us whole, 32.3 us cut; 512: 48 and 35), on the average of the
 // prompts, as the lengths are not known here; then segments may be as short as
-// two chunks (2048 tokens: 43 us at 128 tokens a segment, 57 us at 256).  Longer
+// two chunks (2048 tokens: 46 us at 128 tokens a segment, 51 us at 256).  Longer
 // than kSegMax, a batch of equal prompts does not care (8 x 4096 tokens of 80
-// heads: 528 us whole, 535 us at 1024) while one of unequal prompts would wait for
-// its longest (24 prompts, 32768 tokens: 571 us at 1024, 622 us at 2560).
+// heads: 629 us whole, 615 us at 1024) while one of unequal prompts would wait for
+// its longest (24 prompts, 32768 tokens: 664 us at 1024, 737 us at 2560).
 //
-// Tiles of 16 columns do a chunk in two thirds of the time but form its decays
+// Tiles of 16 columns do a chunk in three quarters of the time but form its decays
 // twice: for calls that leave a quarter of the workgroup slots empty at 32 (200
-// tokens of 24 heads: 21.8 us, 27.9 us at 32; 1000 tokens of 80 heads: 49 and 54;
-// 2000 tokens of 80 heads, over that line: 74 and 69) and still run at once (8 x 200
-// tokens of 80 heads, which do not: 55 and 49).
+// tokens of 24 heads: 27.2 us, 35.4 us at 32; 1000 tokens of 80 heads: 55 and 60;
+// 2000 tokens of 80 heads, over that line: 82 and 77) and still run at once (8 x 200
+// tokens of 80 heads, which do not: 62 and 58).
 struct HeadScanPlan {
   bool narrow = false;
   int64_t ptiles, tiles, seg_len = 0, cut_slots = 0, cut_prompts = 0;

@@ -26,24 +26,26 @@
 //
 // bf16 inputs enter the products as they are.  The decayed C B^T and the entering
 // state are split into two bf16 parts where they make y: each term is off by
-// 2^-16 at most, far below y's own rounding (one part alone, in 545 us where this
-// takes 598 on the batch below, left 1.9e-3 of y in place of its rounding's 1.66e-3).  The state itself stays in fp32: its addends
-// delta e^(..) x are split into three bf16 parts (24 bits), so states are
-// as exact as an fp32 sum.  fp32 inputs use the fp32 matrix instruction, with
-// nothing rounded.  The sums c are taken in 64 bits and kept as two floats.
+// 2^-16 at most, far below y's own rounding (one part alone took 545 us where this
+// takes 598, on the batch below, and left y off by 1.9e-3, where its rounding
+// leaves 1.66e-3).  The state itself stays in fp32: its addends delta e^(..) x are
+// split into three bf16 parts (24 bits), so states are as exact as an fp32 sum.
+// fp32 inputs use the fp32 matrix instruction, with nothing rounded.  The sums c
+// are taken in 64 bits and kept as two floats.
 //
 // A prompt longer than a.seg_len is cut into segments: one pass forms what each
 // segment adds to a zero state, one composes the states entering the segments, and
 // the walk then runs all segments at once: the last one's writes the cache entry.
 //
-// What bounds it: instructions.  A chunk of 64 tokens costs a wave 152 MFMAs of 16
-// cycles and 1200 VALU instructions (states of 128; counted); with two waves a SIMD
-// (two workgroups of 80 KB of LDS and 225 registers a CU) the SIMDs issue in 63% of
+// What bounds it: instructions.  A chunk of 64 tokens costs a wave 196 MFMAs of 16
+// cycles and 1450 VALU instructions (states of 128; counted); with two waves a SIMD
+// (two workgroups of 80 KB of LDS and 227 registers a CU) the SIMDs issue in 64% of
 // their cycles, and the waits between a chunk's products take most of the rest.
-// 80 heads of 64 x 128, 8 x 4096 tokens in bf16: 538 us, 160 TFLOP/s of the 4 P N a
-// token that the recurrence needs; 24 heads, one prompt of 32768: 193 us (walk 132,
-// sums 67, states between 15 in a profile); 200 tokens of 24 heads: 22 us, four
-// chunks one after the other.  Measured and not kept: three waves a SIMD for the
+// 80 heads of 64 x 128, 8 x 4096 tokens in bf16: 597 to 616 us from box to box, 140
+// TFLOP/s of the 4 P N a token that the recurrence needs; 24 heads, one prompt of
+// 32768: 217 to 224 us (walk 149, sums 64, states between 16 in a profile); 200
+// tokens of 24 heads: 27 us, four chunks one after the other.  Measured and not
+// kept, before the outputs' operands had two parts: three waves a SIMD for the
 // sums (same time); two parts for the addends of states that only outputs read (one
 // long prompt 4% faster, a short one 4% slower); steps left to the compiler's
 // schedule, without the barriers between them (4% at most).
