@@ -367,7 +367,7 @@ __device__ inline Where find_cut(const HeadScanArgs& a, int at, bool by_prompt) 
 constexpr float kSteep = 60.0f;
 // From here on a value of x, or of C B^T, takes the token-by-token walk, as an
 // infinity does: below it, and with the time steps and growth below, no product
-// that the chunked form makes overflows by itself.
+// that the chunked form makes of a chunk's own tokens overflows by itself.
 constexpr int kLargeExponent = 60;
 // A chunk is walked token by token where a time step lies past kLargeStep (or is
 // not finite: the sums over the tokens would be, and differences of those NaN), a
