@@ -1,7 +1,7 @@
 /*
  * mss.h -- C ABI of libmss, the MI355X (gfx950) Mamba selective-scan library.
  *
- * Ten operations.  The scan forward and backward can also run in reverse
+ * Fourteen operations.  The scan forward and backward can also run in reverse
  * time (mss_scan_args.reverse), the second direction of a bidirectional
  * layer (SpeechLens kernel-optimization notes, the bidirectional variant in
  * its rejected-fusion list):
@@ -103,6 +103,38 @@
  *     with one fp32 scale a row or a block of MSS_SCALE_BLOCK columns; r is
  *     written back as the new residual.
  *
+ *  The operations around the scans of a training step:
+ *
+ * 11. mss_layer_norm_fwd: r = x (+ residual), mean and rstd = 1 / sqrt(var + eps)
+ *     of each row (var = mean((r - mean)^2)), y = (r - mean) rstd weight + bias;
+ *     mean and rstd are kept for the backward.
+ *
+ * 12. mss_layer_norm_bwd: with h = (r - mean) rstd and g = dy weight,
+ *        dr_total = dr + rstd (g - mean(g) - h mean(g h)),
+ *        dweight = sum_rows dy h,  dbias = sum_rows dy,
+ *     where dr is the gradient that reaches r past the norm (0 without it).
+ *     x and residual both have the gradient dr_total.
+ *
+ * 13. mss_linear_loss on one target a row: the softmax cross entropy of hidden
+ *     states x [rows, dim] over a vocabulary weight [vocab, dim], the logits
+ *     never whole in memory:
+ *        z_v = logit_scale x.weight_v;  lse = log sum_v e^{z_v};  loss = lse - z_target;
+ *        dz_v = c (e^{z_v - lse} - [v = target]);
+ *        dx = logit_scale sum_v dz_v weight_v;  dweight_v = logit_scale sum_rows dz_v x,
+ *     the gradients of sum_rows c loss.
+ *
+ * 14. mss_linear_loss on `entries` (id, teacher logit) pairs a row: distillation
+ *     from a teacher's top logits at a temperature tau:
+ *        t_k = softmax over the row's entries of teacher_k / tau;
+ *        z_v = logit_scale x.weight_v / tau;  lse as above;
+ *        loss = tau^2 sum_k t_k (log t_k - z_{id_k} + lse);
+ *        dz_v = c tau^2 (e^{z_v - lse} - sum_{k: id_k = v} t_k),
+ *     dx and dweight with logit_scale / tau.  An id that occurs twice in a row
+ *     has both shares.
+ *     A target or id outside [0, vocab) does not count; a row without one that
+ *     does gives loss, lse and dx 0 and adds nothing to dweight, whatever its x,
+ *     teacher and row weight hold.
+ *
  * Conventions shared by every entry point
  *  - All tensor pointers are DEVICE pointers owned by the caller.  The library
  *    never allocates, frees or retains caller memory and keeps no per-call
@@ -145,7 +177,7 @@
 extern "C" {
 #endif
 
-#define MSS_ABI_VERSION 6
+#define MSS_ABI_VERSION 7
 
 /* Chunk states: the state entering every MSS_STATE_CHUNK-step chunk of
  * logical time, fp32, laid out [ceil(L / MSS_STATE_CHUNK)][b][d][MSS_MAX_DSTATE]
@@ -158,6 +190,7 @@ extern "C" {
 #define MSS_MAX_CONV_WIDTH 4
 #define MSS_MAX_HEAD_DSTATE 128
 #define MSS_SCALE_BLOCK 128
+#define MSS_MAX_LOSS_ENTRIES 1024
 
 /* Device scratch that mss_selective_scan_fwd_noalloc holds per GPU (16 MiB):
  * enough for the time-segment carries of any shape (at most 6.3 MB, for
@@ -645,6 +678,89 @@ typedef struct mss_norm_args {
     int32_t reserved0;           /* must be 0                                            */
 } mss_norm_args;
 
+/* Arguments of mss_layer_norm_fwd.  Set struct_size = sizeof(mss_layer_norm_args). */
+typedef struct mss_layer_norm_args {
+    uint32_t struct_size;
+    int32_t io_dtype;            /* mss_dtype of x and out                               */
+    int32_t residual_dtype;      /* mss_dtype of residual and residual_out               */
+    int32_t reserved0;           /* must be 0                                            */
+    int64_t rows;                /* >= 1                                                 */
+    int64_t dim;                 /* columns, 1..32768                                    */
+    const void *x;               /* [r,d], unit stride in d                              */
+    int64_t x_stride;
+    const void *residual;        /* [r,d], unit stride in d; NULL means 0                */
+    int64_t residual_stride;
+    const float *weight;         /* [d] fp32 contiguous                                  */
+    const float *bias;           /* [d] fp32 contiguous; NULL means 0                    */
+    void *out;                   /* [r,d] io_dtype, unit stride in d                     */
+    int64_t out_stride;
+    float *mean;                 /* [r] fp32 contiguous; NULL: not written               */
+    float *rstd;                 /* [r] fp32 contiguous; NULL: not written               */
+    void *residual_out;          /* [r,d]: x + residual; may be `residual` itself (same  */
+    int64_t residual_out_stride; /* stride); NULL: not written                           */
+    float eps;                   /* >= 0                                                 */
+    int32_t reserved1;           /* must be 0                                            */
+} mss_layer_norm_args;
+
+/* Arguments of mss_layer_norm_bwd.  Set struct_size = sizeof(mss_layer_norm_bwd_args). */
+typedef struct mss_layer_norm_bwd_args {
+    uint32_t struct_size;
+    int32_t io_dtype;            /* mss_dtype of dy and dx                               */
+    int32_t r_dtype;             /* mss_dtype of r, dr and dresidual                     */
+    int32_t reserved0;           /* must be 0                                            */
+    int64_t rows;                /* >= 1                                                 */
+    int64_t dim;                 /* columns, 1..32768                                    */
+    const void *dy;              /* [r,d], unit stride in d                              */
+    int64_t dy_stride;
+    const void *r;               /* [r,d] what the forward normed, unit stride in d      */
+    int64_t r_stride;
+    const void *dr;              /* [r,d], unit stride in d; NULL means 0                */
+    int64_t dr_stride;
+    const float *weight;         /* [d] fp32 contiguous                                  */
+    const float *mean;           /* [r] fp32 contiguous                                  */
+    const float *rstd;           /* [r] fp32 contiguous                                  */
+    void *dx;                    /* [r,d] io_dtype, unit stride in d; NULL: not written  */
+    int64_t dx_stride;
+    void *dresidual;             /* [r,d] r_dtype, unit stride in d; NULL: not written   */
+    int64_t dresidual_stride;
+    float *dweight;              /* [d] fp32 contiguous; NULL: not written               */
+    float *dbias;                /* [d] fp32 contiguous; NULL: not written               */
+    void *workspace;             /* mss_layer_norm_bwd_workspace_size bytes, 256-aligned */
+    size_t workspace_bytes;
+} mss_layer_norm_bwd_args;
+
+/* Arguments of mss_linear_loss.  Set struct_size = sizeof(mss_linear_loss_args). */
+typedef struct mss_linear_loss_args {
+    uint32_t struct_size;
+    int32_t io_dtype;            /* mss_dtype of x, weight, dx and dweight               */
+    int64_t rows;                /* 0..2^24                                              */
+    int64_t dim;                 /* 1..32768                                             */
+    int64_t vocab;               /* 1..2^22                                              */
+    int64_t entries;             /* 1..MSS_MAX_LOSS_ENTRIES; 1 without teacher           */
+    const void *x;               /* [r,d], unit stride in d                              */
+    int64_t x_stride;
+    const void *weight;          /* [v,d], unit stride in d                              */
+    int64_t weight_stride;
+    const int64_t *ids;          /* [r,k] targets, or ids of the teacher's logits        */
+    int64_t ids_stride[2];
+    const void *teacher;         /* [r,k] logits; NULL: cross entropy                    */
+    int64_t teacher_stride[2];
+    int32_t teacher_dtype;       /* mss_dtype of teacher                                 */
+    float logit_scale;           /* finite                                               */
+    float temperature;           /* finite, > 0; 1 without teacher                       */
+    int32_t reserved0;           /* must be 0                                            */
+    const float *row_weight;     /* [r] c, fp32 contiguous; NULL: 1 / (rows that count)  */
+    float *loss;                 /* [r] fp32 contiguous                                  */
+    float *lse;                  /* [r] fp32 contiguous                                  */
+    float *total;                /* [1] sum of c loss; NULL: not written                 */
+    void *dx;                    /* [r,d], unit stride in d; NULL: not computed          */
+    int64_t dx_stride;
+    void *dweight;               /* [v,d], unit stride in d; NULL: not computed          */
+    int64_t dweight_stride;
+    void *workspace;             /* mss_linear_loss_workspace_size bytes, 256-aligned    */
+    size_t workspace_bytes;
+} mss_linear_loss_args;
+
 /* Conv over packed prompts (see the top of this file).  Channel-last rows with
  * aligned vectors move whole vectors; any non-negative strides are accepted.
  * out must not overlap any input; window is the only in/out buffer.  Each
@@ -673,6 +789,36 @@ mss_status mss_head_scan_step(const mss_head_step_args *args, void *stream);
  * infinity or a NaN gives NaN wherever the formula does.  Only residual_out may overlap an input, and only by being
  * `residual`. */
 mss_status mss_rms_norm(const mss_norm_args *args, void *stream);
+
+/* Layer norm (see the top of this file).  The sum x + residual is taken in
+ * fp32; the statistics, and y, come from the unrounded sum.  Only residual_out
+ * may overlap an input, and only by being `residual`. */
+mss_status mss_layer_norm_fwd(const mss_layer_norm_args *args, void *stream);
+
+/* Bytes of device workspace mss_layer_norm_bwd needs (0 where neither dweight
+ * nor dbias is wanted).  Depends only on rows, dim and which of the two are
+ * not NULL.  Returns 0 and sets *status (if not NULL) on invalid sizes. */
+size_t mss_layer_norm_bwd_workspace_size(const mss_layer_norm_bwd_args *args, mss_status *status);
+
+/* Layer norm's backward (see the top of this file).  Sums over rows are fp32
+ * in a fixed order.  Outputs must not overlap inputs or each other. */
+mss_status mss_layer_norm_bwd(const mss_layer_norm_bwd_args *args, void *stream);
+
+/* Bytes of device workspace mss_linear_loss needs.  Depends only on the sizes,
+ * dtypes, the alignment of weight and which of dx and dweight are not NULL.
+ * Returns 0 and sets *status (if not NULL) on invalid sizes. */
+size_t mss_linear_loss_workspace_size(const mss_linear_loss_args *args, mss_status *status);
+
+/* Cross entropy or distillation over a vocabulary, with the gradients that are
+ * not NULL (see the top of this file).  Which rows count is read on the device
+ * only.  Sums are fp32 in a fixed order.  Outputs must not overlap inputs or
+ * each other.  A call's workspace is its own until the call has run. */
+mss_status mss_linear_loss(const mss_linear_loss_args *args, void *stream);
+
+/* out[i] = in[i] * *factor over n elements of `dtype` in n contiguous elements
+ * each: a gradient times the factor that reaches it, read on the device. */
+mss_status mss_scale(const void *in, const float *factor, void *out, int64_t n, int32_t dtype,
+                     void *stream);
 
 #ifdef __cplusplus
 }

@@ -24,6 +24,13 @@ packed prompts, caches by slot) are in heads.py:
     y = head_scan_step(states, windows, xbc, dt_raw, A_log, weight, bias, D, z, dt_bias)
     q, scale, residual = rms_norm(x, weight, residual=residual, quant="row")
 
+The operations around the scans of a training step (layer norm, and the losses
+over a vocabulary, with their gradients) are in training.py:
+
+    y, r = layer_norm(x, weight, bias, residual)                       # autograd
+    loss = linear_cross_entropy(x, vocab_weight, targets)              # autograd
+    loss = linear_distillation(x, vocab_weight, ids, teacher, temperature=2.0)
+
 Shapes (logical index order, any strides): u, delta_raw, z, out [B, D, L];
 B, C [B, N, L]; A_log [D, N]; D, dt_bias [D]; states [B, D, N] (fp32,
 contiguous).  A channel-last [B, L, D] buffer is passed as its transpose(1, 2)
@@ -44,17 +51,27 @@ __all__ = ["selective_scan_fwd", "selective_scan_fwd_noalloc", "selective_state_
            "causal_conv1d_fwd", "causal_conv1d_update", "selective_scan_bwd",
            "scan_bwd_workspace_size", "selective_scan", "selective_scan_fwd_complex",
            "scan_complex_workspace_size", "causal_conv1d_prompts", "head_scan_prompts",
-           "head_scan_step", "rms_norm", "MssError", "MSS_MAX_DSTATE", "library_path"]
+           "head_scan_step", "rms_norm", "layer_norm_fwd", "layer_norm_bwd", "layer_norm",
+           "linear_cross_entropy_fwd", "linear_cross_entropy_grad", "linear_cross_entropy",
+           "linear_distillation_fwd", "linear_distillation_grad", "linear_distillation", "MssError", "MSS_MAX_DSTATE", "library_path"]
 
 _HEAD_OPS = ("causal_conv1d_prompts", "head_scan_prompts", "head_scan_step", "rms_norm")
+_TRAINING_OPS = ("layer_norm_fwd", "layer_norm_bwd", "layer_norm", "linear_cross_entropy_fwd",
+                 "linear_cross_entropy_grad", "linear_cross_entropy", "linear_distillation_fwd",
+                 "linear_distillation_grad", "linear_distillation")
 
 
 def __getattr__(name):
-    # the head-wise operations live in a module that imports torch: loaded on
-    # first use, so that importing this one does not
+    # the head-wise operations and those around a training step's scans live in
+    # modules that import torch: loaded on first use, so that importing this one
+    # does not
     if name in _HEAD_OPS:
         from . import heads
         globals().update({n: getattr(heads, n) for n in _HEAD_OPS})
+        return globals()[name]
+    if name in _TRAINING_OPS:
+        from . import training
+        globals().update({n: getattr(training, n) for n in _TRAINING_OPS})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

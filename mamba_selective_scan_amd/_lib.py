@@ -14,12 +14,13 @@ import struct
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmss.so")
 
-MSS_ABI_VERSION = 6
+MSS_ABI_VERSION = 7
 MSS_MAX_DSTATE = 16
 MSS_STATE_CHUNK = 16
 MSS_MAX_CONV_WIDTH = 4
 MSS_MAX_HEAD_DSTATE = 128
 MSS_SCALE_BLOCK = 128
+MSS_MAX_LOSS_ENTRIES = 1024
 MSS_NOALLOC_SCRATCH_BYTES = 16 << 20
 MSS_F32 = 0
 MSS_BF16 = 1
@@ -51,7 +52,9 @@ EXPORTS = ("mss_abi_version", "mss_status_string", "mss_selective_scan_workspace
            "mss_selective_scan_bwd", "mss_selective_scan_fwd_complex",
            "mss_selective_scan_fwd_noalloc", "mss_selective_scan_fwd_complex_workspace_size",
            "mss_causal_conv1d_prompts", "mss_head_scan_prompts",
-           "mss_head_scan_prompts_workspace_size", "mss_head_scan_step", "mss_rms_norm")
+           "mss_head_scan_prompts_workspace_size", "mss_head_scan_step", "mss_rms_norm",
+           "mss_layer_norm_fwd", "mss_layer_norm_bwd", "mss_layer_norm_bwd_workspace_size",
+           "mss_linear_loss", "mss_linear_loss_workspace_size", "mss_scale")
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -282,6 +285,54 @@ class NormArgs(ctypes.Structure):
     ]
 
 
+class LayerNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("io_dtype", _i32), ("residual_dtype", _i32),
+        ("reserved0", _i32),
+        ("rows", _i64), ("dim", _i64),
+        ("x", _vp), ("x_stride", _i64),
+        ("residual", _vp), ("residual_stride", _i64),
+        ("weight", _vp), ("bias", _vp),
+        ("out", _vp), ("out_stride", _i64),
+        ("mean", _vp), ("rstd", _vp),
+        ("residual_out", _vp), ("residual_out_stride", _i64),
+        ("eps", ctypes.c_float), ("reserved1", _i32),
+    ]
+
+
+class LayerNormBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("io_dtype", _i32), ("r_dtype", _i32),
+        ("reserved0", _i32),
+        ("rows", _i64), ("dim", _i64),
+        ("dy", _vp), ("dy_stride", _i64),
+        ("r", _vp), ("r_stride", _i64),
+        ("dr", _vp), ("dr_stride", _i64),
+        ("weight", _vp), ("mean", _vp), ("rstd", _vp),
+        ("dx", _vp), ("dx_stride", _i64),
+        ("dresidual", _vp), ("dresidual_stride", _i64),
+        ("dweight", _vp), ("dbias", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class LinearLossArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("io_dtype", _i32),
+        ("rows", _i64), ("dim", _i64), ("vocab", _i64), ("entries", _i64),
+        ("x", _vp), ("x_stride", _i64),
+        ("weight", _vp), ("weight_stride", _i64),
+        ("ids", _vp), ("ids_stride", _i64 * 2),
+        ("teacher", _vp), ("teacher_stride", _i64 * 2),
+        ("teacher_dtype", _i32), ("logit_scale", ctypes.c_float),
+        ("temperature", ctypes.c_float), ("reserved0", _i32),
+        ("row_weight", _vp), ("loss", _vp), ("lse", _vp), ("total", _vp),
+        ("dx", _vp), ("dx_stride", _i64),
+        ("dweight", _vp), ("dweight_stride", _i64),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def packer(cls):
     """A function that makes a ``cls`` from its fields' values in order, without
     struct_size (arrays flattened, 0 for a null pointer): one call of struct
@@ -351,6 +402,20 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.mss_head_scan_step.restype = ctypes.c_int
     lib.mss_rms_norm.argtypes = [ctypes.POINTER(NormArgs), _vp]
     lib.mss_rms_norm.restype = ctypes.c_int
+    lib.mss_layer_norm_fwd.argtypes = [ctypes.POINTER(LayerNormArgs), _vp]
+    lib.mss_layer_norm_fwd.restype = ctypes.c_int
+    lib.mss_layer_norm_bwd_workspace_size.argtypes = [ctypes.POINTER(LayerNormBwdArgs),
+                                                      ctypes.POINTER(ctypes.c_int)]
+    lib.mss_layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.mss_layer_norm_bwd.argtypes = [ctypes.POINTER(LayerNormBwdArgs), _vp]
+    lib.mss_layer_norm_bwd.restype = ctypes.c_int
+    lib.mss_linear_loss_workspace_size.argtypes = [ctypes.POINTER(LinearLossArgs),
+                                                   ctypes.POINTER(ctypes.c_int)]
+    lib.mss_linear_loss_workspace_size.restype = ctypes.c_size_t
+    lib.mss_linear_loss.argtypes = [ctypes.POINTER(LinearLossArgs), _vp]
+    lib.mss_linear_loss.restype = ctypes.c_int
+    lib.mss_scale.argtypes = [_vp, _vp, _vp, _i64, _i32, _vp]
+    lib.mss_scale.restype = ctypes.c_int
     return lib
 
 

@@ -1,0 +1,296 @@
+// layer_norm.hip -- layer norm with the residual's addition, and its backward
+// with the reduction of the weight's and the bias's gradients, gfx950.
+//
+//   r = x + residual;  y = (r - mean) rstd weight + bias
+//   h = (r - mean) rstd;  g = dy weight
+//   dr_total = dr + rstd (g - mean(g) - h mean(g h));  dweight = sum dy h;  dbias = sum dy
+//
+// Streams: every input is read once and every output written once, so both are
+// bound by HBM bandwidth.  A row stays in registers between its sums and its
+// output.  A lane owns 8 adjacent columns.
+#include "mss.h"
+#include "mss_train.hpp"
+
+namespace mss {
+namespace {
+
+constexpr int kV = 8;
+
+__device__ inline float wave_sum(float v) {
+  v = row_sum16(v);
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// Two sums over the TPR threads of a row, left in all of them.  `buf` holds two
+// floats a wave; calls that follow each other alternate between two of them, so
+// that one barrier a call is enough.
+template <int TPR>
+__device__ inline void row_sums(float& a, float& b, float2* buf) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) {
+      a += buf[i].x;
+      b += buf[i].y;
+    }
+  }
+}
+
+// A mean square below kFewBits may have lost addends, and one past fp32 is
+// infinite: such rows are scaled towards 1 by a power of two, as the
+// root-mean-square norm's are.
+constexpr float kFewBits = 0x1p-80f, kScaleUp = 0x1p75f;
+
+// TPR threads a row, K vectors a thread.
+template <typename IO, typename RES, int TPR, int K>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void fwd_kernel(LayerNormArgs a) {
+  constexpr int kBlock = TPR < 256 ? 256 : TPR;
+  __shared__ float2 buf[4][TPR > 64 ? TPR / 64 : 1];
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kBlock / TPR) + threadIdx.x / TPR;
+  if (TPR == 64 && row >= a.rows) return;  // (whole waves; never with barriers)
+  const int tid = threadIdx.x % TPR;
+  const IO* x = static_cast<const IO*>(a.x) + row * a.sx;
+  const RES* res = static_cast<const RES*>(a.res) + row * a.sr;
+  float r[K][kV];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * TPR + tid) * kV;
+    load_part<IO, kV>(x + c, a.dim - c, r[k]);
+  }
+  if (a.res != nullptr) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + tid) * kV;
+      float q[kV];
+      load_part<RES, kV>(res + c, a.dim - c, q);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) r[k][i] += q[i];
+    }
+  }
+  if (a.res_out != nullptr) {
+    RES* ro = static_cast<RES*>(a.res_out) + row * a.sro;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + tid) * kV;
+      store_part<RES, kV>(ro + c, a.dim - c, r[k]);
+    }
+  }
+  const float n = static_cast<float>(a.dim);
+  // The first mean is rounded; what it misses (`rest`, about half a bit of it)
+  // is found with the squares and taken out of both.
+  float mean, rest, var;
+  auto statistics = [&](float by, int at) __attribute__((always_inline)) {
+    float s = 0.0f, unused = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < kV; ++i) s += r[k][i] * by;
+    row_sums<TPR>(s, unused, buf[at]);
+    mean = s / n;
+    float d1 = 0.0f, d2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + tid) * kV;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const float d = c + i < a.dim ? fmaf(r[k][i], by, -mean) : 0.0f;
+        d1 += d;
+        d2 = fmaf(d, d, d2);
+      }
+    }
+    row_sums<TPR>(d1, d2, buf[at + 1]);
+    rest = d1 / n;
+    var = fmaxf(d2 / n - rest * rest, 0.0f) + (d2 - d2);  // (fmax drops a NaN, the sum keeps it)
+  };
+  statistics(1.0f, 0);
+  float by = 1.0f, spread = var + a.eps;
+  if (!(spread < INFINITY) || spread < kFewBits || !(fabsf(mean) < INFINITY)) {
+    by = spread < kFewBits ? kScaleUp : 1.0f / kScaleUp;
+    statistics(by, 2);
+    spread = var + a.eps * by * by;
+  }
+  const float inv = 1.0f / sqrtf(spread);  // of the row times `by`
+  if (tid == 0) {
+    if (a.mean != nullptr) a.mean[row] = (mean + rest) / by;
+    if (a.rstd != nullptr) a.rstd[row] = inv * by;
+  }
+  IO* out = static_cast<IO*>(a.out) + row * a.so;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * TPR + tid) * kV;
+    float w[kV], b[kV] = {};
+    load_part<float, kV>(a.weight + c, a.dim - c, w);
+    if (a.bias != nullptr) load_part<float, kV>(a.bias + c, a.dim - c, b);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) b[i] = fmaf((fmaf(r[k][i], by, -mean) - rest) * inv, w[i], b[i]);
+    store_part<IO, kV>(out + c, a.dim - c, b);
+  }
+}
+
+template <typename IO, typename RES>
+hipError_t launch_fwd(const LayerNormArgs& a, hipStream_t stream) {
+  const int d = a.dim;
+  const unsigned by4 = static_cast<unsigned>((a.rows + 3) / 4), by1 = static_cast<unsigned>(a.rows);
+  if (d <= 512) fwd_kernel<IO, RES, 64, 1><<<by4, 256, 0, stream>>>(a);
+  else if (d <= 1024) fwd_kernel<IO, RES, 64, 2><<<by4, 256, 0, stream>>>(a);
+  else if (d <= 2048) fwd_kernel<IO, RES, 64, 4><<<by4, 256, 0, stream>>>(a);
+  else if (d <= 4096) fwd_kernel<IO, RES, 256, 2><<<by1, 256, 0, stream>>>(a);
+  else if (d <= 8192) fwd_kernel<IO, RES, 256, 4><<<by1, 256, 0, stream>>>(a);
+  else if (d <= 16384) fwd_kernel<IO, RES, 1024, 2><<<by1, 1024, 0, stream>>>(a);
+  else fwd_kernel<IO, RES, 1024, 4><<<by1, 1024, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+// One workgroup walks rows blockIdx.x * (rows a pass), ... and keeps the sums of
+// its columns in registers.  LEAN: a row is read again (from the caches) for its
+// output instead of being kept, which leaves the registers to the sums.
+template <typename IO, typename RES, int TPR, int K, bool LEAN>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void bwd_kernel(LayerNormBwdArgs a) {
+  constexpr int kBlock = TPR < 256 ? 256 : TPR;
+  constexpr int kRows = kBlock / TPR;  // rows a pass
+  __shared__ float2 buf[2][TPR > 64 ? TPR / 64 : 1];
+  const int tid = threadIdx.x % TPR;
+  float dw[K][kV] = {}, db[K][kV] = {};
+  const float n = static_cast<float>(a.dim);
+  int at = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR; row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows) {
+    const IO* dyp = static_cast<const IO*>(a.dy) + row * a.sdy;
+    const RES* rp = static_cast<const RES*>(a.r) + row * a.sr;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float dy[LEAN ? 1 : K][kV], h[LEAN ? 1 : K][kV];
+    float s1 = 0.0f, s2 = 0.0f;
+    auto load = [&](int k, float* y, float* x) __attribute__((always_inline)) {
+      const int c = (k * TPR + tid) * kV;
+      load_part<IO, kV>(dyp + c, a.dim - c, y);
+      load_part<RES, kV>(rp + c, a.dim - c, x);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) x[i] = c + i < a.dim ? (x[i] - mean) * rstd : 0.0f;
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + tid) * kV, o = LEAN ? 0 : k;
+      load(k, dy[o], h[o]);
+      float w[kV];
+      load_part<float, kV>(a.weight + c, a.dim - c, w);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const float g = dy[o][i] * w[i];
+        s1 += g;
+        s2 = fmaf(g, h[o][i], s2);
+        dw[k][i] = fmaf(dy[o][i], h[o][i], dw[k][i]);
+        db[k][i] += dy[o][i];
+      }
+    }
+    if (a.dx == nullptr && a.dres == nullptr) continue;
+    row_sums<TPR>(s1, s2, buf[at]);
+    at ^= 1;
+    s1 /= n;
+    s2 /= n;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + tid) * kV, o = LEAN ? 0 : k;
+      if (LEAN) load(k, dy[o], h[o]);
+      float w[kV], q[kV] = {};
+      load_part<float, kV>(a.weight + c, a.dim - c, w);
+      if (a.dr != nullptr)
+        load_part<RES, kV>(static_cast<const RES*>(a.dr) + row * a.sdr + c, a.dim - c, q);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) q[i] = fmaf(rstd, dy[o][i] * w[i] - s1 - h[o][i] * s2, q[i]);
+      if (a.dx != nullptr) store_part<IO, kV>(static_cast<IO*>(a.dx) + row * a.sdx + c, a.dim - c, q);
+      if (a.dres != nullptr) store_part<RES, kV>(static_cast<RES*>(a.dres) + row * a.sdres + c, a.dim - c, q);
+    }
+  }
+  if (a.dweight == nullptr && a.dbias == nullptr) return;
+  if constexpr (kRows > 1) {
+    // the waves' sums meet in a fixed order
+    __shared__ float meet[kRows][K * 64 * kV];
+    auto join = [&](float (&v)[K][kV]) __attribute__((always_inline)) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < kV; ++i) meet[threadIdx.x / TPR][(k * kV + i) * 64 + tid] = v[k][i];
+      __syncthreads();
+      if (threadIdx.x < TPR)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < kV; ++i) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) s += meet[q][(k * kV + i) * 64 + tid];
+            v[k][i] = s;
+          }
+    };
+    join(dw);
+    join(db);
+    if (threadIdx.x >= TPR) return;
+  }
+  float* sw = a.sums + static_cast<int64_t>(blockIdx.x) * a.dim;
+  float* sb = sw + static_cast<int64_t>(gridDim.x) * a.dim;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * TPR + tid) * kV;
+    store_part<float, kV>(sw + c, a.dim - c, dw[k]);
+    store_part<float, kV>(sb + c, a.dim - c, db[k]);
+  }
+}
+
+// The workgroups' sums of 64 columns: 4 threads a column, each over every fourth.
+__global__ __launch_bounds__(256) void bwd_sum_kernel(LayerNormBwdArgs a) {
+  __shared__ float meet[4][64];
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  float* out = blockIdx.y == 0 ? a.dweight : a.dbias;
+  if (out == nullptr) return;
+  const float* p = a.sums + static_cast<int64_t>(blockIdx.y) * a.parts * a.dim + c;
+  float s = 0.0f;
+  if (c < a.dim)
+    for (int i = q; i < a.parts; i += 4) s += p[static_cast<int64_t>(i) * a.dim];
+  meet[q][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (q == 0 && c < a.dim)
+    out[c] = (meet[0][threadIdx.x] + meet[1][threadIdx.x]) + (meet[2][threadIdx.x] + meet[3][threadIdx.x]);
+}
+
+template <typename IO, typename RES>
+hipError_t launch_bwd(const LayerNormBwdArgs& a, hipStream_t stream) {
+  const int d = a.dim;
+  const unsigned g = static_cast<unsigned>(a.parts);
+  if (d <= 512) bwd_kernel<IO, RES, 64, 1, false><<<g, 256, 0, stream>>>(a);
+  else if (d <= 1024) bwd_kernel<IO, RES, 64, 2, false><<<g, 256, 0, stream>>>(a);
+  else if (d <= 2048) bwd_kernel<IO, RES, 256, 1, false><<<g, 256, 0, stream>>>(a);
+  else if (d <= 4096) bwd_kernel<IO, RES, 256, 2, false><<<g, 256, 0, stream>>>(a);
+  else if (d <= 8192) bwd_kernel<IO, RES, 256, 4, false><<<g, 256, 0, stream>>>(a);
+  else if (d <= 16384) bwd_kernel<IO, RES, 1024, 2, false><<<g, 1024, 0, stream>>>(a);
+  else bwd_kernel<IO, RES, 1024, 4, true><<<g, 1024, 0, stream>>>(a);
+  if (a.dweight != nullptr || a.dbias != nullptr)
+    bwd_sum_kernel<<<dim3(static_cast<unsigned>((d + 63) / 64), 2), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int layer_norm_bwd_parts(int64_t rows, int64_t dim) {
+  const int64_t pass = dim <= 1024 ? 4 : 1;  // rows a workgroup takes at a time
+  const int64_t most = dim <= 8192 ? 1024 : 512;
+  const int64_t n = (rows + pass - 1) / pass;
+  return static_cast<int>(n < most ? n : most);
+}
+
+hipError_t launch_layer_norm(const LayerNormArgs& a, bool io_bf16, bool res_bf16, hipStream_t stream) {
+  if (io_bf16) return res_bf16 ? launch_fwd<bf16_t, bf16_t>(a, stream) : launch_fwd<bf16_t, float>(a, stream);
+  return res_bf16 ? launch_fwd<float, bf16_t>(a, stream) : launch_fwd<float, float>(a, stream);
+}
+
+hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, bool io_bf16, bool r_bf16, hipStream_t stream) {
+  if (io_bf16) return r_bf16 ? launch_bwd<bf16_t, bf16_t>(a, stream) : launch_bwd<bf16_t, float>(a, stream);
+  return r_bf16 ? launch_bwd<float, bf16_t>(a, stream) : launch_bwd<float, float>(a, stream);
+}
+
+}  // namespace mss

@@ -1,0 +1,102 @@
+// mss_train.hpp -- shapes and pointers of the operations around the scans of a
+// training step: layer norm and its backward, the losses over a vocabulary.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mss_head.hpp"
+
+namespace mss {
+
+struct LayerNormArgs {
+  int64_t rows;
+  int dim;
+  int64_t sx, sr, so, sro;
+  float eps;
+  const void* x;
+  const void* res;
+  const float* weight;
+  const float* bias;
+  void* out;
+  float* mean;
+  float* rstd;
+  void* res_out;
+};
+
+struct LayerNormBwdArgs {
+  int64_t rows;
+  int dim;
+  int parts;  // workgroups, each with its own sums over its rows
+  int64_t sdy, sr, sdr, sdx, sdres;
+  const void* dy;
+  const void* r;
+  const void* dr;
+  const float* weight;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  void* dres;
+  float* dweight;
+  float* dbias;
+  float* sums;  // workspace [2][parts][dim]
+};
+
+hipError_t launch_layer_norm(const LayerNormArgs& a, bool io_bf16, bool res_bf16, hipStream_t stream);
+int layer_norm_bwd_parts(int64_t rows, int64_t dim);
+hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, bool io_bf16, bool r_bf16, hipStream_t stream);
+
+// ---------------------------------------------------------------- losses
+
+constexpr int kLossVocabTile = 64;  // vocabulary entries that share a maximum
+
+struct LossArgs {
+  int rows, dim, vocab, entries;
+  int64_t sx, sw, sids[2], steach[2], sdx, sdw;
+  const void* x;
+  const void* weight;
+  const int64_t* ids;
+  const void* teacher;  // null: cross entropy
+  bool teacher_bf16;
+  const float* row_weight;
+  float inv_tau;   // 1 / temperature
+  float scale2;    // logit_scale / temperature * log2 e: x.w to logits in powers of two
+  float back;      // logit_scale * temperature: dz's factor before c
+  float tau2;      // temperature^2
+  float* loss;
+  float* lse;
+  float* total;
+  void* dx;
+  void* dweight;
+  // workspace
+  int* live;       // [1] rows that count
+  int* row_of;     // [rows] row of the i-th of them
+  int* place;      // [rows] the i of a row, or -1
+  uint8_t* counts; // [rows] whether it counts
+  float* share;    // [rows][entries] t_k by row (teacher only)
+  float* known;    // [rows] sum_k t_k log t_k (teacher only)
+  float* picked;   // [rows][entries] z_{id_k} log2 e of the i-th row that counts
+  // rows and weights as bf16 operands: one plane, or three whose sum is the fp32 value
+  uint16_t* xp;    // [planes][rows][dpad]
+  uint16_t* wp;    // [planes][vocab][dpad], or the weight itself
+  int planes;
+  int64_t dpad, wp_stride, wp_plane;
+  bool pack_w;
+  // of a piece of rows
+  int piece;       // rows of a piece
+  int pieces;
+  int tiles;       // vocabulary tiles
+  int64_t vpad;
+  float2* stats;   // [piece][tiles] exponent R and sum of 2^(z2 - R)
+  void* probs;     // [piece][vpad] codes of z2 (bf16), or z2 (fp32)
+  uint16_t* dz;    // [planes][piece][vpad] (bf16: probs itself)
+  float* part;     // [splits][piece][dpad]
+  int splits;
+  float* dw_sum;   // [vocab][dpad] (more than one piece)
+};
+
+hipError_t launch_loss(const LossArgs& a, bool io_bf16, hipStream_t stream);
+hipError_t launch_scale(const void* in, const float* factor, void* out, int64_t n, bool bf16,
+                        hipStream_t stream);
+
+}  // namespace mss

@@ -1,0 +1,339 @@
+// train_api.hip -- the C ABI of the operations around the scans of a training
+// step: argument checks, launch planning and stream-ordered enqueue.  As in
+// mss_api.hip, every check runs on the host before any HIP call.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "mss.h"
+#include "mss_checks.hpp"
+#include "mss_train.hpp"
+
+namespace {
+
+using mss::Extent;
+using mss::aligned;
+using mss::extent_of;
+using mss::overlaps;
+
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;  // of a launch
+constexpr int64_t kMaxNormDim = 32768;
+const int64_t kOne[1] = {1};
+
+bool bad_dtype(int32_t t) { return t != MSS_F32 && t != MSS_BF16; }
+int64_t elem(int32_t t) { return t == MSS_BF16 ? 2 : 4; }
+Extent vec(const void* p, int64_t n, int64_t es) { return extent_of(p, &n, kOne, 1, es); }
+Extent mat(const void* p, int64_t rows, int64_t cols, int64_t stride, int64_t es) {
+  const int64_t sz[2] = {rows, cols}, st[2] = {stride, 1};
+  return extent_of(p, sz, st, 2, es);
+}
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// No output overlaps an input or another output.
+template <size_t I, size_t O>
+bool apart(const Extent (&ins)[I], const Extent (&outs)[O]) {
+  for (size_t o = 0; o < O; ++o) {
+    for (const Extent& e : ins)
+      if (overlaps(outs[o], e)) return false;
+    for (size_t q = 0; q < o; ++q)
+      if (overlaps(outs[o], outs[q])) return false;
+  }
+  return true;
+}
+
+// Rows at any distance for an input, one behind another for an output.
+bool out_stride_ok(const void* p, int64_t rows, int64_t cols, int64_t stride) {
+  return p == nullptr || rows <= 1 || stride >= cols;
+}
+
+bool norm_sizes_ok(int64_t rows, int64_t dim) {
+  return rows >= 1 && rows < (int64_t{1} << 31) && dim >= 1 && dim <= kMaxNormDim &&
+         rows <= kMaxThreads / (dim <= 2048 ? 64 : dim <= 8192 ? 256 : 1024) - 3;
+}
+
+mss_status check_norm_bwd_shape(const mss_layer_norm_bwd_args* a) {
+  if (a == nullptr || a->struct_size != sizeof(mss_layer_norm_bwd_args) || a->reserved0 != 0)
+    return MSS_ERR_BAD_STRUCT;
+  if (bad_dtype(a->io_dtype) || bad_dtype(a->r_dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
+  return norm_sizes_ok(a->rows, a->dim) ? MSS_OK : MSS_ERR_BAD_SHAPE;
+}
+
+size_t norm_bwd_workspace(const mss_layer_norm_bwd_args* a) {
+  if (a->dweight == nullptr && a->dbias == nullptr) return 0;
+  return static_cast<size_t>(mss::layer_norm_bwd_parts(a->rows, a->dim) * a->dim * 2) * 4;
+}
+
+// How a loss is cut: rows in pieces whose dz stays within kPieceBytes, and the
+// dx product over the vocabulary.
+constexpr int64_t kPieceBytes = int64_t{1} << 30;
+
+struct LossPlan {
+  bool grad, pack_w;
+  int64_t planes, dpad, vpad, tiles, piece, pieces, splits;
+  size_t live, row_of, place, counts, share, known, picked, xp, wp, stats, probs, dz, part, dw_sum, bytes;
+};
+
+LossPlan loss_plan(const mss_linear_loss_args* a) {
+  LossPlan p{};
+  const bool f32 = a->io_dtype == MSS_F32;
+  p.grad = a->dx != nullptr || a->dweight != nullptr;
+  p.planes = f32 ? 3 : 1;
+  p.dpad = up(a->dim, 64);
+  p.vpad = up(a->vocab, 256);
+  p.tiles = (a->vocab + mss::kLossVocabTile - 1) / mss::kLossVocabTile;
+  // bf16 weights are read where they are if their rows are whole 16-byte vectors
+  p.pack_w = f32 || a->dim % 8 != 0 || !aligned(a->weight, 16) || (a->vocab > 1 && a->weight_stride % 8 != 0);
+  const int64_t a_row = p.tiles * 8 + (p.grad ? p.vpad * (f32 ? 10 : 2) : 0);
+  const int64_t rows = std::max<int64_t>(a->rows, 1);
+  p.pieces = (rows * a_row + kPieceBytes - 1) / kPieceBytes;
+  p.piece = up((rows + p.pieces - 1) / p.pieces, 256);
+  p.pieces = (rows + p.piece - 1) / p.piece;
+  p.splits = 1;
+  size_t at = 0;
+  auto room = [&](int64_t n) {
+    const size_t here = at;
+    at += static_cast<size_t>(up(n, 256));
+    return here;
+  };
+  p.live = room(4);
+  p.row_of = room(rows * 4);
+  p.place = room(rows * 4);
+  p.counts = room(rows);
+  p.share = room(a->teacher != nullptr ? rows * a->entries * 4 : 0);
+  p.known = room(a->teacher != nullptr ? rows * 4 : 0);
+  p.picked = room(rows * a->entries * 4);
+  p.xp = room(p.planes * rows * p.dpad * 2);
+  p.wp = room(p.pack_w ? p.planes * a->vocab * p.dpad * 2 : 0);
+  p.stats = room(p.piece * p.tiles * 8);
+  p.probs = room(p.grad ? p.piece * p.vpad * (f32 ? 4 : 2) : 0);
+  p.dz = p.grad && f32 ? room(3 * p.piece * p.vpad * 2) : p.probs;
+  p.part = room(a->dx != nullptr ? p.splits * p.piece * p.dpad * 4 : 0);
+  p.dw_sum = room(a->dweight != nullptr && p.pieces > 1 ? a->vocab * p.dpad * 4 : 0);
+  p.bytes = at;
+  return p;
+}
+
+mss_status check_loss_shape(const mss_linear_loss_args* a) {
+  if (a == nullptr || a->struct_size != sizeof(mss_linear_loss_args) || a->reserved0 != 0)
+    return MSS_ERR_BAD_STRUCT;
+  if (bad_dtype(a->io_dtype) || (a->teacher != nullptr && bad_dtype(a->teacher_dtype)))
+    return MSS_ERR_UNSUPPORTED_DTYPE;
+  if (a->rows < 0 || a->rows > (int64_t{1} << 22) || a->dim < 1 || a->dim > kMaxNormDim || a->vocab < 1 ||
+      a->vocab > (int64_t{1} << 22) || a->entries < 1 || a->entries > MSS_MAX_LOSS_ENTRIES ||
+      (a->teacher == nullptr && (a->entries != 1 || a->temperature != 1.0f)) || !std::isfinite(a->logit_scale) ||
+      !std::isfinite(a->temperature) || !(a->temperature > 0.0f))
+    return MSS_ERR_BAD_SHAPE;
+  return MSS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mss_status mss_layer_norm_fwd(const mss_layer_norm_args* a, void* stream) {
+  if (a == nullptr || a->struct_size != sizeof(mss_layer_norm_args) || a->reserved0 != 0 || a->reserved1 != 0)
+    return MSS_ERR_BAD_STRUCT;
+  if (bad_dtype(a->io_dtype) || bad_dtype(a->residual_dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
+  const int64_t R = a->rows, D = a->dim;
+  if (!norm_sizes_ok(R, D) || !(a->eps >= 0.0f)) return MSS_ERR_BAD_SHAPE;
+  if (a->x == nullptr || a->weight == nullptr || a->out == nullptr) return MSS_ERR_NULL_POINTER;
+  const int64_t es = elem(a->io_dtype), rs = elem(a->residual_dtype);
+  const bool in_place = a->residual_out != nullptr && a->residual_out == a->residual;
+  if (a->x_stride < 0 || (a->residual != nullptr && a->residual_stride < 0) ||
+      !out_stride_ok(a->out, R, D, a->out_stride) || !out_stride_ok(a->residual_out, R, D, a->residual_out_stride) ||
+      (R > 1 && in_place && a->residual_out_stride != a->residual_stride))
+    return MSS_ERR_BAD_STRIDE;
+  if (!aligned(a->x, es) || !aligned(a->residual, rs) || !aligned(a->weight, 4) || !aligned(a->bias, 4) ||
+      !aligned(a->out, es) || !aligned(a->mean, 4) || !aligned(a->rstd, 4) || !aligned(a->residual_out, rs))
+    return MSS_ERR_MISALIGNED;
+  const Extent ins[] = {mat(a->x, R, D, a->x_stride, es), vec(a->weight, D, 4), vec(a->bias, D, 4),
+                        in_place ? Extent{} : mat(a->residual, R, D, a->residual_stride, rs)};
+  const Extent outs[] = {mat(a->out, R, D, a->out_stride, es), vec(a->mean, R, 4), vec(a->rstd, R, 4),
+                         mat(a->residual_out, R, D, a->residual_out_stride, rs)};
+  if (!apart(ins, outs)) return MSS_ERR_ALIASING;
+  mss::LayerNormArgs k{};
+  k.rows = R;
+  k.dim = static_cast<int>(D);
+  k.sx = a->x_stride;
+  k.sr = a->residual_stride;
+  k.so = a->out_stride;
+  k.sro = a->residual_out_stride;
+  k.eps = a->eps;
+  k.x = a->x;
+  k.res = a->residual;
+  k.weight = a->weight;
+  k.bias = a->bias;
+  k.out = a->out;
+  k.mean = a->mean;
+  k.rstd = a->rstd;
+  k.res_out = a->residual_out;
+  const hipError_t e = mss::launch_layer_norm(k, a->io_dtype == MSS_BF16, a->residual_dtype == MSS_BF16,
+                                              static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
+}
+
+size_t mss_layer_norm_bwd_workspace_size(const mss_layer_norm_bwd_args* a, mss_status* status) {
+  const mss_status st = check_norm_bwd_shape(a);
+  if (status != nullptr) *status = st;
+  return st == MSS_OK ? norm_bwd_workspace(a) : 0;
+}
+
+mss_status mss_layer_norm_bwd(const mss_layer_norm_bwd_args* a, void* stream) {
+  const mss_status shape = check_norm_bwd_shape(a);
+  if (shape != MSS_OK) return shape;
+  const int64_t R = a->rows, D = a->dim;
+  if (a->dy == nullptr || a->r == nullptr || a->weight == nullptr || a->mean == nullptr || a->rstd == nullptr ||
+      (a->dx == nullptr && a->dresidual == nullptr && a->dweight == nullptr && a->dbias == nullptr))
+    return MSS_ERR_NULL_POINTER;
+  const int64_t es = elem(a->io_dtype), rs = elem(a->r_dtype);
+  if (a->dy_stride < 0 || a->r_stride < 0 || (a->dr != nullptr && a->dr_stride < 0) ||
+      !out_stride_ok(a->dx, R, D, a->dx_stride) || !out_stride_ok(a->dresidual, R, D, a->dresidual_stride))
+    return MSS_ERR_BAD_STRIDE;
+  if (!aligned(a->dy, es) || !aligned(a->r, rs) || !aligned(a->dr, rs) || !aligned(a->weight, 4) ||
+      !aligned(a->mean, 4) || !aligned(a->rstd, 4) || !aligned(a->dx, es) || !aligned(a->dresidual, rs) ||
+      !aligned(a->dweight, 4) || !aligned(a->dbias, 4) || !aligned(a->workspace, 256))
+    return MSS_ERR_MISALIGNED;
+  const size_t need = norm_bwd_workspace(a);
+  if (need > 0 && (a->workspace == nullptr || a->workspace_bytes < need)) return MSS_ERR_WORKSPACE_TOO_SMALL;
+  const Extent ins[] = {mat(a->dy, R, D, a->dy_stride, es), mat(a->r, R, D, a->r_stride, rs),
+                        mat(a->dr, R, D, a->dr_stride, rs), vec(a->weight, D, 4), vec(a->mean, R, 4),
+                        vec(a->rstd, R, 4)};
+  const Extent outs[] = {mat(a->dx, R, D, a->dx_stride, es), mat(a->dresidual, R, D, a->dresidual_stride, rs),
+                         vec(a->dweight, D, 4), vec(a->dbias, D, 4),
+                         need > 0 ? vec(a->workspace, static_cast<int64_t>(need), 1) : Extent{}};
+  if (!apart(ins, outs)) return MSS_ERR_ALIASING;
+  mss::LayerNormBwdArgs k{};
+  k.rows = R;
+  k.dim = static_cast<int>(D);
+  k.parts = mss::layer_norm_bwd_parts(R, D);
+  k.sdy = a->dy_stride;
+  k.sr = a->r_stride;
+  k.sdr = a->dr_stride;
+  k.sdx = a->dx_stride;
+  k.sdres = a->dresidual_stride;
+  k.dy = a->dy;
+  k.r = a->r;
+  k.dr = a->dr;
+  k.weight = a->weight;
+  k.mean = a->mean;
+  k.rstd = a->rstd;
+  k.dx = a->dx;
+  k.dres = a->dresidual;
+  k.dweight = a->dweight;
+  k.dbias = a->dbias;
+  k.sums = static_cast<float*>(a->workspace);
+  const hipError_t e = mss::launch_layer_norm_bwd(k, a->io_dtype == MSS_BF16, a->r_dtype == MSS_BF16,
+                                                  static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
+}
+
+size_t mss_linear_loss_workspace_size(const mss_linear_loss_args* a, mss_status* status) {
+  const mss_status st = check_loss_shape(a);
+  if (status != nullptr) *status = st;
+  return st == MSS_OK ? loss_plan(a).bytes : 0;
+}
+
+mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
+  const mss_status shape = check_loss_shape(a);
+  if (shape != MSS_OK) return shape;
+  const LossPlan p = loss_plan(a);
+  const int64_t R = a->rows, D = a->dim, V = a->vocab, K = a->entries;
+  const int64_t es = elem(a->io_dtype), ts = elem(a->teacher_dtype);
+  if (a->weight == nullptr ||
+      (R > 0 && (a->x == nullptr || a->ids == nullptr || a->loss == nullptr || a->lse == nullptr)))
+    return MSS_ERR_NULL_POINTER;
+  if (a->x_stride < 0 || a->weight_stride < 0 || !mss::strides_nonneg(a->ids_stride, 2) ||
+      (a->teacher != nullptr && !mss::strides_nonneg(a->teacher_stride, 2)) ||
+      !out_stride_ok(a->dx, R, D, a->dx_stride) || !out_stride_ok(a->dweight, V, D, a->dweight_stride))
+    return MSS_ERR_BAD_STRIDE;
+  if (!aligned(a->x, es) || !aligned(a->weight, es) || !aligned(a->ids, 8) || !aligned(a->teacher, ts) ||
+      !aligned(a->row_weight, 4) || !aligned(a->loss, 4) || !aligned(a->lse, 4) || !aligned(a->total, 4) ||
+      !aligned(a->dx, es) ||
+      !aligned(a->dweight, es) || !aligned(a->workspace, 256))
+    return MSS_ERR_MISALIGNED;
+  if (a->workspace == nullptr || a->workspace_bytes < p.bytes) return MSS_ERR_WORKSPACE_TOO_SMALL;
+  const Extent none{};
+  const int64_t ks[2] = {R, K};
+  const Extent ins[] = {R > 0 ? mat(a->x, R, D, a->x_stride, es) : none, mat(a->weight, V, D, a->weight_stride, es),
+                        R > 0 ? extent_of(a->ids, ks, a->ids_stride, 2, 8) : none,
+                        R > 0 ? extent_of(a->teacher, ks, a->teacher_stride, 2, ts) : none,
+                        R > 0 ? vec(a->row_weight, R, 4) : none};
+  const Extent outs[] = {R > 0 ? vec(a->loss, R, 4) : none, R > 0 ? vec(a->lse, R, 4) : none, vec(a->total, 1, 4),
+                         R > 0 ? mat(a->dx, R, D, a->dx_stride, es) : none,
+                         mat(a->dweight, V, D, a->dweight_stride, es),
+                         vec(a->workspace, static_cast<int64_t>(p.bytes), 1)};
+  if (!apart(ins, outs)) return MSS_ERR_ALIASING;
+
+  char* ws = static_cast<char*>(a->workspace);
+  mss::LossArgs k{};
+  k.rows = static_cast<int>(R);
+  k.dim = static_cast<int>(D);
+  k.vocab = static_cast<int>(V);
+  k.entries = static_cast<int>(K);
+  k.sx = a->x_stride;
+  k.sw = a->weight_stride;
+  for (int i = 0; i < 2; ++i) {
+    k.sids[i] = a->ids_stride[i];
+    k.steach[i] = a->teacher_stride[i];
+  }
+  k.sdx = a->dx_stride;
+  k.sdw = a->dweight_stride;
+  k.x = a->x;
+  k.weight = a->weight;
+  k.ids = a->ids;
+  k.teacher = a->teacher;
+  k.teacher_bf16 = a->teacher_dtype == MSS_BF16;
+  k.row_weight = a->row_weight;
+  k.inv_tau = 1.0f / a->temperature;
+  k.scale2 = static_cast<float>(static_cast<double>(a->logit_scale) / a->temperature * 1.4426950408889634);
+  k.back = a->logit_scale * a->temperature;
+  k.tau2 = a->temperature * a->temperature;
+  k.loss = a->loss;
+  k.lse = a->lse;
+  k.total = a->total;
+  k.dx = R > 0 ? a->dx : nullptr;
+  k.dweight = a->dweight;
+  k.live = reinterpret_cast<int*>(ws + p.live);
+  k.row_of = reinterpret_cast<int*>(ws + p.row_of);
+  k.place = reinterpret_cast<int*>(ws + p.place);
+  k.counts = reinterpret_cast<uint8_t*>(ws + p.counts);
+  k.share = reinterpret_cast<float*>(ws + p.share);
+  k.known = reinterpret_cast<float*>(ws + p.known);
+  k.picked = reinterpret_cast<float*>(ws + p.picked);
+  k.planes = static_cast<int>(p.planes);
+  k.dpad = p.dpad;
+  k.xp = reinterpret_cast<uint16_t*>(ws + p.xp);
+  k.pack_w = p.pack_w;
+  k.wp = p.pack_w ? reinterpret_cast<uint16_t*>(ws + p.wp) : const_cast<uint16_t*>(static_cast<const uint16_t*>(a->weight));
+  k.wp_stride = p.pack_w ? p.dpad : a->weight_stride;
+  k.wp_plane = V * p.dpad;
+  k.piece = static_cast<int>(p.piece);
+  k.pieces = static_cast<int>(p.pieces);
+  k.tiles = static_cast<int>(p.tiles);
+  k.vpad = p.vpad;
+  k.stats = reinterpret_cast<float2*>(ws + p.stats);
+  k.probs = ws + p.probs;
+  k.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
+  k.part = reinterpret_cast<float*>(ws + p.part);
+  k.splits = static_cast<int>(p.splits);
+  k.dw_sum = reinterpret_cast<float*>(ws + p.dw_sum);
+  const hipError_t e = mss::launch_loss(k, a->io_dtype == MSS_BF16, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
+}
+
+mss_status mss_scale(const void* in, const float* factor, void* out, int64_t n, int32_t dtype, void* stream) {
+  if (bad_dtype(dtype)) return MSS_ERR_UNSUPPORTED_DTYPE;
+  if (n < 0 || n > (int64_t{1} << 46)) return MSS_ERR_BAD_SHAPE;
+  if (factor == nullptr || (n > 0 && (in == nullptr || out == nullptr))) return MSS_ERR_NULL_POINTER;
+  const int64_t es = elem(dtype);
+  if (!aligned(in, es) || !aligned(out, es) || !aligned(factor, 4)) return MSS_ERR_MISALIGNED;
+  if (n == 0) return MSS_OK;
+  const Extent ins[] = {vec(in, n, es), vec(factor, 1, 4)}, outs[] = {vec(out, n, es)};
+  if (!apart(ins, outs)) return MSS_ERR_ALIASING;
+  const hipError_t e = mss::launch_scale(in, factor, out, n, dtype == MSS_BF16, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
+}
+
+}  // extern "C"

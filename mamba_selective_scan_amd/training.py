@@ -1,0 +1,319 @@
+"""The operations around the scans of a training step: layer norm, and the losses
+over a vocabulary, with their gradients.
+
+    y, mean, rstd, r = layer_norm_fwd(x, weight, bias, residual=residual)
+    g = layer_norm_bwd(dy, r, weight, mean, rstd, dr=dr)     # x, residual, weight, bias
+    y, r = layer_norm(x, weight, bias, residual)             # autograd: fwd + bwd
+
+    loss, lse = linear_cross_entropy_fwd(x, weight, targets)
+    loss, lse, dx, dweight = linear_cross_entropy_grad(x, weight, targets)
+    mean_loss = linear_cross_entropy(x, weight, targets)     # autograd
+
+    loss, lse = linear_distillation_fwd(x, weight, ids, teacher, temperature=2.0)
+    loss, lse, dx, dweight = linear_distillation_grad(x, weight, ids, teacher, temperature=2.0)
+    mean_loss = linear_distillation(x, weight, ids, teacher, temperature=2.0)   # autograd
+
+The losses take hidden states x [T, D] and the vocabulary's matrix weight [V, D]
+(both float32 or both bfloat16, unit stride in D) and never hold the logits of
+all rows.  A target or id outside [0, V) does not count (-100 and -1 are such);
+a row without one that does has loss 0 and gradient 0 and adds nothing to
+dweight, whatever it holds.  Nothing here synchronises.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from .heads import (_Tensor, _current_device, _current_stream, _give_workspace, _gpu, _io, _launch, _like, _out,
+                    _rows, _vector)
+
+_norm_args = _lib.packer(_lib.LayerNormArgs)
+_norm_bwd_args = _lib.packer(_lib.LayerNormBwdArgs)
+_loss_args = _lib.packer(_lib.LinearLossArgs)
+
+
+def _matrix(t, name, device=None):
+    """A matrix with unit stride in its columns: its address and row stride."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got shape {tuple(t.shape)}")
+    return _rows(t, name, t.shape, t.dtype, t.device if device is None else device)
+
+
+def _vec_out(n, device):
+    return torch.empty_strided((n,), (1,), dtype=torch.float32, device=device)
+
+
+def layer_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, out=None, residual_out=None):
+    """Layer norm over the columns of x [R, D] (float32 or bfloat16, unit stride
+    in D), after adding ``residual`` [R, D] (its own dtype), ordered on torch's
+    current stream: r = x + residual, y = (r - mean) * rstd * weight + bias, with
+    weight and bias [D] fp32.
+
+    Returns (y, mean, rstd): y in x's dtype, mean and rstd [R] fp32 for the
+    backward.  With a residual, r in the residual's dtype is returned last;
+    ``residual_out`` may be ``residual`` itself, which is then updated in place.
+    """
+    dev = _gpu(x, "x")
+    x_rows = _matrix(x, "x")
+    shape = x.shape
+    rows, dim = shape
+    out = _out(out, x, x.dtype, dev)
+    mean, rstd = _vec_out(rows, dev), _vec_out(rows, dev)
+    left, res, res_type = (out, mean, rstd), (0, 0, 0, 0), _io(x)
+    if residual is not None:
+        if not isinstance(residual, _Tensor):
+            raise TypeError("residual must be a torch.Tensor")
+        res_type = _io(residual)
+        res = _rows(residual, "residual", shape, residual.dtype, dev)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+        res += _rows(residual_out, "residual_out", shape, residual.dtype, dev)
+        left += (residual_out,)
+    elif residual_out is not None:
+        raise ValueError("residual_out is given without residual")
+    a = _norm_args(_io(x), res_type, 0, rows, dim, *x_rows, *res[:2],
+                   _vector(weight, "weight", dim, torch.float32, dev),
+                   _vector(bias, "bias", dim, torch.float32, dev),
+                   *_rows(out, "out", shape, x.dtype, dev), mean.data_ptr(), rstd.data_ptr(), *res[2:], eps, 0)
+    if rows:
+        _launch(_lib.lib().mss_layer_norm_fwd, a, dev)
+    return left
+
+
+def layer_norm_bwd(dy, r, weight, mean, rstd, *, dr=None, bias=True, params=True, workspace=None):
+    """Layer norm's backward, ordered on torch's current stream: the gradients of
+    sum(dy * y), and of sum(dr * r) where ``dr`` is given.
+
+    dy [R, D] in y's dtype; r [R, D] what was normed (x, or the sum that
+    layer_norm_fwd returned) and dr [R, D] in its dtype; mean, rstd [R] as the
+    forward left them.  Returns a dict: "x" in dy's dtype; "residual", the same
+    gradient in r's dtype (the same tensor where the dtypes are equal), if r's
+    dtype differs or dr is given; "weight" and, unless ``bias`` is false, "bias"
+    [D] fp32 (neither if ``params`` is false).
+    """
+    dev = _gpu(dy, "dy")
+    dy_rows = _matrix(dy, "dy")
+    shape = dy.shape
+    rows, dim = shape
+    if not isinstance(r, _Tensor):
+        raise TypeError("r must be a torch.Tensor")
+    r_type = _io(r)
+    both = r.dtype is not dy.dtype
+    g = {"x": torch.empty_like(dy, memory_format=torch.contiguous_format)}
+    dres = 0
+    if both:
+        g["residual"] = torch.empty_like(r, memory_format=torch.contiguous_format)
+        dres = g["residual"].data_ptr()
+    elif dr is not None:
+        g["residual"] = g["x"]
+    dw = db = 0
+    if params:
+        make = torch.zeros if rows == 0 else torch.empty
+        g["weight"] = make(dim, dtype=torch.float32, device=dev)
+        dw = g["weight"].data_ptr()
+        if bias:
+            g["bias"] = make(dim, dtype=torch.float32, device=dev)
+            db = g["bias"].data_ptr()
+    a = _norm_bwd_args(_io(dy), r_type, 0, rows, dim, *dy_rows, *_rows(r, "r", shape, r.dtype, dev),
+                       *((0, 0) if dr is None else _rows(dr, "dr", shape, r.dtype, dev)),
+                       *(_vector(_needed(t, n), n, k, torch.float32, dev)
+                         for t, n, k in ((weight, "weight", dim), (mean, "mean", rows), (rstd, "rstd", rows))),
+                       g["x"].data_ptr(), dim, dres, dim, dw, db, 0, 0)
+    if rows:
+        lib = _lib.lib()
+        _give_workspace(a, lib.mss_layer_norm_bwd_workspace_size(ctypes.byref(a), None), workspace, dev)
+        _launch(lib.mss_layer_norm_bwd, a, dev)
+    return g
+
+
+def _needed(t, name):
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        wide, rest = x.shape, None
+        x = x.reshape(-1, wide[-1])
+        if residual is not None:
+            residual = residual.reshape(x.shape)
+        y, mean, rstd, *rest = layer_norm_fwd(x, weight, bias, residual=residual, eps=eps)
+        r = rest[0] if rest else x
+        ctx.save_for_backward(r, weight, mean, rstd)
+        ctx.bias, ctx.wide, ctx.pair = bias is not None, wide, bool(rest)
+        return (y.view(wide), r.view(wide)) if rest else y.view(wide)
+
+    @staticmethod
+    def backward(ctx, dy, dr=None):
+        r, weight, mean, rstd = ctx.saved_tensors
+        flat = [None if t is None else t.reshape(-1, ctx.wide[-1]) for t in (dy, dr)]
+        flat = [t if t is None or t.shape[1] == 1 or t.stride(1) == 1 else t.contiguous() for t in flat]
+        want = ctx.needs_input_grad
+        g = layer_norm_bwd(flat[0], r, weight, mean, rstd, dr=flat[1], bias=ctx.bias and want[2],
+                           params=want[1] or (ctx.bias and want[2]))
+        dx = g["x"].view(ctx.wide)
+        dres = (g["residual"] if "residual" in g else g["x"]).view(ctx.wide) if ctx.pair and want[3] else None
+        return (dx if want[0] else None, g.get("weight") if want[1] else None,
+                g.get("bias") if want[2] else None, dres, None)
+
+
+def layer_norm(x, weight, bias=None, residual=None, eps=1e-5):
+    """Layer norm with autograd over the last dimension of x [..., D]: y, or
+    (y, x + residual) with a ``residual`` of x's shape (see layer_norm_fwd)."""
+    _gpu(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least 1 dimension")
+    if residual is not None and (not isinstance(residual, _Tensor) or residual.shape != x.shape):
+        raise ValueError(f"residual must have shape {tuple(x.shape)}")
+    return _LayerNorm.apply(x, weight, bias, residual, eps)
+
+
+def _loss(x, weight, ids, teacher, row_weight, scale, tau, grads, out, workspace, total=None):
+    """(loss, lse, dx, dweight) of mss_linear_loss; dx and dweight None unless
+    wanted (``grads``: which).  ``total`` (one float) receives sum(c * loss)."""
+    dev = _gpu(x, "x")
+    x_rows = _matrix(x, "x")
+    rows, dim = x.shape
+    w_rows = _matrix(weight, "weight", dev)
+    vocab = weight.shape[0]
+    _like(weight, "weight", (vocab, dim), x.dtype, dev)
+    if not isinstance(ids, _Tensor):
+        raise TypeError("targets and ids must be torch.Tensors")
+    entries = 1
+    if teacher is None:
+        id_strides = (*_like(ids, "targets", (rows,), torch.int64, dev).stride(), 0)
+        teach = (0, 0, 0, _lib.MSS_F32)
+    else:
+        if ids.dim() != 2:
+            raise ValueError(f"ids must have shape [{rows}, entries], got {tuple(ids.shape)}")
+        entries = ids.shape[1]
+        id_strides = _like(ids, "ids", (rows, entries), torch.int64, dev).stride()
+        if not isinstance(teacher, _Tensor):
+            raise TypeError("teacher must be a torch.Tensor")
+        teach_type = _io(teacher)
+        _like(teacher, "teacher", (rows, entries), teacher.dtype, dev)
+        teach = (teacher.data_ptr(), *teacher.stride(), teach_type)
+        if rows == 0:  # (no addresses: neither loss has anything to compute but dweight = 0)
+            entries, tau = 1, 1.0
+    loss, lse = _vec_out(rows, dev), _vec_out(rows, dev)
+    made, addresses = [], []
+    for like, name, want, given in zip((x, weight), ("dx", "dweight"), grads, out):
+        if not want:
+            if given is not None:
+                raise ValueError(f"{name} is given but not computed")
+            made.append(None)
+            addresses += (0, 0)
+            continue
+        made.append(torch.empty_like(like, memory_format=torch.contiguous_format) if given is None else given)
+        addresses += _rows(made[-1], name, like.shape, like.dtype, dev)
+    a = _loss_args(_io(x), rows, dim, vocab, entries, *x_rows, *w_rows, ids.data_ptr(), *id_strides,
+                   *teach, scale, tau, 0, _vector(row_weight, "row_weight", rows, torch.float32, dev),
+                   loss.data_ptr(), lse.data_ptr(), 0 if total is None else total.data_ptr(), *addresses, 0, 0)
+    lib = _lib.lib()
+    _give_workspace(a, lib.mss_linear_loss_workspace_size(ctypes.byref(a), None), workspace, dev)
+    _launch(lib.mss_linear_loss, a, dev)
+    return (loss, lse, *made)
+
+
+def linear_cross_entropy_fwd(x, weight, targets, *, logit_scale=1.0, workspace=None):
+    """Softmax cross entropy of hidden states x [T, D] over a vocabulary weight
+    [V, D], ordered on torch's current stream: z = logit_scale * x @ weight.T,
+    lse = logsumexp(z), loss = lse - z[targets], with targets [T] int64.
+
+    Returns (loss, lse), both [T] fp32.
+    """
+    return _loss(x, weight, targets, None, None, logit_scale, 1.0, (False, False), (None, None), workspace)[:2]
+
+
+def linear_cross_entropy_grad(x, weight, targets, row_weight=None, *, logit_scale=1.0, dx=None, dweight=None,
+                              workspace=None):
+    """linear_cross_entropy_fwd, and the gradients of sum(c * loss) with c =
+    ``row_weight`` [T] fp32, or 1 / (rows that count): the mean over those.
+
+    Returns (loss, lse, dx, dweight), dx in x's and dweight in weight's shape and
+    dtype (``dx`` and ``dweight`` may be supplied).
+    """
+    return _loss(x, weight, targets, None, row_weight, logit_scale, 1.0, (True, True), (dx, dweight), workspace)
+
+
+def linear_distillation_fwd(x, weight, ids, teacher, *, temperature=1.0, logit_scale=1.0, workspace=None):
+    """Distillation of hidden states x [T, D] over a vocabulary weight [V, D] from
+    a teacher's top logits, ordered on torch's current stream: ids [T, K] int64
+    and teacher [T, K] (float32 or bfloat16); t = softmax(teacher / temperature)
+    over a row's entries that count, z = logit_scale * x @ weight.T / temperature,
+    lse = logsumexp(z), loss = temperature^2 * sum(t * (log t - z[ids] + lse)).
+
+    Returns (loss, lse), both [T] fp32.
+    """
+    return _loss(x, weight, ids, _needed(teacher, "teacher"), None, logit_scale, temperature, (False, False),
+                 (None, None), workspace)[:2]
+
+
+def linear_distillation_grad(x, weight, ids, teacher, row_weight=None, *, temperature=1.0, logit_scale=1.0,
+                             dx=None, dweight=None, workspace=None):
+    """linear_distillation_fwd, and the gradients of sum(c * loss) with c =
+    ``row_weight`` [T] fp32, or 1 / (rows that count): the mean over those.
+
+    Returns (loss, lse, dx, dweight) as linear_cross_entropy_grad does.
+    """
+    return _loss(x, weight, ids, _needed(teacher, "teacher"), row_weight, logit_scale, temperature, (True, True),
+                 (dx, dweight), workspace)
+
+
+def _scaled(t, factor):
+    """A contiguous tensor times a factor on the device."""
+    out = torch.empty_like(t)
+    dev = t.device
+    with torch.cuda.device(dev):
+        _lib.check(_lib.lib().mss_scale(t.data_ptr(), factor.data_ptr(), out.data_ptr(), t.numel(), _io(t),
+                                        _current_stream(dev.index)))
+    return out
+
+
+class _LinearLoss(torch.autograd.Function):
+    # The gradients come with the loss: computing them later would form the
+    # logits again, a third more work.
+    @staticmethod
+    def forward(ctx, x, weight, ids, teacher, row_weight, scale, tau):
+        wide = x.shape
+        flat = x.reshape(-1, wide[-1])
+        ids = ids.reshape(-1) if teacher is None else ids.reshape(flat.shape[0], -1)
+        if teacher is not None:
+            teacher = teacher.reshape(ids.shape)
+        if row_weight is not None:
+            row_weight = row_weight.reshape(-1)
+        want = ctx.needs_input_grad[:2]
+        total = torch.empty((), dtype=torch.float32, device=x.device)
+        _, _, dx, dw = _loss(flat, weight, ids, teacher, row_weight, scale, tau, want, (None, None), None, total)
+        ctx.save_for_backward(None if dx is None else dx.view(wide), dw)
+        return total
+
+    @staticmethod
+    def backward(ctx, g):
+        g = g.float().contiguous()
+        return (*(None if t is None else _scaled(t, g) for t in ctx.saved_tensors), None, None, None, None, None)
+
+
+def linear_cross_entropy(x, weight, targets, row_weight=None, *, logit_scale=1.0):
+    """Cross entropy with autograd: sum(row_weight * loss) over the rows, or the
+    mean loss of the rows that count, as a scalar; x [..., D], targets and
+    row_weight [...] (see linear_cross_entropy_grad; targets and row_weight have
+    no gradient)."""
+    _gpu(x, "x")
+    return _LinearLoss.apply(x, weight, targets, None, row_weight, logit_scale, 1.0)
+
+
+def linear_distillation(x, weight, ids, teacher, row_weight=None, *, temperature=1.0, logit_scale=1.0):
+    """Distillation with autograd: sum(row_weight * loss) over the rows, or the
+    mean loss of the rows that count, as a scalar; x [..., D], ids and teacher
+    [..., K], row_weight [...] (see linear_distillation_grad; only x and weight
+    have gradients)."""
+    _gpu(x, "x")
+    return _LinearLoss.apply(x, weight, ids, _needed(teacher, "teacher"), row_weight, logit_scale, temperature)
