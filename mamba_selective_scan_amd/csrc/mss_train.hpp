@@ -48,8 +48,6 @@ hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, bool io_bf16, bool r
 
 // ---------------------------------------------------------------- losses
 
-constexpr int kLossVocabTile = 64;  // vocabulary entries that share a maximum
-
 struct LossArgs {
   int rows, dim, vocab, entries;
   int64_t sx, sw, sids[2], steach[2], sdx, sdw;
@@ -60,7 +58,7 @@ struct LossArgs {
   bool teacher_bf16;
   const float* row_weight;
   float inv_tau;   // 1 / temperature
-  float scale2;    // logit_scale / temperature * log2 e: x.w to logits in powers of two
+  float scale;     // logit_scale / temperature: x.w to logits
   float back;      // logit_scale * temperature: dz's factor before c
   float tau2;      // temperature^2
   float* loss;
@@ -75,26 +73,34 @@ struct LossArgs {
   uint8_t* counts; // [rows] whether it counts
   float* share;    // [rows][entries] t_k by row (teacher only)
   float* known;    // [rows] sum_k t_k log t_k (teacher only)
-  float* picked;   // [rows][entries] z_{id_k} log2 e of the i-th row that counts
+  int* near;       // [rows][entries] ids of the i-th row that counts, -1 for those that do not
+  uint32_t* where; // [rows][where_words] the tiles that hold one of them, a bit each
+  int where_words;
+  float* picked;   // [rows][entries] their logits
   // rows and weights as bf16 operands: one plane, or three whose sum is the fp32 value
   uint16_t* xp;    // [planes][rows][dpad]
   uint16_t* wp;    // [planes][vocab][dpad], or the weight itself
   int planes;
   int64_t dpad, wp_stride, wp_plane;
+  int wcols;       // columns of wp's rows that may be read, a multiple of 8
   bool pack_w;
+  bool small;      // small tiles of the products
   // of a piece of rows
   int piece;       // rows of a piece
   int pieces;
-  int tiles;       // vocabulary tiles
+  int tiles;       // vocabulary tiles, whose entries share a maximum
   int64_t vpad;
-  float2* stats;   // [piece][tiles] exponent R and sum of 2^(z2 - R)
-  void* probs;     // [piece][vpad] codes of z2 (bf16), or z2 (fp32)
+  float2* stats;   // [piece][tiles] an integer R and the sum of e^(z - R)
+  void* probs;     // [piece][vpad] codes of the logits (bf16), or the logits (fp32)
   uint16_t* dz;    // [planes][piece][vpad] (bf16: probs itself)
+  int2* fix;       // [piece][fixes] (bf16) id and what its dz lost by its rounding, as float bits; or id -1
+  int fixes;
   float* part;     // [splits][piece][dpad]
-  int splits;
+  int splits;      // at most
   float* dw_sum;   // [vocab][dpad] (more than one piece)
 };
 
+int loss_vocab_tile(bool small);
 hipError_t launch_loss(const LossArgs& a, bool io_bf16, hipStream_t stream);
 hipError_t launch_scale(const void* in, const float* factor, void* out, int64_t n, bool bf16,
                         hipStream_t stream);

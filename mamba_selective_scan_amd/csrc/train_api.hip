@@ -70,9 +70,10 @@ size_t norm_bwd_workspace(const mss_layer_norm_bwd_args* a) {
 constexpr int64_t kPieceBytes = int64_t{1} << 30;
 
 struct LossPlan {
-  bool grad, pack_w;
-  int64_t planes, dpad, vpad, tiles, piece, pieces, splits;
-  size_t live, row_of, place, counts, share, known, picked, xp, wp, stats, probs, dz, part, dw_sum, bytes;
+  bool grad, pack_w, small;
+  int64_t planes, dpad, vpad, tiles, words, piece, pieces, splits, fixes;
+  size_t live, row_of, place, counts, share, known, near, where, picked, xp, wp, stats, probs, dz, fix, part, dw_sum,
+      bytes;
 };
 
 LossPlan loss_plan(const mss_linear_loss_args* a) {
@@ -82,15 +83,23 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.planes = f32 ? 3 : 1;
   p.dpad = up(a->dim, 64);
   p.vpad = up(a->vocab, 256);
-  p.tiles = (a->vocab + mss::kLossVocabTile - 1) / mss::kLossVocabTile;
-  // bf16 weights are read where they are if their rows are whole 16-byte vectors
-  p.pack_w = f32 || a->dim % 8 != 0 || !aligned(a->weight, 16) || (a->vocab > 1 && a->weight_stride % 8 != 0);
+  p.small = a->rows <= 128;
+  p.tiles = (a->vocab + mss::loss_vocab_tile(p.small) - 1) / mss::loss_vocab_tile(p.small);
+  p.words = (p.tiles + 31) / 32;
+  // bf16 weights are read where they are if their rows are whole 16-byte vectors,
+  // one behind another, and 256 of them within 32-bit offsets
+  p.pack_w = f32 || a->dim % 8 != 0 || !aligned(a->weight, 16) ||
+             (a->vocab > 1 && (a->weight_stride % 8 != 0 || a->weight_stride < a->dim ||
+                               a->weight_stride > (int64_t{1} << 21)));
   const int64_t a_row = p.tiles * 8 + (p.grad ? p.vpad * (f32 ? 10 : 2) : 0);
   const int64_t rows = std::max<int64_t>(a->rows, 1);
   p.pieces = (rows * a_row + kPieceBytes - 1) / kPieceBytes;
   p.piece = up((rows + p.pieces - 1) / p.pieces, 256);
   p.pieces = (rows + p.piece - 1) / p.piece;
-  p.splits = 1;
+  // parts of the dx product, within 512 MiB of them
+  p.splits = std::clamp<int64_t>((int64_t{1} << 29) / (p.piece * p.dpad * 4), 1, 64);
+  // workgroups of a row's softmax: as many as give 512, each with 2048 columns or more
+  p.fixes = std::clamp<int64_t>(std::min((rows + 511) / rows, p.vpad / 2048), 1, 64);
   size_t at = 0;
   auto room = [&](int64_t n) {
     const size_t here = at;
@@ -103,12 +112,15 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.counts = room(rows);
   p.share = room(a->teacher != nullptr ? rows * a->entries * 4 : 0);
   p.known = room(a->teacher != nullptr ? rows * 4 : 0);
+  p.near = room(rows * a->entries * 4);
+  p.where = room(rows * p.words * 4);
   p.picked = room(rows * a->entries * 4);
   p.xp = room(p.planes * rows * p.dpad * 2);
   p.wp = room(p.pack_w ? p.planes * a->vocab * p.dpad * 2 : 0);
   p.stats = room(p.piece * p.tiles * 8);
   p.probs = room(p.grad ? p.piece * p.vpad * (f32 ? 4 : 2) : 0);
   p.dz = p.grad && f32 ? room(3 * p.piece * p.vpad * 2) : p.probs;
+  p.fix = room(p.grad && !f32 ? p.piece * p.fixes * 8 : 0);
   p.part = room(a->dx != nullptr ? p.splits * p.piece * p.dpad * 4 : 0);
   p.dw_sum = room(a->dweight != nullptr && p.pieces > 1 ? a->vocab * p.dpad * 4 : 0);
   p.bytes = at;
@@ -287,7 +299,7 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.teacher_bf16 = a->teacher_dtype == MSS_BF16;
   k.row_weight = a->row_weight;
   k.inv_tau = 1.0f / a->temperature;
-  k.scale2 = static_cast<float>(static_cast<double>(a->logit_scale) / a->temperature * 1.4426950408889634);
+  k.scale = a->logit_scale / a->temperature;
   k.back = a->logit_scale * a->temperature;
   k.tau2 = a->temperature * a->temperature;
   k.loss = a->loss;
@@ -301,14 +313,19 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.counts = reinterpret_cast<uint8_t*>(ws + p.counts);
   k.share = reinterpret_cast<float*>(ws + p.share);
   k.known = reinterpret_cast<float*>(ws + p.known);
+  k.near = reinterpret_cast<int*>(ws + p.near);
+  k.where = reinterpret_cast<uint32_t*>(ws + p.where);
+  k.where_words = static_cast<int>(p.words);
   k.picked = reinterpret_cast<float*>(ws + p.picked);
   k.planes = static_cast<int>(p.planes);
   k.dpad = p.dpad;
   k.xp = reinterpret_cast<uint16_t*>(ws + p.xp);
   k.pack_w = p.pack_w;
   k.wp = p.pack_w ? reinterpret_cast<uint16_t*>(ws + p.wp) : const_cast<uint16_t*>(static_cast<const uint16_t*>(a->weight));
-  k.wp_stride = p.pack_w ? p.dpad : a->weight_stride;
+  k.wp_stride = p.pack_w ? p.dpad : std::max(a->weight_stride, D);
   k.wp_plane = V * p.dpad;
+  k.wcols = static_cast<int>(p.pack_w ? p.dpad : D);
+  k.small = p.small;
   k.piece = static_cast<int>(p.piece);
   k.pieces = static_cast<int>(p.pieces);
   k.tiles = static_cast<int>(p.tiles);
@@ -316,6 +333,8 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.stats = reinterpret_cast<float2*>(ws + p.stats);
   k.probs = ws + p.probs;
   k.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
+  k.fix = reinterpret_cast<int2*>(ws + p.fix);
+  k.fixes = static_cast<int>(p.fixes);
   k.part = reinterpret_cast<float*>(ws + p.part);
   k.splits = static_cast<int>(p.splits);
   k.dw_sum = reinterpret_cast<float*>(ws + p.dw_sum);

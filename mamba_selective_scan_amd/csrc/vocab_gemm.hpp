@@ -7,6 +7,34 @@
 
 namespace mss {
 
+// bf16 losses keep a logit as its distance below its tile's ceiling in 16 bits:
+// steps of 2^-10, so that a probability is off by at most 2^-11, an eighth of
+// what its rounding to bf16 takes; one 64 below (1e-28 of its tile's largest) is 0.
+constexpr float kCodeSteps = 1024.0f;
+
+// How many parts of the vocabulary the dx product is cut into, for `tiles` tiles
+// of its rows and columns: as many as fill the card (256 workgroups of large
+// tiles at a time, 768 of small ones) best, a part costing some steps besides its
+// own.  Host and device agree on it.
+__host__ __device__ inline int dx_splits(const LossArgs& a, int tiles) {
+  const float slots = a.small ? 768.0f : 256.0f, steps = static_cast<float>((a.vocab + 63) / 64);
+  int best = 1;
+  float least = 3e38f;
+  for (int s = 1; s <= a.splits; s += s < 8 ? 1 : s / 4) {
+    const float t = ceilf(static_cast<float>(tiles) * s / slots) * (steps / s + 6.0f) + 1.0f * s;
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// Tiles of the dx product for this many rows.
+__host__ __device__ inline int dx_tiles(const LossArgs& a, int rows) {
+  return a.small ? (rows + 63) / 64 * ((a.dim + 127) / 128) : (rows + 255) / 256 * ((a.dim + 255) / 256);
+}
+
 // logits of the piece's rows: stats, and with `keep` the codes or logits
 hipError_t launch_logits(const LossArgs& a, int first, bool io_bf16, bool keep, hipStream_t stream);
 // part = dz weight, by splits of the vocabulary

@@ -4,7 +4,7 @@
 //
 // Rows that count are packed one behind another (x, and everything that is
 // computed of it), so that ignored rows cost no products, and whatever they hold
-// reaches nothing.  Logits are kept in powers of two, z2 = z log2 e.
+// reaches nothing.
 #include "mss.h"
 #include "mss_train.hpp"
 #include "vocab_gemm.hpp"
@@ -118,27 +118,30 @@ __device__ inline void to_planes(float v, uint16_t* p, int64_t plane, int planes
   }
 }
 
-// One workgroup a row that counts: its x as an operand, and its entries' logits.
+constexpr int kMaxWords = (1 << 22) / 64 / 32;  // of the largest vocabulary's tiles
+
+// One workgroup a row that counts: its x as an operand, its ids, and the tiles of
+// the vocabulary that hold one.
 template <typename IO>
-__global__ __launch_bounds__(256) void pack_kernel(LossArgs a) {
+__global__ __launch_bounds__(256) void pack_kernel(LossArgs a, int tile_shift) {
   const int j = blockIdx.x;
   if (j >= *a.live) return;
   const int row = a.row_of[j];
   const IO* x = static_cast<const IO*>(a.x) + row * a.sx;
   uint16_t* xp = a.xp + j * a.dpad;
   const int64_t plane = static_cast<int64_t>(a.rows) * a.dpad;
+  __shared__ uint32_t where[kMaxWords];
+  for (int i = threadIdx.x; i < a.where_words; i += 256) where[i] = 0;
   for (int c = threadIdx.x; c < a.dpad; c += 256)
     to_planes<IO>(c < a.dim ? io_traits<IO>::load(x + c) : 0.0f, xp + c, plane, a.planes);
-  for (int k = threadIdx.x >> 6; k < a.entries; k += 4) {
+  __syncthreads();
+  for (int k = threadIdx.x; k < a.entries; k += 256) {
     const int id = id_at(a, row, k);
-    if (id < 0) continue;
-    const IO* w = static_cast<const IO*>(a.weight) + id * a.sw;
-    float s = 0.0f;
-    for (int c = threadIdx.x & 63; c < a.dim; c += 64)
-      s = fmaf(io_traits<IO>::load(x + c), io_traits<IO>::load(w + c), s);
-    s = wave_sum(s);
-    if ((threadIdx.x & 63) == 0) a.picked[static_cast<int64_t>(j) * a.entries + k] = s * a.scale2;
+    a.near[static_cast<int64_t>(j) * a.entries + k] = id;
+    if (id >= 0) atomicOr(where + (id >> tile_shift >> 5), 1u << (id >> tile_shift & 31));
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.where_words; i += 256) a.where[static_cast<int64_t>(j) * a.where_words + i] = where[i];
 }
 
 template <typename IO>
@@ -149,9 +152,13 @@ __global__ __launch_bounds__(256) void pack_weight_kernel(LossArgs a) {
     to_planes<IO>(c < a.dim ? io_traits<IO>::load(w + c) : 0.0f, a.wp + v * a.dpad + c, a.wp_plane, a.planes);
 }
 
-// A row's log-sum-exp from its tiles, in powers of two; every thread of the
-// workgroup takes part and has it.
-__device__ inline float row_lse2(const LossArgs& a, int i, float* meet) {
+// A row's sum of e^z from its tiles, as sum e^from with an integer `from`, so that
+// a logit's distance from it keeps its last bits.  Every thread of the workgroup
+// takes part and has it.
+struct RowSum {
+  float from, sum;
+};
+__device__ inline RowSum row_sum(const LossArgs& a, int i, float* meet) {
   const float2* st = a.stats + static_cast<int64_t>(i) * a.tiles;
   float top = -INFINITY;
   for (int t = threadIdx.x; t < a.tiles; t += 256) top = fmaxf(top, st[t].x);
@@ -161,44 +168,48 @@ __device__ inline float row_lse2(const LossArgs& a, int i, float* meet) {
   top = fmaxf(fmaxf(meet[0], meet[1]), fmaxf(meet[2], meet[3]));
   const float from = top == -INFINITY ? 0.0f : top;
   float s = 0.0f;
-  for (int t = threadIdx.x; t < a.tiles; t += 256) s += st[t].y * exp2f(st[t].x - from);
+  for (int t = threadIdx.x; t < a.tiles; t += 256) s += st[t].y * expf(st[t].x - from);
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) meet[4 + (threadIdx.x >> 6)] = s;
   __syncthreads();
   s = (meet[4] + meet[5]) + (meet[6] + meet[7]);
-  return from + log2f(s);
+  return {from, s};
 }
 
 // Loss and gradient of the rows of a piece: a workgroup of row i writes loss and
 // lse (blockIdx.y 0) and its columns of dz.
 template <typename IO>
-__global__ __launch_bounds__(256) void softmax_kernel(LossArgs a, int first, bool grad, int cols) {
+__global__ __launch_bounds__(256) void softmax_kernel(LossArgs a, int first, bool grad, int cols, int tile_shift) {
   __shared__ float meet[8];
+  __shared__ int2 lost[4];
   const int i = blockIdx.x, j = first + i, live = *a.live;
   if (j >= live) return;
   const int row = a.row_of[j];
-  const float lse2 = row_lse2(a, i, meet);
+  const RowSum all = row_sum(a, i, meet);
+  const int* near = a.near + static_cast<int64_t>(j) * a.entries;
   const float* picked = a.picked + static_cast<int64_t>(j) * a.entries;
   const float* share = a.teacher != nullptr ? a.share + static_cast<int64_t>(row) * a.entries : nullptr;
   if (blockIdx.y == 0) {
+    const float log_sum = logf(all.sum);
     float s = 0.0f;
     for (int k = threadIdx.x; k < a.entries; k += 256)
-      if (id_at(a, row, k) >= 0) {
+      if (near[k] >= 0) {
         const float t = share != nullptr ? share[k] : 1.0f;
-        if (t != 0.0f) s += t * (lse2 - picked[k]);
+        if (t != 0.0f) s += t * ((all.from - picked[k]) + log_sum);
       }
     s = wave_sum(s);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) meet[threadIdx.x >> 6] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
-      s = ((meet[0] + meet[1]) + (meet[2] + meet[3])) * kLn2;
+      s = (meet[0] + meet[1]) + (meet[2] + meet[3]);
       a.loss[row] = a.tau2 * (share != nullptr ? s + a.known[row] : s);
-      a.lse[row] = lse2 * kLn2;
+      a.lse[row] = all.from + log_sum;
     }
   }
   if (!grad) return;
   const float c = (a.row_weight != nullptr ? a.row_weight[row] : 1.0f / static_cast<float>(live)) * a.back;
+  const float by = c / all.sum;
   const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, static_cast<int>(a.vpad));
   const float2* st = a.stats + static_cast<int64_t>(i) * a.tiles;
   const int64_t plane = static_cast<int64_t>(a.piece) * a.vpad;
@@ -206,30 +217,55 @@ __global__ __launch_bounds__(256) void softmax_kernel(LossArgs a, int first, boo
   for (int v = c0 + threadIdx.x; v < c1; v += 256) {
     float p = 0.0f;
     if (v < a.vocab) {
-      float z2;
+      float z;
       if constexpr (sizeof(IO) == 2) {
         const int code = static_cast<const uint16_t*>(a.probs)[i * a.vpad + v];
-        z2 = code == 65535 ? -INFINITY : st[v / kLossVocabTile].x - static_cast<float>(code) * (1.0f / 1024.0f);
+        z = code == 65535 ? -INFINITY : st[v >> tile_shift].x - static_cast<float>(code) * (1.0f / kCodeSteps);
       } else {
-        z2 = static_cast<const float*>(a.probs)[i * a.vpad + v];
+        z = static_cast<const float*>(a.probs)[i * a.vpad + v];
       }
-      p = exp2f(z2 - lse2) * c;
+      p = expf(z - all.from) * by;
     }
     to_planes<IO>(p, dz + v, plane, a.planes);
   }
   __syncthreads();
+  float most = 0.0f;
+  int2 best = make_int2(-1, 0);
   for (int k = threadIdx.x; k < a.entries; k += 256) {
-    const int id = id_at(a, row, k);
+    const int id = near[k];
     if (id < c0 || id >= c1) continue;
     float t = 1.0f;
     if (share != nullptr) {  // all shares of this id
       t = 0.0f;
       for (int q = 0; q < a.entries; ++q)
-        if (id_at(a, row, q) == id) t += share[q];
+        if (near[q] == id) t += share[q];
     }
-    const float d = picked[k] - lse2;
-    const float p = d > -1.0f ? expm1f(d * kLn2) + (1.0f - t) : exp2f(d) - t;
-    to_planes<IO>(p * c, dz + id, plane, a.planes);
+    const float v = fmaf(-t, all.sum, expf(picked[k] - all.from)) * by;
+    to_planes<IO>(v, dz + id, plane, a.planes);
+    const float miss = v - __uint_as_float(static_cast<uint32_t>(bf16_bits(v)) << 16);
+    if (fabsf(miss) > most) {
+      most = fabsf(miss);
+      best = make_int2(id, __float_as_int(miss));
+    }
+  }
+  if constexpr (sizeof(IO) == 2) {
+    // the entry that lost most, of equal ones the one with the lowest id
+    auto better = [](int2 p, int2 q) __attribute__((always_inline)) {
+      const float x = fabsf(__int_as_float(p.y)), y = fabsf(__int_as_float(q.y));
+      return x > y || (x == y && p.x < q.x);
+    };
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const int2 q = make_int2(__shfl_xor(best.x, o, 64), __shfl_xor(best.y, o, 64));
+      if (better(q, best)) best = q;
+    }
+    if ((threadIdx.x & 63) == 0) lost[threadIdx.x >> 6] = best;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < 4; ++w)
+        if (better(lost[w], best)) best = lost[w];
+      a.fix[i * a.fixes + blockIdx.y] = best;
+    }
   }
 }
 
@@ -253,17 +289,23 @@ __global__ __launch_bounds__(1024) void total_kernel(LossArgs a) {
   *a.total = static_cast<float>(a.row_weight != nullptr ? s : s / max(live, 1));
 }
 
-// dx of every row: the splits' sums of a row of this piece, 0 for one that does
-// not count.
+// dx of every row: the splits' sums of a row of this piece and what its dz lost, 0
+// for one that does not count.
 template <typename IO>
 __global__ __launch_bounds__(256) void dx_kernel(LossArgs a, int first) {
   const int row = blockIdx.x, j = a.place[row];
   if (j < 0 ? first != 0 : j < first || j >= first + a.piece) return;
+  const int splits = dx_splits(a, dx_tiles(a, min(a.piece, *a.live - first)));
   for (int c = threadIdx.x; c < a.dim; c += 256) {
     float s = 0.0f;
     if (j >= 0)
-      for (int q = 0; q < a.splits; ++q)
+      for (int q = 0; q < splits; ++q)
         s += a.part[(static_cast<int64_t>(q) * a.piece + (j - first)) * a.dpad + c];
+    if (sizeof(IO) == 2 && j >= 0)
+      for (int q = 0; q < a.fixes; ++q) {
+        const int2 f = a.fix[(j - first) * a.fixes + q];
+        if (f.x >= 0) s = fmaf(__int_as_float(f.y), io_traits<IO>::load(static_cast<const IO*>(a.weight) + f.x * a.sw + c), s);
+      }
     io_traits<IO>::store(static_cast<IO*>(a.dx) + row * a.sdx + c, s);
   }
 }
@@ -282,6 +324,8 @@ __global__ __launch_bounds__(256) void scale_kernel(const IO* in, const float* f
     io_traits<IO>::store(out + i, io_traits<IO>::load(in + i) * f);
 }
 
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
 template <typename IO>
 hipError_t launch_io(const LossArgs& a, hipStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.rows);
@@ -292,15 +336,16 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
     if (a.total != nullptr) total_kernel<<<1, 1024, 0, s>>>(a);
     return a.dweight != nullptr ? launch_dw(a, 0, sizeof(IO) == 2, s) : hipGetLastError();
   }
-  pack_kernel<IO><<<rows, 256, 0, s>>>(a);
+  const int shift = loss_vocab_tile(a.small) == 64 ? 6 : 7;
+  pack_kernel<IO><<<rows, 256, 0, s>>>(a, shift);
   if (a.pack_w) pack_weight_kernel<IO><<<static_cast<unsigned>(a.vocab), 256, 0, s>>>(a);
   for (int p = 0; p < a.pieces; ++p) {
     const int first = p * a.piece;
     const unsigned n = static_cast<unsigned>(std::min(a.piece, a.rows - first));
     hipError_t e = launch_logits(a, first, sizeof(IO) == 2, grad, s);
     if (e != hipSuccess) return e;
-    const int cols = grad ? 8192 : static_cast<int>(a.vpad);
-    softmax_kernel<IO><<<dim3(n, grad ? (static_cast<unsigned>(a.vpad) + cols - 1) / cols : 1), 256, 0, s>>>(a, first, grad, cols);
+    const int64_t cols = grad ? up256((a.vpad + a.fixes - 1) / a.fixes) : a.vpad;
+    softmax_kernel<IO><<<dim3(n, grad ? a.fixes : 1), 256, 0, s>>>(a, first, grad, static_cast<int>(cols), shift);
     if (a.dx != nullptr) {
       if ((e = launch_dx(a, first, s)) != hipSuccess) return e;
       dx_kernel<IO><<<rows, 256, 0, s>>>(a, first);

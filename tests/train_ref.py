@@ -131,8 +131,8 @@ def loss_ref(x, weight, ids, teacher=None, row_weight=None, tau=1.0, scale=1.0, 
     dz = f * (p - dense)
     e_soft = p * (e_p + e_lse[:, None] + 8 * U)
     if bf16:
-        # the code of a logit, dropped 64 powers of two below its tile; then dz
-        code = p * (2.0 ** -11 * 0.6932) + 2.0 ** -60
+        # the code of a logit, dropped 64 below its tile's largest; then dz
+        code = p * 2.0 ** -11 + 2.0 ** -90
         e_dz = torch.where(hit, e_soft + 2 * U, e_soft + code * 1.01)
         e_dz = f.abs() * e_dz + half_step(torch.bfloat16) * 1.01 * dz.abs()
     else:
