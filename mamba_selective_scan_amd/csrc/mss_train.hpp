@@ -77,24 +77,27 @@ struct LossArgs {
   uint32_t* where; // [rows][where_words] the tiles that hold one of them, a bit each
   int where_words;
   float* picked;   // [rows][entries] their logits
-  // rows and weights as bf16 operands: one plane, or three whose sum is the fp32 value
-  uint16_t* xp;    // [planes][rows][dpad]
-  uint16_t* wp;    // [planes][vocab][dpad], or the weight itself
+  // Rows, weights and dz as bf16 operands of the products: one plane, or three
+  // whose sum is the fp32 value.  They lie in panels 64 columns wide, [columns / 64]
+  // [rows][64], so that a tile's part of any of them is one stretch of memory.
   int planes;
-  int64_t dpad, wp_stride, wp_plane;
-  int wcols;       // columns of wp's rows that may be read, a multiple of 8
+  int64_t dpad;    // columns of x and weight, a multiple of 64
+  uint16_t* xp;    // [planes][dpad / 64][xrows][64]
+  int64_t xrows;   // a multiple of 64; those behind the last row that counts, to the next 64, are 0
+  uint16_t* wp;    // [planes][dpad / 64][vocab][64], or the weight itself
   bool pack_w;
   bool small;      // small tiles of the products
   // of a piece of rows
-  int piece;       // rows of a piece
+  int piece;       // rows of a piece, a multiple of 64
   int pieces;
   int tiles;       // vocabulary tiles, whose entries share a maximum
-  int64_t vpad;
+  int64_t vpad;    // columns of dz, a multiple of 64
   float2* stats;   // [piece][tiles] an integer R and the sum of e^(z - R)
-  void* probs;     // [piece][vpad] codes of the logits (bf16), or the logits (fp32)
-  uint16_t* dz;    // [planes][piece][vpad] (bf16: probs itself)
-  int2* fix;       // [piece][fixes] (bf16) id and what its dz lost by its rounding, as float bits; or id -1
-  int fixes;
+  float2* sums;    // [piece] `from` and c / sum, the row's sum of e^z being sum e^from
+  void* probs;     // [vpad / 64][piece][64] codes of the logits (bf16), or the logits (fp32)
+  uint16_t* dz;    // [planes][vpad / 64][piece][64] (bf16: probs itself)
+  float* value;    // [piece][entries] dz of the entries
+  int2* fix;       // [piece] (bf16) id and what its dz lost by its rounding, as float bits; or id -1
   float* part;     // [splits][piece][dpad]
   int splits;      // at most
   float* dw_sum;   // [vocab][dpad] (more than one piece)

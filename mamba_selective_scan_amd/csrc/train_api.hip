@@ -67,13 +67,13 @@ size_t norm_bwd_workspace(const mss_layer_norm_bwd_args* a) {
 
 // How a loss is cut: rows in pieces whose dz stays within kPieceBytes, and the
 // dx product over the vocabulary.
-constexpr int64_t kPieceBytes = int64_t{1} << 30;
+constexpr int64_t kPieceBytes = int64_t{2} << 30;
 
 struct LossPlan {
   bool grad, pack_w, small;
-  int64_t planes, dpad, vpad, tiles, words, piece, pieces, splits, fixes;
-  size_t live, row_of, place, counts, share, known, near, where, picked, xp, wp, stats, probs, dz, fix, part, dw_sum,
-      bytes;
+  int64_t planes, dpad, vpad, tiles, words, piece, pieces, splits, xrows;
+  size_t live, row_of, place, counts, share, known, near, where, picked, xp, wp, stats, sums, probs, dz, value, fix, part,
+      dw_sum, bytes;
 };
 
 LossPlan loss_plan(const mss_linear_loss_args* a) {
@@ -82,7 +82,7 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.grad = a->dx != nullptr || a->dweight != nullptr;
   p.planes = f32 ? 3 : 1;
   p.dpad = up(a->dim, 64);
-  p.vpad = up(a->vocab, 256);
+  p.vpad = up(a->vocab, 64);
   p.small = a->rows <= 128;
   p.tiles = (a->vocab + mss::loss_vocab_tile(p.small) - 1) / mss::loss_vocab_tile(p.small);
   p.words = (p.tiles + 31) / 32;
@@ -98,8 +98,7 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.pieces = (rows + p.piece - 1) / p.piece;
   // parts of the dx product, within 512 MiB of them
   p.splits = std::clamp<int64_t>((int64_t{1} << 29) / (p.piece * p.dpad * 4), 1, 64);
-  // workgroups of a row's softmax: as many as give 512, each with 2048 columns or more
-  p.fixes = std::clamp<int64_t>(std::min((rows + 511) / rows, p.vpad / 2048), 1, 64);
+  p.xrows = up(rows, 64);
   size_t at = 0;
   auto room = [&](int64_t n) {
     const size_t here = at;
@@ -115,12 +114,14 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.near = room(rows * a->entries * 4);
   p.where = room(rows * p.words * 4);
   p.picked = room(rows * a->entries * 4);
-  p.xp = room(p.planes * rows * p.dpad * 2);
+  p.xp = room(p.planes * p.xrows * p.dpad * 2);
   p.wp = room(p.pack_w ? p.planes * a->vocab * p.dpad * 2 : 0);
   p.stats = room(p.piece * p.tiles * 8);
+  p.sums = room(p.grad ? p.piece * 8 : 0);
   p.probs = room(p.grad ? p.piece * p.vpad * (f32 ? 4 : 2) : 0);
   p.dz = p.grad && f32 ? room(3 * p.piece * p.vpad * 2) : p.probs;
-  p.fix = room(p.grad && !f32 ? p.piece * p.fixes * 8 : 0);
+  p.value = room(p.grad ? p.piece * a->entries * 4 : 0);
+  p.fix = room(p.grad && !f32 ? p.piece * 8 : 0);
   p.part = room(a->dx != nullptr ? p.splits * p.piece * p.dpad * 4 : 0);
   p.dw_sum = room(a->dweight != nullptr && p.pieces > 1 ? a->vocab * p.dpad * 4 : 0);
   p.bytes = at;
@@ -322,9 +323,7 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.xp = reinterpret_cast<uint16_t*>(ws + p.xp);
   k.pack_w = p.pack_w;
   k.wp = p.pack_w ? reinterpret_cast<uint16_t*>(ws + p.wp) : const_cast<uint16_t*>(static_cast<const uint16_t*>(a->weight));
-  k.wp_stride = p.pack_w ? p.dpad : std::max(a->weight_stride, D);
-  k.wp_plane = V * p.dpad;
-  k.wcols = static_cast<int>(p.pack_w ? p.dpad : D);
+  k.xrows = p.xrows;
   k.small = p.small;
   k.piece = static_cast<int>(p.piece);
   k.pieces = static_cast<int>(p.pieces);
@@ -334,7 +333,8 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.probs = ws + p.probs;
   k.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
   k.fix = reinterpret_cast<int2*>(ws + p.fix);
-  k.fixes = static_cast<int>(p.fixes);
+  k.value = reinterpret_cast<float*>(ws + p.value);
+  k.sums = reinterpret_cast<float2*>(ws + p.sums);
   k.part = reinterpret_cast<float*>(ws + p.part);
   k.splits = static_cast<int>(p.splits);
   k.dw_sum = reinterpret_cast<float*>(ws + p.dw_sum);

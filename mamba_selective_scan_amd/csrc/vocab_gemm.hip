@@ -32,14 +32,14 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 64;  // of the summed axis
 
-// One operand of a tile: `rows` rows of the tile's axis from `base`, or with the
-// other axis contiguous rows of the summed one.  `span` bytes from base on may be
-// read.
+// One operand of a tile, in bytes: rows of the tile's axis from `base` on, or rows
+// of the summed one with the tile's axis contiguous.  A row is `stride` behind the
+// one before it, its columns 64 .. 127 are `panel` behind its columns 0 .. 63.
+// `span` from base on may be read (of a plane).
 struct Side {
   const char* base;
-  int64_t plane;  // bytes
-  int64_t span;
-  int stride;     // bytes
+  int64_t plane, span, panel;
+  int stride;
 };
 
 __device__ inline int plane_of(int pair, bool second) {
@@ -57,63 +57,72 @@ struct Panel {
   static constexpr int kVecs = KC ? 8 : ROWS / 8;  // 16-byte vectors of a row
   static_assert(kBytes % (16 * NT) == 0 && NT % kVecs == 0, "whole loads");
 
-  // The vector in which vector c of row r lies.  KC: eight rows side by side are
-  // read at one vector each, so they spread over the eight.  Otherwise rows r ..
+  // The vector in which vector c of row r lies.  KC: sixteen rows side by side are
+  // read at one vector each, two rows to the width of all banks, so every two
+  // spread over the eight.  Otherwise rows r ..
   // r + 3 and r + 8 .. r + 11 are read at 64 bytes each: they spread over the
   // 64-byte parts of a row as far as there are any.
   __device__ static inline int swizzle(int r, int c) {
-    if constexpr (KC) return c ^ (r & 7);
+    if constexpr (KC) return c ^ (r >> 1 & 7);
     if constexpr (kVecs >= 32) return c ^ (((r & 3) | (r >> 1 & 4)) << 2);
     if constexpr (kVecs == 16) return c ^ ((r & 3) << 2);
     return c ^ ((r >> 1 & 1) << 2);
   }
   __device__ static inline int first_row() { return static_cast<int>(threadIdx.x) / kVecs; }
-  // vector in memory of this thread's loads (the same for all: rows a whole
-  // number of swizzle periods apart)
-  __device__ static inline int column() {
-    static_assert((NT / kVecs) % (KC ? 8 : 16) == 0 || kLoads == 1, "loads share their swizzle");
-    return swizzle(first_row(), static_cast<int>(threadIdx.x) % kVecs);
+  // vector in memory of this thread's loads: the same for all whose rows are a
+  // whole number of swizzle periods apart, which every second or every one is
+  static constexpr int kApart = NT / kVecs;
+  static_assert(kApart % (KC ? 16 : 8) == 0 && (KC || kApart % 16 == 0 || kVecs == 32), "loads share one or two swizzles");
+  __device__ static inline int column(int i) {
+    return swizzle(first_row() + i * kApart, static_cast<int>(threadIdx.x) % kVecs);
   }
 
-  // Loads of one step from summed index k on.  `dim`: where the summed axis ends
-  // in a row (KC), a multiple of 8.
-  __device__ static inline void load(const Side& s, int64_t at, int k, int dim, char MSS_LDS* lds) {
-    const int64_t from = KC ? static_cast<int64_t>(k) * 2 : static_cast<int64_t>(k) * s.stride;
-    const int64_t left = s.span - from;
-    const int range = static_cast<int>(left < 0 ? 0 : left < kRsrcRange ? left : kRsrcRange);
-    const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(s.base) + at + from, 0, range, kRsrcFlags);
-    const int col = column();
-    uint32_t off = static_cast<uint32_t>(first_row() * s.stride + col * 16);
-    uint32_t next = static_cast<uint32_t>(NT / kVecs * s.stride);
-    if (KC && k + col * 8 >= dim) {
-      off = kOffNone;
-      next = 0;
+  // One step's loads, from summed index k on (none if it is past the end: they
+  // read 0).  `dim`: where the summed axis ends in a row (KC), a multiple of 8.
+  struct Loads {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t off, odd, next;
+    char MSS_LDS* lds;
+    __device__ inline Loads(const Side& s, int64_t at, int k, int dim, bool any, char MSS_LDS* stage) {
+      const int64_t from = KC ? k / kStep * s.panel : static_cast<int64_t>(k) * s.stride;
+      const int64_t left = any ? s.span - from : 0;
+      const int range = static_cast<int>(left < 0 ? 0 : left < kRsrcRange ? left : kRsrcRange);
+      rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(s.base) + at + from, 0, range, kRsrcFlags);
+      const uint32_t row = static_cast<uint32_t>(first_row() * s.stride), panel = static_cast<uint32_t>(s.panel);
+      off = row + column(0) / 8 * panel + column(0) % 8 * 16;
+      odd = row + column(1) / 8 * panel + column(1) % 8 * 16;
+      next = static_cast<uint32_t>(kApart * s.stride);
+      if (KC && k + column(0) * 8 >= dim) {
+        off = odd = kOffNone;
+        next = 0;
+      }
+      lds = stage + uniform(static_cast<int>(threadIdx.x) >> 6) * 1024;
     }
-    const int wave = uniform(static_cast<int>(threadIdx.x) >> 6);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, reinterpret_cast<MSS_LDS void*>(lds + (i * NT + wave * 64) * 16), 16,
-                                               off, 0, 0, 0);
-      off += next;
+    __device__ inline void issue(int i) const {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MSS_LDS void*)(lds + i * NT * 16), 16, (i & 1 ? odd : off) + i * next, 0, 0, 0);
     }
-  }
+  };
 
-  // The fragment of rows row .. row + 31 at summed indices 16 ks .. 16 ks + 15.
-  __device__ static inline bf16x8 fragment(const char MSS_LDS* lds, int row, int ks) {
+  // The fragments of N x 32 rows from `row` on, at summed indices 16 ks .. 16 ks + 15.
+  static constexpr int kReads = KC ? 1 : 2;  // LDS reads of one
+  template <int N>
+  __device__ static inline void fragments(const char MSS_LDS* lds, int row, int ks, bf16x8 (&f)[N]) {
     const int lane = static_cast<int>(threadIdx.x) & 63;
     if constexpr (KC) {
-      const int r = row + (lane & 31);
-      return *reinterpret_cast<const bf16x8 MSS_LDS*>(lds + r * 128 + swizzle(r, 2 * ks + (lane >> 5)) * 16);
+      const char MSS_LDS* p = lds + (row + (lane & 31)) * 128 + swizzle(lane, 2 * ks + (lane >> 5)) * 16;
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = *reinterpret_cast<const bf16x8 MSS_LDS*>(p + i * 32 * 128);
     } else {
       // a group of 16 lanes reads 4 rows of 32 bytes and turns them about
-      const int k = ks * 16 + 8 * (lane >> 5) + ((lane & 15) >> 2);
-      const int c = row / 8 + 2 * (lane >> 4 & 1) + ((lane & 3) >> 1);
-      const char MSS_LDS* p = lds + k * (ROWS * 2) + swizzle(k, c) * 16 + (lane & 1) * 8;
-      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          reinterpret_cast<s16x4 MSS_LDS*>(const_cast<char MSS_LDS*>(p)));
-      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          reinterpret_cast<s16x4 MSS_LDS*>(const_cast<char MSS_LDS*>(p + 4 * ROWS * 2)));
-      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+      const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = row / 8 + 4 * i + 2 * (lane >> 4 & 1) + ((lane & 3) >> 1);
+        const char MSS_LDS* p = lds + k * (ROWS * 2) + swizzle(k, c) * 16 + (lane & 1) * 8 + ks * 16 * ROWS * 2;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 MSS_LDS*)p);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 MSS_LDS*)(p + 4 * ROWS * 2));
+        f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
     }
   }
 };
@@ -129,47 +138,98 @@ struct Tile {
   __device__ static inline int wave_m() { return uniform(static_cast<int>(threadIdx.x) >> 6) / WN * (32 * IM); }
   __device__ static inline int wave_n() { return uniform(static_cast<int>(threadIdx.x) >> 6) % WN * (32 * IN); }
 
-  // What one stage adds.
-  __device__ static inline void multiply(const char MSS_LDS* now, f32x16 (&acc)[IM][IN]) {
-    const int m0 = wave_m(), n0 = wave_n();
-#pragma unroll
-    for (int ks = 0; ks < kStep / 16; ++ks) {
-      bf16x8 fa[IM], fb[IN];
-#pragma unroll
-      for (int i = 0; i < IM; ++i) fa[i] = A::fragment(now, m0 + 32 * i, ks);
-#pragma unroll
-      for (int j = 0; j < IN; ++j) fb[j] = B::fragment(now + A::kBytes, n0 + 32 * j, ks);
+  struct Frags {
+    bf16x8 a[IM], b[IN];
+    __device__ inline void read(const char MSS_LDS* stage, int ks) {
+      A::fragments(stage, wave_m(), ks, a);
+      B::fragments(stage + A::kBytes, wave_n(), ks, b);
+    }
+    __device__ inline void multiply(f32x16 (&acc)[IM][IN]) const {
 #pragma unroll
       for (int i = 0; i < IM; ++i)
 #pragma unroll
-        for (int j = 0; j < IN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < IN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  // What one stage adds.
+  __device__ static inline void multiply(const char MSS_LDS* stage, f32x16 (&acc)[IM][IN]) {
+#pragma unroll
+    for (int ks = 0; ks < kStep / 16; ++ks) {
+      Frags f;
+      f.read(stage, ks);
+      f.multiply(acc);
     }
   }
 
   // The sum over summed indices [k0, k1) (k0 a multiple of 64) of all pairs of planes.
+  // While a part's products run, the next part's fragments are read.  At a step's
+  // last part they come from the other stage, whose loads had a step's time to
+  // land; then every wave has read this stage, and the loads of the step after the
+  // next go there.
   __device__ static inline void run(const Side& a, const Side& b, int k0, int k1, int dim, int pairs, char MSS_LDS* lds,
                                     f32x16 (&acc)[IM][IN]) {
-    const int steps = (k1 - k0 + kStep - 1) / kStep, total = steps * pairs;
-    int pair = 0, k = k0;
-    auto load = [&](char MSS_LDS* stage) __attribute__((always_inline)) {
-      A::load(a, plane_of(pair, false) * a.plane, k, dim, stage);
-      B::load(b, plane_of(pair, true) * b.plane, k, dim, stage + A::kBytes);
+    const int total = (k1 - k0 + kStep - 1) / kStep * pairs;
+    if (total <= 0) return;
+    int pair = 0, k = k0, asked = 0;
+    auto advance = [&]() __attribute__((always_inline)) {
+      ++asked;
       k += kStep;
       if (k >= k1) {
         k = k0;
         ++pair;
       }
     };
-    if (total > 0) load(lds);
-    for (int s = 0; s < total; ++s) {
-      // this wave's loads have landed, then all waves': and all have read the
-      // other stage, which the next loads overwrite
-      __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-      __syncthreads();
-      if (s + 1 < total) load(lds + (~s & 1) * kStage);
-      multiply(lds + (s & 1) * kStage, acc);
+    auto load = [&](char MSS_LDS* stage) __attribute__((always_inline)) {
+      const typename A::Loads la(a, plane_of(pair, false) * a.plane, k, dim, asked < total, stage);
+      const typename B::Loads lb(b, plane_of(pair, true) * b.plane, k, dim, asked < total, stage + A::kBytes);
+#pragma unroll
+      for (int i = 0; i < A::kLoads; ++i) la.issue(i);
+#pragma unroll
+      for (int i = 0; i < B::kLoads; ++i) lb.issue(i);
+      advance();
+    };
+    constexpr int kLoads = A::kLoads + B::kLoads, kReads = IM * A::kReads + IN * B::kReads;
+    load(lds);
+    load(lds + kStage);
+    wait_loads<kLoads>();
+    __syncthreads();
+    Frags now, next;
+    now.read(lds, 0);
+    for (int s = 0; s < total; s += 2) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (half == 1 && s + 1 >= total) break;
+        char MSS_LDS* here = lds + half * kStage;
+        char MSS_LDS* there = lds + (1 - half) * kStage;
+#pragma unroll
+        for (int ks = 0; ks < kStep / 16; ++ks) {
+          if (ks < kStep / 16 - 1) {
+            next.read(here, ks + 1);
+          } else {
+            wait_loads<0>();
+            __syncthreads();
+            next.read(there, 0);
+            load(here);
+          }
+          now.multiply(acc);
+#pragma unroll
+          for (int m = 0; m < IM * IN; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product,
+            __builtin_amdgcn_sched_group_barrier(0x100, (kReads + IM * IN - 1) / (IM * IN), 0);  // LDS reads
+            if (ks == kStep / 16 - 1) __builtin_amdgcn_sched_group_barrier(0x010, (kLoads + IM * IN - 1) / (IM * IN), 0);
+          }
+          now = next;
+        }
+      }
     }
+    wait_loads<0>();
     __syncthreads();  // (the stages are free)
+  }
+  template <int N>
+  __device__ static inline void wait_loads() {
+    static_assert(N < 64, "a six-bit count");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);  // vmcnt(N)
   }
 };
 
@@ -186,18 +246,41 @@ __device__ inline int acc_row(int e) { return 8 * (e >> 2) + 4 * (static_cast<in
 
 __device__ inline int live_rows(const LossArgs& a, int first) { return max(min(a.piece, *a.live - first), 0); }
 
+// The operands.
+__device__ inline Side x_side(const LossArgs& a, int row, int d) {
+  const int64_t panel = a.xrows * 128, from = d / 64 * panel + static_cast<int64_t>(row) * 128;
+  return {reinterpret_cast<const char*>(a.xp) + from, a.xrows * a.dpad * 2, a.xrows * a.dpad * 2 - from, panel, 128};
+}
+__device__ inline Side w_side(const LossArgs& a, int v, int d) {
+  if (a.pack_w) {
+    const int64_t panel = static_cast<int64_t>(a.vocab) * 128, from = d / 64 * panel + static_cast<int64_t>(v) * 128;
+    return {reinterpret_cast<const char*>(a.wp) + from, a.vocab * a.dpad * 2, a.vocab * a.dpad * 2 - from, panel, 128};
+  }
+  const int64_t from = (v * a.sw + d) * 2;
+  return {reinterpret_cast<const char*>(a.wp) + from, 0, ((a.vocab - 1) * a.sw + a.dim) * 2 - from, 128,
+          static_cast<int>(a.sw * 2)};
+}
+__device__ inline Side z_side(const LossArgs& a, int row, int v) {
+  const int64_t panel = static_cast<int64_t>(a.piece) * 128, from = v / 64 * panel + static_cast<int64_t>(row) * 128;
+  return {reinterpret_cast<const char*>(a.dz) + from, a.piece * a.vpad * 2, a.piece * a.vpad * 2 - from, panel, 128};
+}
+// Where the summed axis of logits ends in the rows of weights.
+__device__ inline int w_cols(const LossArgs& a) { return a.pack_w ? static_cast<int>(a.dpad) : a.dim; }
+
 // Which tile of mt x nt a workgroup takes: workgroups of one XCD (every eighth)
 // take tiles side by side, in strips of 4 of the first axis, so that what one
 // reads the others find in the XCD's cache.
 struct At {
   int m, n;
 };
+__device__ inline At tile_of(int l, int mt, int nt) {
+  const int strip = l / (4 * nt), in = l - strip * 4 * nt, wide = min(4, mt - strip * 4);
+  return {strip * 4 + in % wide, in / wide};
+}
 __device__ inline At tile_at(int id, int mt, int nt) {
   const int total = mt * nt, per = (total + 7) / 8;
   const int l = (id & 7) * per + (id >> 3);
-  if ((id >> 3) >= per || l >= total) return {-1, -1};
-  const int strip = l / (4 * nt), in = l - strip * 4 * nt, wide = min(4, mt - strip * 4);
-  return {strip * 4 + in % wide, in / wide};
+  return (id >> 3) >= per || l >= total ? At{-1, -1} : tile_of(l, mt, nt);
 }
 unsigned tile_blocks(int64_t mt, int64_t nt) { return static_cast<unsigned>((mt * nt + 7) / 8 * 8); }
 
@@ -212,15 +295,10 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
   const At at = tile_at(blockIdx.x, (a.vocab + T::kM - 1) / T::kM, (rows + T::kN - 1) / T::kN);
   if (at.m < 0) return;
   const int v0 = at.m * T::kM, i0 = at.n * T::kN;
-  const int ws = static_cast<int>(a.wp_stride * 2), xs = static_cast<int>(a.dpad * 2);
-  const Side w{reinterpret_cast<const char*>(a.wp) + static_cast<int64_t>(v0) * ws, a.wp_plane * 2,
-               static_cast<int64_t>(a.vocab - v0 - 1) * ws + a.wcols * 2, ws};
-  const Side x{reinterpret_cast<const char*>(a.xp) + static_cast<int64_t>(first + i0) * xs,
-               static_cast<int64_t>(a.rows) * xs, static_cast<int64_t>(rows - i0) * xs, xs};
   f32x16 acc[IM][IN];
   clear(acc);
   char MSS_LDS* sh = (char MSS_LDS*)lds;
-  T::run(w, x, 0, a.dim, a.wcols, a.planes == 1 ? 1 : 6, sh, acc);
+  T::run(w_side(a, v0, 0), x_side(a, first + i0, 0), 0, a.dim, w_cols(a), a.planes == 1 ? 1 : 6, sh, acc);
 
   constexpr int kWide = 32 * IM;  // entries of a wave: those that share a maximum
   const int wv = v0 + T::wave_m(), wi = i0 + T::wave_n();
@@ -274,16 +352,15 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
       }
     }
     if (keep) {
-      // 8 entries a lane, rows one behind another
-      constexpr int kRow = kWide / 8, kRows = 64 / kRow;
+      // 8 entries a lane, 8 rows of a panel one behind another
 #pragma unroll
-      for (int q = 0; q < 32 / kRows; ++q) {
-        const int r = q * kRows + lane / kRow, c = lane % kRow, turn = r & (kWide / 4 - 1);
+      for (int q = 0; q < kWide / 64 * 4; ++q) {
+        const int r = q % 4 * 8 + (lane >> 3), c = q / 4 * 8 + (lane & 7), turn = r & (kWide / 4 - 1);
         const f32x4 lo = *reinterpret_cast<const f32x4 MSS_LDS*>(mine + r * kWide + ((2 * c) ^ turn) * 4);
         const f32x4 hi = *reinterpret_cast<const f32x4 MSS_LDS*>(mine + r * kWide + ((2 * c + 1) ^ turn) * 4);
         const float t = __shfl(top, r, 64);
-        if (wi + 32 * j + r >= rows) continue;
-        const int64_t o = static_cast<int64_t>(wi + 32 * j + r) * a.vpad + wv + 8 * c;
+        if (wi + 32 * j + r >= rows || wv + q / 4 * 64 >= a.vocab) continue;
+        const int64_t o = (static_cast<int64_t>(wv / 64 + q / 4) * a.piece + wi + 32 * j + r) * 64 + (lane & 7) * 8;
         if constexpr (BF16) {
           uint32_t code[8];
 #pragma unroll
@@ -313,21 +390,18 @@ __global__ __launch_bounds__(T::kThreads) void dx_part_kernel(LossArgs a, int fi
   const int rows = live_rows(a, first), lane = threadIdx.x & 63;
   const int mt = (rows + T::kM - 1) / T::kM, nt = (a.dim + T::kN - 1) / T::kN;
   if (mt == 0) return;
+  // tiles of one part side by side: those of an XCD read the same rows of weights
   const int splits = dx_splits(a, mt * nt), per = (a.vocab + kStep - 1) / kStep;
-  const int split = blockIdx.x % splits;
-  const At at = tile_at(blockIdx.x / splits, mt, nt);
-  if (at.m < 0) return;
+  const int all = mt * nt * splits, share = (all + 7) / 8, l = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= share || l >= all) return;
+  const int split = l / (mt * nt);
+  const At at = tile_of(l - split * (mt * nt), mt, nt);
   const int k0 = static_cast<int>(static_cast<int64_t>(per) * split / splits) * kStep;
   const int k1 = static_cast<int>(static_cast<int64_t>(per) * (split + 1) / splits) * kStep;
   const int i0 = at.m * T::kM, d0 = at.n * T::kN;
-  const int zs = static_cast<int>(a.vpad * 2), ws = static_cast<int>(a.wp_stride * 2);
-  const Side z{reinterpret_cast<const char*>(a.dz) + static_cast<int64_t>(i0) * zs, static_cast<int64_t>(a.piece) * zs,
-               static_cast<int64_t>(rows - i0) * zs, zs};
-  const Side w{reinterpret_cast<const char*>(a.wp + d0), a.wp_plane * 2,
-               static_cast<int64_t>(a.vocab - 1) * ws + (a.wcols - d0) * 2, ws};
   f32x16 acc[IM][IN];
   clear(acc);
-  T::run(z, w, k0, k1, k1, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
+  T::run(z_side(a, i0, 0), w_side(a, 0, d0), k0, k1, k1, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
   float* part = a.part + static_cast<int64_t>(split) * a.piece * a.dpad;
 #pragma unroll
   for (int i = 0; i < IM; ++i)
@@ -360,7 +434,7 @@ __device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, 
       const int r = q / T::B::kVecs, c = q % T::B::kVecs, d = d0 + c * 8;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (r < n && d < a.dpad)
-        x = *reinterpret_cast<const uint4*>(a.xp + (first + list[r].x) * a.dpad + d);
+        x = *reinterpret_cast<const uint4*>(a.xp + (d / 64 * a.xrows + first + list[r].x) * 64 + d % 64);
       *reinterpret_cast<uint4*>(lds + T::A::kBytes + (r * T::B::kVecs + T::B::swizzle(r, c)) * 16) = x;
     }
     __syncthreads();
@@ -373,10 +447,9 @@ __device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, 
     T::multiply(sh, acc);
     __syncthreads();
   };
-  const int all = rows * a.fixes;
-  for (int base = 0; base < all; base += T::kThreads) {
+  for (int base = 0; base < rows; base += T::kThreads) {
     int2 f = make_int2(-1, 0);
-    if (base + t < all) f = a.fix[base + t];
+    if (base + t < rows) f = a.fix[base + t];
     const bool in = f.x >= v0 && f.x < v0 + T::kM;
     const uint64_t mask = __ballot(in);
     if (lane == 0) counts[wave] = __popcll(mask);
@@ -387,7 +460,7 @@ __device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, 
       if (w < wave) at += counts[w];
       sum += counts[w];
     }
-    if (in) list[at] = make_int2((base + t) / a.fixes, (f.x - v0) << 16 | bf16_bits(__int_as_float(f.y)));
+    if (in) list[at] = make_int2(base + t, (f.x - v0) << 16 | bf16_bits(__int_as_float(f.y)));
     __syncthreads();
     held += sum;
     while (held >= kStep) {
@@ -412,14 +485,9 @@ __global__ __launch_bounds__(T::kThreads) void dw_tile_kernel(LossArgs a, int fi
   const At at = tile_at(blockIdx.x, (a.vocab + T::kM - 1) / T::kM, (a.dim + T::kN - 1) / T::kN);
   if (at.m < 0) return;
   const int v0 = at.m * T::kM, d0 = at.n * T::kN;
-  const int zs = static_cast<int>(a.vpad * 2), xs = static_cast<int>(a.dpad * 2);
-  const Side z{reinterpret_cast<const char*>(a.dz + v0), static_cast<int64_t>(a.piece) * zs,
-               static_cast<int64_t>(rows) * zs - v0 * 2, zs};
-  const Side x{reinterpret_cast<const char*>(a.xp + first * a.dpad + d0), static_cast<int64_t>(a.rows) * xs,
-               static_cast<int64_t>(rows) * xs - d0 * 2, xs};
   f32x16 acc[IM][IN];
   clear(acc);
-  T::run(z, x, 0, rows, rows, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
+  T::run(z_side(a, 0, v0), x_side(a, first, d0), 0, rows, rows, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
   if (a.planes == 1) add_lost<T>(a, first, rows, v0, d0, lds, acc);
   const int d1 = d0 + T::wave_n() + (lane & 31);
 #pragma unroll
@@ -474,7 +542,7 @@ hipError_t launch_dx(const LossArgs& a, int first, hipStream_t stream) {
   int64_t g = 0;  // the most that any count of live rows asks for
   for (int64_t mt = 1; mt <= tiles(n, m); ++mt) {
     const int64_t t = mt * tiles(a.dim, w);
-    g = std::max<int64_t>(g, (t + 7) / 8 * 8 * dx_splits(a, static_cast<int>(t)));
+    g = std::max<int64_t>(g, (t * dx_splits(a, static_cast<int>(t)) + 7) / 8 * 8);
   }
   if (a.small) dx_part_kernel<Tile<true, false, 2, 2, 1, 2>, 1, 2><<<static_cast<unsigned>(g), 256, 0, stream>>>(a, first);
   else dx_part_kernel<Big<true, false>, 4, 2><<<static_cast<unsigned>(g), 512, 0, stream>>>(a, first);

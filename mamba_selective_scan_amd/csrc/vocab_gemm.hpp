@@ -13,15 +13,17 @@ namespace mss {
 constexpr float kCodeSteps = 1024.0f;
 
 // How many parts of the vocabulary the dx product is cut into, for `tiles` tiles
-// of its rows and columns: as many as fill the card (256 workgroups of large
-// tiles at a time, 768 of small ones) best, a part costing some steps besides its
-// own.  Host and device agree on it.
+// of its rows and columns: the least time, in steps of about a microsecond, of the
+// rounds that the parts' workgroups make (256 of large tiles at a time, 768 of
+// small ones), each with some steps besides its own, and of writing and adding
+// the parts.  Host and device agree on it.
 __host__ __device__ inline int dx_splits(const LossArgs& a, int tiles) {
   const float slots = a.small ? 768.0f : 256.0f, steps = static_cast<float>((a.vocab + 63) / 64);
+  const float part = a.small ? 0.016f : 0.13f;
   int best = 1;
   float least = 3e38f;
   for (int s = 1; s <= a.splits; s += s < 8 ? 1 : s / 4) {
-    const float t = ceilf(static_cast<float>(tiles) * s / slots) * (steps / s + 6.0f) + 1.0f * s;
+    const float n = static_cast<float>(tiles) * s, t = ceilf(n / slots) * (steps / s + 6.0f) + n * part;
     if (t < least) {
       least = t;
       best = s;

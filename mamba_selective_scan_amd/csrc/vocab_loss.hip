@@ -108,32 +108,39 @@ __global__ __launch_bounds__(1024) void place_kernel(LossArgs a) {
   if (threadIdx.x == 0) *a.live = base;
 }
 
-// An fp32 value as the sum of three bf16 ones (exact: 3 x 8 bits), or a bf16 one.
-template <typename IO>
-__device__ inline void to_planes(float v, uint16_t* p, int64_t plane, int planes) {
+// 8 values as bf16, or as three bf16 planes whose sums they are (exact: 3 x 8 bits).
+__device__ inline void to_planes(float (&v)[8], uint16_t* p, int64_t plane, int planes) {
   for (int i = 0; i < planes; ++i) {
-    const uint16_t q = bf16_bits(v);
-    p[i * plane] = q;
-    v -= __uint_as_float(static_cast<uint32_t>(q) << 16);
+    uint32_t q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      q[e] = bf16x2_bits(v[2 * e], v[2 * e + 1]);
+      v[2 * e] -= __uint_as_float(q[e] << 16);
+      v[2 * e + 1] -= __uint_as_float(q[e] & 0xffff0000u);
+    }
+    *reinterpret_cast<uint4*>(p + i * plane) = make_uint4(q[0], q[1], q[2], q[3]);
   }
 }
 
 constexpr int kMaxWords = (1 << 22) / 64 / 32;  // of the largest vocabulary's tiles
 
 // One workgroup a row that counts: its x as an operand, its ids, and the tiles of
-// the vocabulary that hold one.
+// the vocabulary that hold one.  The rows behind the last one, up to the next 64,
+// are 0.
 template <typename IO>
 __global__ __launch_bounds__(256) void pack_kernel(LossArgs a, int tile_shift) {
-  const int j = blockIdx.x;
-  if (j >= *a.live) return;
-  const int row = a.row_of[j];
-  const IO* x = static_cast<const IO*>(a.x) + row * a.sx;
-  uint16_t* xp = a.xp + j * a.dpad;
-  const int64_t plane = static_cast<int64_t>(a.rows) * a.dpad;
   __shared__ uint32_t where[kMaxWords];
+  const int j = blockIdx.x, live = *a.live;
+  if (j >= (live + 63) / 64 * 64) return;
+  const int row = j < live ? a.row_of[j] : 0;
+  const IO* x = static_cast<const IO*>(a.x) + row * a.sx;
+  for (int c = threadIdx.x * 8; c < a.dpad; c += 2048) {
+    float v[8];
+    load_part<IO, 8>(x + c, j < live ? a.dim - c : 0, v);
+    to_planes(v, a.xp + (c / 64 * a.xrows + j) * 64 + c % 64, a.xrows * a.dpad, a.planes);
+  }
+  if (j >= live) return;
   for (int i = threadIdx.x; i < a.where_words; i += 256) where[i] = 0;
-  for (int c = threadIdx.x; c < a.dpad; c += 256)
-    to_planes<IO>(c < a.dim ? io_traits<IO>::load(x + c) : 0.0f, xp + c, plane, a.planes);
   __syncthreads();
   for (int k = threadIdx.x; k < a.entries; k += 256) {
     const int id = id_at(a, row, k);
@@ -144,12 +151,17 @@ __global__ __launch_bounds__(256) void pack_kernel(LossArgs a, int tile_shift) {
   for (int i = threadIdx.x; i < a.where_words; i += 256) a.where[static_cast<int64_t>(j) * a.where_words + i] = where[i];
 }
 
+// Eight rows of weights a workgroup.
 template <typename IO>
 __global__ __launch_bounds__(256) void pack_weight_kernel(LossArgs a) {
-  const int v = blockIdx.x;
+  const int v = blockIdx.x * 8 + (threadIdx.x >> 3 & 7);
+  if (v >= a.vocab) return;
   const IO* w = static_cast<const IO*>(a.weight) + v * a.sw;
-  for (int c = threadIdx.x; c < a.dpad; c += 256)
-    to_planes<IO>(c < a.dim ? io_traits<IO>::load(w + c) : 0.0f, a.wp + v * a.dpad + c, a.wp_plane, a.planes);
+  for (int c = (threadIdx.x >> 6) * 64 + (threadIdx.x & 7) * 8; c < a.dpad; c += 256) {
+    float q[8];
+    load_part<IO, 8>(w + c, a.dim - c, q);
+    to_planes(q, a.wp + (static_cast<int64_t>(c / 64) * a.vocab + v) * 64 + c % 64, a.vocab * a.dpad, a.planes);
+  }
 }
 
 // A row's sum of e^z from its tiles, as sum e^from with an integer `from`, so that
@@ -176,10 +188,10 @@ __device__ inline RowSum row_sum(const LossArgs& a, int i, float* meet) {
   return {from, s};
 }
 
-// Loss and gradient of the rows of a piece: a workgroup of row i writes loss and
-// lse (blockIdx.y 0) and its columns of dz.
-template <typename IO>
-__global__ __launch_bounds__(256) void softmax_kernel(LossArgs a, int first, bool grad, int cols, int tile_shift) {
+// One workgroup a row of a piece: loss and lse, and with gradients what its dz is
+// made of: the sum, and dz of its entries.  In bf16 the entry that lost most by its
+// rounding, of equal ones the one with the lowest id, is carried apart.
+__global__ __launch_bounds__(256) void row_kernel(LossArgs a, int first, bool bf16, bool grad) {
   __shared__ float meet[8];
   __shared__ int2 lost[4];
   const int i = blockIdx.x, j = first + i, live = *a.live;
@@ -189,82 +201,106 @@ __global__ __launch_bounds__(256) void softmax_kernel(LossArgs a, int first, boo
   const int* near = a.near + static_cast<int64_t>(j) * a.entries;
   const float* picked = a.picked + static_cast<int64_t>(j) * a.entries;
   const float* share = a.teacher != nullptr ? a.share + static_cast<int64_t>(row) * a.entries : nullptr;
-  if (blockIdx.y == 0) {
-    const float log_sum = logf(all.sum);
-    float s = 0.0f;
-    for (int k = threadIdx.x; k < a.entries; k += 256)
-      if (near[k] >= 0) {
-        const float t = share != nullptr ? share[k] : 1.0f;
-        if (t != 0.0f) s += t * ((all.from - picked[k]) + log_sum);
-      }
-    s = wave_sum(s);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) meet[threadIdx.x >> 6] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s = (meet[0] + meet[1]) + (meet[2] + meet[3]);
-      a.loss[row] = a.tau2 * (share != nullptr ? s + a.known[row] : s);
-      a.lse[row] = all.from + log_sum;
-    }
-  }
-  if (!grad) return;
+  const float log_sum = logf(all.sum);
   const float c = (a.row_weight != nullptr ? a.row_weight[row] : 1.0f / static_cast<float>(live)) * a.back;
   const float by = c / all.sum;
-  const int c0 = blockIdx.y * cols, c1 = min(c0 + cols, static_cast<int>(a.vpad));
-  const float2* st = a.stats + static_cast<int64_t>(i) * a.tiles;
-  const int64_t plane = static_cast<int64_t>(a.piece) * a.vpad;
-  uint16_t* dz = a.dz + i * a.vpad;
-  for (int v = c0 + threadIdx.x; v < c1; v += 256) {
-    float p = 0.0f;
-    if (v < a.vocab) {
-      float z;
-      if constexpr (sizeof(IO) == 2) {
-        const int code = static_cast<const uint16_t*>(a.probs)[i * a.vpad + v];
-        z = code == 65535 ? -INFINITY : st[v >> tile_shift].x - static_cast<float>(code) * (1.0f / kCodeSteps);
-      } else {
-        z = static_cast<const float*>(a.probs)[i * a.vpad + v];
-      }
-      p = expf(z - all.from) * by;
-    }
-    to_planes<IO>(p, dz + v, plane, a.planes);
-  }
-  __syncthreads();
-  float most = 0.0f;
+  float s = 0.0f, most = 0.0f;
   int2 best = make_int2(-1, 0);
   for (int k = threadIdx.x; k < a.entries; k += 256) {
     const int id = near[k];
-    if (id < c0 || id >= c1) continue;
-    float t = 1.0f;
+    if (id < 0) continue;
+    float t = share != nullptr ? share[k] : 1.0f;
+    if (t != 0.0f) s += t * ((all.from - picked[k]) + log_sum);
+    if (!grad) continue;
     if (share != nullptr) {  // all shares of this id
       t = 0.0f;
       for (int q = 0; q < a.entries; ++q)
         if (near[q] == id) t += share[q];
     }
     const float v = fmaf(-t, all.sum, expf(picked[k] - all.from)) * by;
-    to_planes<IO>(v, dz + id, plane, a.planes);
+    a.value[static_cast<int64_t>(i) * a.entries + k] = v;
     const float miss = v - __uint_as_float(static_cast<uint32_t>(bf16_bits(v)) << 16);
     if (fabsf(miss) > most) {
       most = fabsf(miss);
       best = make_int2(id, __float_as_int(miss));
     }
   }
-  if constexpr (sizeof(IO) == 2) {
-    // the entry that lost most, of equal ones the one with the lowest id
-    auto better = [](int2 p, int2 q) __attribute__((always_inline)) {
-      const float x = fabsf(__int_as_float(p.y)), y = fabsf(__int_as_float(q.y));
-      return x > y || (x == y && p.x < q.x);
-    };
+  auto better = [](int2 p, int2 q) __attribute__((always_inline)) {
+    const float x = fabsf(__int_as_float(p.y)), y = fabsf(__int_as_float(q.y));
+    return x > y || (x == y && p.x < q.x);
+  };
+  s = wave_sum(s);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const int2 q = make_int2(__shfl_xor(best.x, o, 64), __shfl_xor(best.y, o, 64));
-      if (better(q, best)) best = q;
+  for (int o = 32; o > 0; o >>= 1) {
+    const int2 q = make_int2(__shfl_xor(best.x, o, 64), __shfl_xor(best.y, o, 64));
+    if (better(q, best)) best = q;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    meet[threadIdx.x >> 6] = s;
+    lost[threadIdx.x >> 6] = best;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  s = (meet[0] + meet[1]) + (meet[2] + meet[3]);
+  a.loss[row] = a.tau2 * (share != nullptr ? s + a.known[row] : s);
+  a.lse[row] = all.from + log_sum;
+  if (!grad) return;
+  a.sums[i] = make_float2(all.from, by);
+  if (!bf16) return;
+  for (int w = 1; w < 4; ++w)
+    if (better(lost[w], best)) best = lost[w];
+  a.fix[i] = best;
+}
+
+// dz of 32 rows of a piece in `panels` panels: a panel's 32 rows are one stretch of
+// memory.  Rows behind the last one that counts, up to the next 64, and columns
+// behind the vocabulary are 0.
+template <typename IO>
+__global__ __launch_bounds__(256) void dz_kernel(LossArgs a, int first, int panels, int tile_shift) {
+  const int rows = min(a.piece, *a.live - first), i0 = blockIdx.x * 32, i = i0 + (threadIdx.x >> 3);
+  if (i0 >= (rows + 63) / 64 * 64) return;
+  const int p0 = blockIdx.y * panels, p1 = min(p0 + panels, static_cast<int>(a.vpad / 64));
+  const bool on = i < rows;
+  const float2 sum = on ? a.sums[i] : make_float2(0.0f, 0.0f);
+  const float2* st = a.stats + static_cast<int64_t>(i) * a.tiles;
+  const int64_t plane = static_cast<int64_t>(a.piece) * a.vpad;
+  const int c = (threadIdx.x & 7) * 8;
+#pragma unroll 2
+  for (int p = p0; p < p1; ++p) {
+    const int64_t at = (static_cast<int64_t>(p) * a.piece + i) * 64 + c;
+    const int v = p * 64 + c;
+    float q[8];
+    if constexpr (sizeof(IO) == 2) {
+      const uint4 raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.probs) + at);
+      const uint32_t code[4] = {raw.x, raw.y, raw.z, raw.w};
+      const float top = (on ? st[p * 64 >> tile_shift].x : 0.0f) - sum.x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t c16 = e & 1 ? code[e / 2] >> 16 : code[e / 2] & 0xffff;
+        const float z = fmaf(static_cast<float>(c16), -1.0f / kCodeSteps, top);
+        q[e] = c16 != 65535 ? fast_exp2(z * kLog2e) : 0.0f;
+      }
+    } else {
+      const float* z = static_cast<const float*>(a.probs) + at;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = expf(z[e] - sum.x);
     }
-    if ((threadIdx.x & 63) == 0) lost[threadIdx.x >> 6] = best;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < 4; ++w)
-        if (better(lost[w], best)) best = lost[w];
-      a.fix[i * a.fixes + blockIdx.y] = best;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = on && v + e < a.vocab ? q[e] * sum.y : 0.0f;
+    to_planes(q, a.dz + at, plane, sizeof(IO) == 2 ? 1 : 3);
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < min(32, rows - i0) * a.entries; k += 256) {
+    const int r = i0 + k / a.entries, e = k % a.entries;
+    const int id = a.near[static_cast<int64_t>(first + r) * a.entries + e];
+    if (id < p0 * 64 || id >= p1 * 64) continue;
+    uint16_t* z = a.dz + (static_cast<int64_t>(id / 64) * a.piece + r) * 64 + id % 64;
+    float v = a.value[static_cast<int64_t>(r) * a.entries + e];
+    for (int n = 0; n < (sizeof(IO) == 2 ? 1 : 3); ++n) {
+      const uint16_t b = bf16_bits(v);
+      z[n * plane] = b;
+      v -= __uint_as_float(static_cast<uint32_t>(b) << 16);
     }
   }
 }
@@ -296,17 +332,29 @@ __global__ __launch_bounds__(256) void dx_kernel(LossArgs a, int first) {
   const int row = blockIdx.x, j = a.place[row];
   if (j < 0 ? first != 0 : j < first || j >= first + a.piece) return;
   const int splits = dx_splits(a, dx_tiles(a, min(a.piece, *a.live - first)));
-  for (int c = threadIdx.x; c < a.dim; c += 256) {
-    float s = 0.0f;
-    if (j >= 0)
-      for (int q = 0; q < splits; ++q)
-        s += a.part[(static_cast<int64_t>(q) * a.piece + (j - first)) * a.dpad + c];
-    if (sizeof(IO) == 2 && j >= 0)
-      for (int q = 0; q < a.fixes; ++q) {
-        const int2 f = a.fix[(j - first) * a.fixes + q];
-        if (f.x >= 0) s = fmaf(__int_as_float(f.y), io_traits<IO>::load(static_cast<const IO*>(a.weight) + f.x * a.sw + c), s);
+  IO* out = static_cast<IO*>(a.dx) + row * a.sdx;
+  const float* part = a.part + static_cast<int64_t>(j < 0 ? 0 : j - first) * a.dpad;
+  const int64_t next = static_cast<int64_t>(a.piece) * a.dpad;
+  for (int c = threadIdx.x * 4; c < a.dim; c += 1024) {
+    float s[4] = {};
+    if (j >= 0) {
+#pragma unroll 4
+      for (int q = 0; q < splits; ++q) {
+        const float4 v = *reinterpret_cast<const float4*>(part + q * next + c);  // (rows are padded)
+        s[0] += v.x;
+        s[1] += v.y;
+        s[2] += v.z;
+        s[3] += v.w;
       }
-    io_traits<IO>::store(static_cast<IO*>(a.dx) + row * a.sdx + c, s);
+      const int2 f = sizeof(IO) == 2 ? a.fix[j - first] : make_int2(-1, 0);
+      if (f.x >= 0) {
+        float w[4];
+        load_part<IO, 4>(static_cast<const IO*>(a.weight) + f.x * a.sw + c, a.dim - c, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = fmaf(__int_as_float(f.y), w[e], s[e]);
+      }
+    }
+    store_part<IO, 4>(out + c, a.dim - c, s);
   }
 }
 
@@ -324,8 +372,6 @@ __global__ __launch_bounds__(256) void scale_kernel(const IO* in, const float* f
     io_traits<IO>::store(out + i, io_traits<IO>::load(in + i) * f);
 }
 
-int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
-
 template <typename IO>
 hipError_t launch_io(const LossArgs& a, hipStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.rows);
@@ -337,15 +383,20 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
     return a.dweight != nullptr ? launch_dw(a, 0, sizeof(IO) == 2, s) : hipGetLastError();
   }
   const int shift = loss_vocab_tile(a.small) == 64 ? 6 : 7;
-  pack_kernel<IO><<<rows, 256, 0, s>>>(a, shift);
-  if (a.pack_w) pack_weight_kernel<IO><<<static_cast<unsigned>(a.vocab), 256, 0, s>>>(a);
+  pack_kernel<IO><<<static_cast<unsigned>(a.xrows), 256, 0, s>>>(a, shift);
+  if (a.pack_w) pack_weight_kernel<IO><<<static_cast<unsigned>(a.vocab + 7) / 8, 256, 0, s>>>(a);
   for (int p = 0; p < a.pieces; ++p) {
     const int first = p * a.piece;
     const unsigned n = static_cast<unsigned>(std::min(a.piece, a.rows - first));
     hipError_t e = launch_logits(a, first, sizeof(IO) == 2, grad, s);
     if (e != hipSuccess) return e;
-    const int64_t cols = grad ? up256((a.vpad + a.fixes - 1) / a.fixes) : a.vpad;
-    softmax_kernel<IO><<<dim3(n, grad ? a.fixes : 1), 256, 0, s>>>(a, first, grad, static_cast<int>(cols), shift);
+    row_kernel<<<n, 256, 0, s>>>(a, first, sizeof(IO) == 2, grad);
+    if (grad) {
+      // panels a workgroup: so many that there are 2048 workgroups, up to 32
+      const unsigned groups = (n + 63) / 64 * 2, all = static_cast<unsigned>(a.vpad / 64);
+      const unsigned panels = std::clamp(all * groups / 2048, 1u, 32u);
+      dz_kernel<IO><<<dim3(groups, (all + panels - 1) / panels), 256, 0, s>>>(a, first, static_cast<int>(panels), shift);
+    }
     if (a.dx != nullptr) {
       if ((e = launch_dx(a, first, s)) != hipSuccess) return e;
       dx_kernel<IO><<<rows, 256, 0, s>>>(a, first);

@@ -140,10 +140,10 @@ def test_workspace_sizes():
     assert size("loss", dx=0, dweight=0)[0] < n < size("loss", io_dtype=0)[0]
     # an unaligned matrix is copied
     assert size("loss", weight=fake(1) + 2)[0] >= n + 1000 * 256 * 2
-    # the probabilities of all rows are never there: a piece of them takes 1 GiB
+    # the probabilities of all rows are never there: a piece of them takes 2 GiB
     big = dict(dim=1024, vocab=65536, x_stride=1024, weight_stride=1024, dx_stride=1024, dweight_stride=1024)
-    few, many = size("loss", rows=16384, **big)[0], size("loss", rows=262144, **big)[0]
-    assert many - few < (262144 - 16384) * (1024 * 2 + 200) + (1 << 29)
+    few, many = size("loss", rows=32768, **big)[0], size("loss", rows=262144, **big)[0]
+    assert many - few < (262144 - 32768) * (1024 * 2 + 200) + (1 << 30)
 
 
 # ---------------------------------------------------------------- the binding

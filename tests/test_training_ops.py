@@ -437,14 +437,14 @@ def test_losses_of_no_rows(dtype):
 
 @gpu
 def test_rows_in_pieces():
-    """More rows than one piece of dz holds: 2^30 bytes over 2 * 65536 a row are
-    8192 rows, so 9000 take two; against one piece of each half."""
+    """More rows than one piece of dz holds: 2^31 bytes over a little more than
+    2 * 65536 a row are 16000 rows, so 17000 take two; against one piece of each half."""
     note("cross entropy in two pieces")
     g = gen(11)
-    x, w, ids = loss_case(9000, 64, 65536, BF16, ignored=0.05)
-    rw = (torch.rand(9000, generator=g) / 9000).to(DEV)
+    x, w, ids = loss_case(17000, 64, 65536, BF16, ignored=0.05)
+    rw = (torch.rand(17000, generator=g) / 17000).to(DEV)
     loss, lse, dx, dw = mss.linear_cross_entropy_grad(x, w, ids, rw)
-    halves = [mss.linear_cross_entropy_grad(x[s], w, ids[s], rw[s]) for s in (slice(0, 4500), slice(4500, 9000))]
+    halves = [mss.linear_cross_entropy_grad(x[s], w, ids[s], rw[s]) for s in (slice(0, 8500), slice(8500, 17000))]
     assert torch.equal(loss, torch.cat([h[0] for h in halves]))
     assert torch.equal(lse, torch.cat([h[1] for h in halves]))
     # the same sums of the same bf16 values in another order and grouping
