@@ -78,8 +78,8 @@ struct LossArgs {
   int where_words;
   float* picked;   // [rows][entries] their logits
   // Rows, weights and dz as bf16 operands of the products: one plane, or three
-  // whose sum is the fp32 value.  They lie in panels 64 columns wide, [columns / 64]
-  // [rows][64], so that a tile's part of any of them is one stretch of memory.
+  // whose sum is the fp32 value.  They lie in panels, [columns / 64][rows][64] (dz:
+  // 32), so that a tile's part of any of them is one stretch of memory.
   int planes;
   int64_t dpad;    // columns of x and weight, a multiple of 64
   uint16_t* xp;    // [planes][dpad / 64][xrows][64]
@@ -94,8 +94,8 @@ struct LossArgs {
   int64_t vpad;    // columns of dz, a multiple of 64
   float2* stats;   // [piece][tiles] an integer R and the sum of e^(z - R)
   float2* sums;    // [piece] `from` and c / sum, the row's sum of e^z being sum e^from
-  void* probs;     // [vpad / 64][piece][64] codes of the logits (bf16), or the logits (fp32)
-  uint16_t* dz;    // [planes][vpad / 64][piece][64] (bf16: probs itself)
+  void* probs;     // [vpad / 32][piece][32] codes of the logits (bf16), or the logits (fp32)
+  uint16_t* dz;    // [planes][vpad / 32][piece][32] (bf16: probs itself)
   float* value;    // [piece][entries] dz of the entries
   int2* fix;       // [piece] (bf16) id and what its dz lost by its rounding, as float bits; or id -1
   float* part;     // [splits][piece][dpad]

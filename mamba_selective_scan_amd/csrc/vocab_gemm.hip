@@ -28,14 +28,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #define MSS_LDS __attribute__((address_space(3)))
-
-constexpr int kStep = 64;  // of the summed axis
 
 // One operand of a tile, in bytes: rows of the tile's axis from `base` on, or rows
 // of the summed one with the tile's axis contiguous.  A row is `stride` behind the
-// one before it, its columns 64 .. 127 are `panel` behind its columns 0 .. 63.
-// `span` from base on may be read (of a plane).
+// one before it, columns W .. 2 W - 1 are `panel` behind columns 0 .. W - 1.
+// `span` from base on may be read (of a plane).  W columns a panel.
+template <int W>
 struct Side {
   const char* base;
   int64_t plane, span, panel;
@@ -47,23 +48,25 @@ __device__ inline int plane_of(int pair, bool second) {
   return (second ? 0x184 : 0x910) >> (2 * pair) & 3;
 }
 
-// How ROWS rows (KC: of the tile's axis, 64 wide; else 64 rows of the summed axis,
-// ROWS wide) of one operand lie in LDS, are loaded by NT threads, and are read as
-// the fragments of 32 x 32 x 16 products.
-template <bool KC, int ROWS, int NT>
+// How ROWS rows (KC: of the tile's axis, STEP wide; else STEP rows of the summed
+// axis, ROWS wide) of one operand lie in LDS, are loaded by NT threads from panels
+// of W columns, and are read as the fragments of 32 x 32 x 16 products.  TAIL: the
+// summed axis may end in a row (KC), at a multiple of 8.
+template <bool KC, int ROWS, int STEP, int W, bool TAIL, int NT>
 struct Panel {
-  static constexpr int kBytes = ROWS * kStep * 2;
+  static constexpr int kBytes = ROWS * STEP * 2;
   static constexpr int kLoads = kBytes / 16 / NT;
-  static constexpr int kVecs = KC ? 8 : ROWS / 8;  // 16-byte vectors of a row
-  static_assert(kBytes % (16 * NT) == 0 && NT % kVecs == 0, "whole loads");
+  static constexpr int kVecs = KC ? STEP / 8 : ROWS / 8;  // 16-byte vectors of a row
+  static_assert(kBytes % (16 * NT) == 0 && NT % kVecs == 0 && (!KC || W == STEP), "whole loads");
 
   // The vector in which vector c of row r lies.  KC: sixteen rows side by side are
-  // read at one vector each, two rows to the width of all banks, so every two
-  // spread over the eight.  Otherwise rows r ..
-  // r + 3 and r + 8 .. r + 11 are read at 64 bytes each: they spread over the
-  // 64-byte parts of a row as far as there are any.
+  // read at one vector each, so the rows that share the width of all banks (256
+  // bytes) spread over a row's vectors.  Otherwise rows r .. r + 3 and r + 8 ..
+  // r + 11 are read at 64 bytes each: they spread over the 64-byte parts of a row
+  // as far as there are any.
   __device__ static inline int swizzle(int r, int c) {
-    if constexpr (KC) return c ^ (r >> 1 & 7);
+    if constexpr (KC && STEP == 64) return c ^ (r >> 1 & 7);
+    if constexpr (KC) return c ^ (r >> 2 & 3);
     if constexpr (kVecs >= 32) return c ^ (((r & 3) | (r >> 1 & 4)) << 2);
     if constexpr (kVecs == 16) return c ^ ((r & 3) << 2);
     return c ^ ((r >> 1 & 1) << 2);
@@ -77,29 +80,42 @@ struct Panel {
     return swizzle(first_row() + i * kApart, static_cast<int>(threadIdx.x) % kVecs);
   }
 
-  // One step's loads, from summed index k on (none if it is past the end: they
-  // read 0).  `dim`: where the summed axis ends in a row (KC), a multiple of 8.
-  struct Loads {
-    __amdgpu_buffer_rsrc_t rsrc;
+  // Where the loads are: the steps of one pair of planes after those of another.
+  struct Feed {
+    const char* at;
+    int64_t left, step;  // bytes that may be read, and to the next step
     uint32_t off, odd, next;
-    char MSS_LDS* lds;
-    __device__ inline Loads(const Side& s, int64_t at, int k, int dim, bool any, char MSS_LDS* stage) {
-      const int64_t from = KC ? k / kStep * s.panel : static_cast<int64_t>(k) * s.stride;
-      const int64_t left = any ? s.span - from : 0;
-      const int range = static_cast<int>(left < 0 ? 0 : left < kRsrcRange ? left : kRsrcRange);
-      rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(s.base) + at + from, 0, range, kRsrcFlags);
+    int k;
+    __device__ inline Feed(const Side<W>& s) {
       const uint32_t row = static_cast<uint32_t>(first_row() * s.stride), panel = static_cast<uint32_t>(s.panel);
-      off = row + column(0) / 8 * panel + column(0) % 8 * 16;
-      odd = row + column(1) / 8 * panel + column(1) % 8 * 16;
+      constexpr int v = W / 8;
+      off = row + column(0) / v * panel + column(0) % v * 16;
+      odd = row + column(1) / v * panel + column(1) % v * 16;
       next = static_cast<uint32_t>(kApart * s.stride);
-      if (KC && k + column(0) * 8 >= dim) {
-        off = odd = kOffNone;
-        next = 0;
-      }
-      lds = stage + uniform(static_cast<int>(threadIdx.x) >> 6) * 1024;
+      step = KC ? s.panel : static_cast<int64_t>(STEP) * s.stride;
     }
-    __device__ inline void issue(int i) const {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MSS_LDS void*)(lds + i * NT * 16), 16, (i & 1 ? odd : off) + i * next, 0, 0, 0);
+    __device__ inline void start(const Side<W>& s, int plane, int k0) {
+      const int64_t from = k0 / STEP * step;
+      at = s.base + plane * s.plane + from;
+      left = s.span - from;
+      k = k0;
+    }
+    __device__ inline void advance() {
+      at += step;
+      left -= step;
+      k += STEP;
+    }
+    // One step's loads; a lane past the range reads 0.
+    __device__ inline void issue(int dim, char MSS_LDS* stage) const {
+      const int range = static_cast<int>(left < 0 ? 0 : left < kRsrcRange ? left : kRsrcRange);
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, range, kRsrcFlags);
+      char MSS_LDS* lds = stage + uniform(static_cast<int>(threadIdx.x) >> 6) * 1024;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        uint32_t o = (i & 1 ? odd : off) + i * next;
+        if (TAIL && k + column(0) * 8 >= dim) o = kOffNone;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MSS_LDS void*)(lds + i * NT * 16), 16, o, 0, 0, 0);
+      }
     }
   };
 
@@ -109,9 +125,9 @@ struct Panel {
   __device__ static inline void fragments(const char MSS_LDS* lds, int row, int ks, bf16x8 (&f)[N]) {
     const int lane = static_cast<int>(threadIdx.x) & 63;
     if constexpr (KC) {
-      const char MSS_LDS* p = lds + (row + (lane & 31)) * 128 + swizzle(lane, 2 * ks + (lane >> 5)) * 16;
+      const char MSS_LDS* p = lds + (row + (lane & 31)) * (STEP * 2) + swizzle(lane, 2 * ks + (lane >> 5)) * 16;
 #pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = *reinterpret_cast<const bf16x8 MSS_LDS*>(p + i * 32 * 128);
+      for (int i = 0; i < N; ++i) f[i] = *reinterpret_cast<const bf16x8 MSS_LDS*>(p + i * 32 * STEP * 2);
     } else {
       // a group of 16 lanes reads 4 rows of 32 bytes and turns them about
       const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);
@@ -127,13 +143,17 @@ struct Panel {
   }
 };
 
-// A tile of WM x WN waves, each with IM x IN products of 32 x 32.
-template <bool KCA, bool KCB, int WM, int WN, int IM, int IN>
+// A tile of WM x WN waves, each with IM x IN products of 32 x 32: A is KC or not
+// and in panels of PA columns, B likewise, STEP of the summed axis a stage, RING
+// stages.
+template <bool KCA, int PA, bool TAIL, bool KCB, int PB, int WM, int WN, int IM, int IN, int STEP, int RING>
 struct Tile {
-  static constexpr int kThreads = 64 * WM * WN, kM = 32 * WM * IM, kN = 32 * WN * IN;
-  typedef Panel<KCA, kM, kThreads> A;
-  typedef Panel<KCB, kN, kThreads> B;
-  static constexpr int kStage = A::kBytes + B::kBytes;
+  static constexpr int kThreads = 64 * WM * WN, kM = 32 * WM * IM, kN = 32 * WN * IN, kStep = STEP;
+  typedef Panel<KCA, kM, STEP, PA, TAIL, kThreads> A;
+  typedef Panel<KCB, kN, STEP, PB, false, kThreads> B;
+  typedef f32x16 Acc[IM][IN];
+  static constexpr int kIM = IM, kIN = IN;
+  static constexpr int kStage = A::kBytes + B::kBytes, kLds = RING * kStage;
 
   __device__ static inline int wave_m() { return uniform(static_cast<int>(threadIdx.x) >> 6) / WN * (32 * IM); }
   __device__ static inline int wave_n() { return uniform(static_cast<int>(threadIdx.x) >> 6) % WN * (32 * IN); }
@@ -144,18 +164,18 @@ struct Tile {
       A::fragments(stage, wave_m(), ks, a);
       B::fragments(stage + A::kBytes, wave_n(), ks, b);
     }
-    __device__ inline void multiply(f32x16 (&acc)[IM][IN]) const {
+    __device__ inline void multiply(Acc& acc) const {
 #pragma unroll
-      for (int i = 0; i < IM; ++i)
+      for (int j = 0; j < IN; ++j)
 #pragma unroll
-        for (int j = 0; j < IN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < IM; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
     }
   };
 
   // What one stage adds.
-  __device__ static inline void multiply(const char MSS_LDS* stage, f32x16 (&acc)[IM][IN]) {
+  __device__ static inline void multiply(const char MSS_LDS* stage, Acc& acc) {
 #pragma unroll
-    for (int ks = 0; ks < kStep / 16; ++ks) {
+    for (int ks = 0; ks < STEP / 16; ++ks) {
       Frags f;
       f.read(stage, ks);
       f.multiply(acc);
@@ -164,72 +184,77 @@ struct Tile {
 
   // The sum over summed indices [k0, k1) (k0 a multiple of 64) of all pairs of planes.
   // While a part's products run, the next part's fragments are read.  At a step's
-  // last part they come from the other stage, whose loads had a step's time to
-  // land; then every wave has read this stage, and the loads of the step after the
-  // next go there.
-  __device__ static inline void run(const Side& a, const Side& b, int k0, int k1, int dim, int pairs, char MSS_LDS* lds,
-                                    f32x16 (&acc)[IM][IN]) {
-    const int total = (k1 - k0 + kStep - 1) / kStep * pairs;
+  // last part they come from the next stage, whose loads had all but one of the
+  // ring's steps to land; then every wave has read this stage, and the loads of the
+  // step a ring on go there.
+  __device__ static inline void run(const Side<PA>& a, const Side<PB>& b, int k0, int k1, int dim, int pairs,
+                                    char MSS_LDS* lds, Acc& acc) {
+    const int steps = (k1 - k0 + STEP - 1) / STEP, total = steps * pairs;
     if (total <= 0) return;
-    int pair = 0, k = k0, asked = 0;
-    auto advance = [&]() __attribute__((always_inline)) {
-      ++asked;
-      k += kStep;
-      if (k >= k1) {
-        k = k0;
-        ++pair;
+    typename A::Feed fa(a);
+    typename B::Feed fb(b);
+    int pair = 0, togo = steps;
+    fa.start(a, 0, k0);
+    fb.start(b, 0, k0);
+    auto load = [&](char MSS_LDS* stage) __attribute__((always_inline)) {
+      fa.issue(dim, stage);
+      fb.issue(dim, stage + A::kBytes);
+      fa.advance();
+      fb.advance();
+      if (--togo == 0) {
+        if (++pair < pairs) {
+          fa.start(a, plane_of(pair, false), k0);
+          fb.start(b, plane_of(pair, true), k0);
+        } else {  // nothing is left: loads of 0
+          fa.left = fb.left = fa.step = fb.step = 0;
+        }
+        togo = steps;
       }
     };
-    auto load = [&](char MSS_LDS* stage) __attribute__((always_inline)) {
-      const typename A::Loads la(a, plane_of(pair, false) * a.plane, k, dim, asked < total, stage);
-      const typename B::Loads lb(b, plane_of(pair, true) * b.plane, k, dim, asked < total, stage + A::kBytes);
+    constexpr int kLoads = A::kLoads + B::kLoads, kReads = IM * A::kReads + IN * B::kReads, kProducts = IM * IN;
 #pragma unroll
-      for (int i = 0; i < A::kLoads; ++i) la.issue(i);
-#pragma unroll
-      for (int i = 0; i < B::kLoads; ++i) lb.issue(i);
-      advance();
-    };
-    constexpr int kLoads = A::kLoads + B::kLoads, kReads = IM * A::kReads + IN * B::kReads;
-    load(lds);
-    load(lds + kStage);
-    wait_loads<kLoads>();
-    __syncthreads();
+    for (int r = 0; r < RING; ++r) load(lds + r * kStage);
+    meet<(RING - 1) * kLoads>();
     Frags now, next;
     now.read(lds, 0);
-    for (int s = 0; s < total; s += 2) {
+    for (int s = 0; s < total; s += RING) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half == 1 && s + 1 >= total) break;
-        char MSS_LDS* here = lds + half * kStage;
-        char MSS_LDS* there = lds + (1 - half) * kStage;
+      for (int r = 0; r < RING; ++r) {
+        if (r > 0 && s + r >= total) break;
+        char MSS_LDS* here = lds + r * kStage;
+        const char MSS_LDS* there = lds + (r + 1) % RING * kStage;
 #pragma unroll
-        for (int ks = 0; ks < kStep / 16; ++ks) {
-          if (ks < kStep / 16 - 1) {
+        for (int ks = 0; ks < STEP / 16; ++ks) {
+          const bool last = ks == STEP / 16 - 1;
+          if (!last) {
             next.read(here, ks + 1);
           } else {
-            wait_loads<0>();
-            __syncthreads();
+            meet<(RING - 2) * kLoads>();
             next.read(there, 0);
             load(here);
           }
           now.multiply(acc);
 #pragma unroll
-          for (int m = 0; m < IM * IN; ++m) {
+          for (int m = 0; m < kProducts; ++m) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product,
-            __builtin_amdgcn_sched_group_barrier(0x100, (kReads + IM * IN - 1) / (IM * IN), 0);  // LDS reads
-            if (ks == kStep / 16 - 1) __builtin_amdgcn_sched_group_barrier(0x010, (kLoads + IM * IN - 1) / (IM * IN), 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kProducts - 1) / kProducts, 0);  // LDS reads
+            if (last) __builtin_amdgcn_sched_group_barrier(0x010, (kLoads + kProducts - 1) / kProducts, 0);
           }
           now = next;
         }
       }
     }
-    wait_loads<0>();
-    __syncthreads();  // (the stages are free)
+    meet<0>();  // (the stages are free)
   }
+  // All but the last N loads of every wave have landed, and its LDS reads have.
+  // (A barrier with a fence would wait for all loads.)
   template <int N>
-  __device__ static inline void wait_loads() {
+  __device__ static inline void meet() {
     static_assert(N < 64, "a six-bit count");
-    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);  // vmcnt(N)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);  // vmcnt(N) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   }
 };
 
@@ -247,11 +272,11 @@ __device__ inline int acc_row(int e) { return 8 * (e >> 2) + 4 * (static_cast<in
 __device__ inline int live_rows(const LossArgs& a, int first) { return max(min(a.piece, *a.live - first), 0); }
 
 // The operands.
-__device__ inline Side x_side(const LossArgs& a, int row, int d) {
+__device__ inline Side<64> x_side(const LossArgs& a, int row, int d) {
   const int64_t panel = a.xrows * 128, from = d / 64 * panel + static_cast<int64_t>(row) * 128;
   return {reinterpret_cast<const char*>(a.xp) + from, a.xrows * a.dpad * 2, a.xrows * a.dpad * 2 - from, panel, 128};
 }
-__device__ inline Side w_side(const LossArgs& a, int v, int d) {
+__device__ inline Side<64> w_side(const LossArgs& a, int v, int d) {
   if (a.pack_w) {
     const int64_t panel = static_cast<int64_t>(a.vocab) * 128, from = d / 64 * panel + static_cast<int64_t>(v) * 128;
     return {reinterpret_cast<const char*>(a.wp) + from, a.vocab * a.dpad * 2, a.vocab * a.dpad * 2 - from, panel, 128};
@@ -260,9 +285,10 @@ __device__ inline Side w_side(const LossArgs& a, int v, int d) {
   return {reinterpret_cast<const char*>(a.wp) + from, 0, ((a.vocab - 1) * a.sw + a.dim) * 2 - from, 128,
           static_cast<int>(a.sw * 2)};
 }
-__device__ inline Side z_side(const LossArgs& a, int row, int v) {
-  const int64_t panel = static_cast<int64_t>(a.piece) * 128, from = v / 64 * panel + static_cast<int64_t>(row) * 128;
-  return {reinterpret_cast<const char*>(a.dz) + from, a.piece * a.vpad * 2, a.piece * a.vpad * 2 - from, panel, 128};
+__device__ inline Side<kZPanel> z_side(const LossArgs& a, int row, int v) {
+  constexpr int kRow = kZPanel * 2;
+  const int64_t panel = static_cast<int64_t>(a.piece) * kRow, from = v / kZPanel * panel + static_cast<int64_t>(row) * kRow;
+  return {reinterpret_cast<const char*>(a.dz) + from, a.piece * a.vpad * 2, a.piece * a.vpad * 2 - from, panel, kRow};
 }
 // Where the summed axis of logits ends in the rows of weights.
 __device__ inline int w_cols(const LossArgs& a) { return a.pack_w ? static_cast<int>(a.dpad) : a.dim; }
@@ -287,15 +313,16 @@ unsigned tile_blocks(int64_t mt, int64_t nt) { return static_cast<unsigned>((mt 
 // ---------------------------------------------------------------- logits
 
 // Tiles of vocabulary x rows: a lane holds one row's values at 16 IM IN entries.
-template <bool BF16, typename T, int IM, int IN>
+template <bool BF16, typename T>
 __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int first, bool keep) {
-  __shared__ __attribute__((aligned(256))) char lds[2 * T::kStage];
-  static_assert(2 * T::kStage >= T::kThreads / 64 * IM * 32 * 32 * 4, "room for the waves' logits");
+  __shared__ __attribute__((aligned(256))) char lds[T::kLds];
+  constexpr int IM = T::kIM, IN = T::kIN;
+  static_assert(T::kLds >= T::kThreads / 64 * IM * 32 * 32 * 4, "room for the waves' logits");
   const int rows = live_rows(a, first), lane = threadIdx.x & 63;
   const At at = tile_at(blockIdx.x, (a.vocab + T::kM - 1) / T::kM, (rows + T::kN - 1) / T::kN);
   if (at.m < 0) return;
   const int v0 = at.m * T::kM, i0 = at.n * T::kN;
-  f32x16 acc[IM][IN];
+  typename T::Acc acc;
   clear(acc);
   char MSS_LDS* sh = (char MSS_LDS*)lds;
   T::run(w_side(a, v0, 0), x_side(a, first + i0, 0), 0, a.dim, w_cols(a), a.planes == 1 ? 1 : 6, sh, acc);
@@ -304,7 +331,18 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
   const int wv = v0 + T::wave_m(), wi = i0 + T::wave_n();
   if (wv >= a.vocab) return;
   const int tile = wv / kWide;
-  float MSS_LDS* mine = reinterpret_cast<float MSS_LDS*>(sh + uniform(static_cast<int>(threadIdx.x) >> 6) * (kWide * 32 * 4));
+  char MSS_LDS* mine = sh + uniform(static_cast<int>(threadIdx.x) >> 6) * (kWide * 32 * 4);
+  float scale = a.scale;
+  if (wv + kWide > a.vocab || scale < 0.0f) {  // (from here on the scale only has to keep the order)
+#pragma unroll
+    for (int m = 0; m < IM; ++m)
+#pragma unroll
+      for (int j = 0; j < IN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[m][j][e] = wv + 32 * m + acc_row(e) < a.vocab ? acc[m][j][e] * scale : -INFINITY;
+    scale = 1.0f;
+  }
 #pragma unroll
   for (int j = 0; j < IN; ++j) {
     const int i = wi + 32 * j + (lane & 31);
@@ -312,94 +350,116 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
 #pragma unroll
     for (int m = 0; m < IM; ++m)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float z = acc[m][j][e] * a.scale;
-        if (wv + 32 * m + acc_row(e) >= a.vocab) z = -INFINITY;
-        acc[m][j][e] = z;
-        top = fmaxf(top, z);
-      }
-    top = ceilf(fmaxf(top, __shfl_xor(top, 32, 64)));
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[m][j][e]);
+    top = ceilf(fmaxf(top, __shfl_xor(top, 32, 64)) * scale);
     const float from = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-    for (int m = 0; m < IM; ++m)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sum += fast_exp2((acc[m][j][e] - from) * kLog2e);
-    sum += __shfl_xor(sum, 32, 64);
-    if (i < rows && lane < 32) a.stats[static_cast<int64_t>(i) * a.tiles + tile] = make_float2(top, sum);
     // The rows' logits in LDS, [32 rows][kWide] with the 16-byte vectors of a row
     // turned by the row; this wave's own.
+    auto spread = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int m = 0; m < IM; ++m)
+      for (int m = 0; m < IM; ++m)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = 8 * m + 2 * q + (lane >> 5), r = lane & 31;
-        *reinterpret_cast<f32x4 MSS_LDS*>(mine + r * kWide + (c ^ (r & (kWide / 4 - 1))) * 4) =
-            f32x4{acc[m][j][4 * q], acc[m][j][4 * q + 1], acc[m][j][4 * q + 2], acc[m][j][4 * q + 3]};
-      }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int q = 0; q < 4; ++q) {
+          const int c = 8 * m + 2 * q + (lane >> 5), r = lane & 31;
+          f32x4 z;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = acc[m][j][4 * q + e] * scale;
+          *reinterpret_cast<f32x4 MSS_LDS*>(mine + (r * (kWide / 4) + (c ^ (r & (kWide / 4 - 1)))) * 16) = z;
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    if (!BF16 && keep) spread();
     // entries of these rows among this wave's
     bool hit = false;
     if (i < rows && lane < 32)
       hit = a.where[static_cast<int64_t>(first + i) * a.where_words + (tile >> 5)] >> (tile & 31) & 1;
     uint64_t hits = __ballot(hit);
-    while (hits != 0) {
-      const int r = __builtin_ctzll(hits);
-      hits &= hits - 1;
-      const int64_t k0 = static_cast<int64_t>(first + wi + 32 * j + r) * a.entries;
-      for (int k = lane; k < a.entries; k += 64) {
-        const int v = a.near[k0 + k] - wv;
-        if (v >= 0 && v < kWide) a.picked[k0 + k] = mine[r * kWide + ((v >> 2) ^ (r & (kWide / 4 - 1))) * 4 + (v & 3)];
-      }
-    }
-    if (keep) {
-      // 8 entries a lane, 8 rows of a panel one behind another
-#pragma unroll
-      for (int q = 0; q < kWide / 64 * 4; ++q) {
-        const int r = q % 4 * 8 + (lane >> 3), c = q / 4 * 8 + (lane & 7), turn = r & (kWide / 4 - 1);
-        const f32x4 lo = *reinterpret_cast<const f32x4 MSS_LDS*>(mine + r * kWide + ((2 * c) ^ turn) * 4);
-        const f32x4 hi = *reinterpret_cast<const f32x4 MSS_LDS*>(mine + r * kWide + ((2 * c + 1) ^ turn) * 4);
-        const float t = __shfl(top, r, 64);
-        if (wi + 32 * j + r >= rows || wv + q / 4 * 64 >= a.vocab) continue;
-        const int64_t o = (static_cast<int64_t>(wv / 64 + q / 4) * a.piece + wi + 32 * j + r) * 64 + (lane & 7) * 8;
-        if constexpr (BF16) {
-          uint32_t code[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            code[e] = static_cast<uint32_t>(fminf(rintf((t - (e < 4 ? lo[e & 3] : hi[e & 3])) * kCodeSteps), 65535.0f));
-          uint4 p;
-          p.x = code[0] | code[1] << 16;
-          p.y = code[2] | code[3] << 16;
-          p.z = code[4] | code[5] << 16;
-          p.w = code[6] | code[7] << 16;
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.probs) + o) = p;
-        } else {
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.probs) + o) = lo;
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.probs) + o + 4) = hi;
+    if (hits != 0) {
+      if (BF16 || !keep) spread();
+      do {
+        const int r = __builtin_ctzll(hits);
+        hits &= hits - 1;
+        const int64_t k0 = static_cast<int64_t>(first + wi + 32 * j + r) * a.entries;
+        for (int k = lane; k < a.entries; k += 64) {
+          const int v = a.near[k0 + k] - wv;
+          if (v >= 0 && v < kWide)
+            a.picked[k0 + k] = *reinterpret_cast<const float MSS_LDS*>(
+                mine + (r * (kWide / 4) + ((v >> 2) ^ (r & (kWide / 4 - 1)))) * 16 + (v & 3) * 4);
         }
-      }
+      } while (hits != 0);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (!BF16 && keep) {
+      // 4 entries a lane, 8 rows of a panel one behind another
+#pragma unroll
+      for (int q = 0; q < kWide / 32 * 4; ++q) {
+        const int r = q % 4 * 8 + (lane >> 3), c = q / 4 * 8 + (lane & 7);
+        const f32x4 z = *reinterpret_cast<const f32x4 MSS_LDS*>(mine + (r * (kWide / 4) + (c ^ (r & (kWide / 4 - 1)))) * 16);
+        if (wi + 32 * j + r < rows && wv + c * 4 < a.vpad)
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.probs) + z_index(a, wi + 32 * j + r, wv + c * 4)) = z;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    // distances from the ceiling, in place, and the sum
+#pragma unroll
+    for (int m = 0; m < IM; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float d = fmaf(acc[m][j][e], scale, -from);
+        acc[m][j][e] = d;
+        sum += fast_exp2(d * kLog2e);
+      }
+    sum += __shfl_xor(sum, 32, 64);
+    if (i < rows && lane < 32) a.stats[static_cast<int64_t>(i) * a.tiles + tile] = make_float2(top, sum);
+  }
+  if (!BF16 || !keep) return;
+  // Codes of all the wave's rows, two bytes each, then 16 bytes a lane of 16 rows
+  // of a panel one behind another.
+  constexpr int kRow = kWide / 8;  // 16-byte vectors of a row
+#pragma unroll
+  for (int j = 0; j < IN; ++j)
+#pragma unroll
+    for (int m = 0; m < IM; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = 4 * m + q, r = 32 * j + (lane & 31);
+        uint32_t code[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          code[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(
+              acc[m][j][4 * q + 2 * e] * (-kCodeSteps / 65535.0f), acc[m][j][4 * q + 2 * e + 1] * (-kCodeSteps / 65535.0f)));
+        *reinterpret_cast<u32x2 MSS_LDS*>(mine + (r * kRow + (c ^ (r & (kRow - 1)))) * 16 + (lane >> 5) * 8) =
+            u32x2{code[0], code[1]};
+      }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+  for (int q = 0; q < kWide / 32 * 2 * IN; ++q) {
+    const int r = q % (2 * IN) * 16 + (lane >> 2), c = q / (2 * IN) * 4 + (lane & 3);
+    const u32x4 p = *reinterpret_cast<const u32x4 MSS_LDS*>(mine + (r * kRow + (c ^ (r & (kRow - 1)))) * 16);
+    if (wi + r < rows && wv + c * 8 < a.vpad)
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.probs) + z_index(a, wi + r, wv + c * 8)) = p;
   }
 }
 
 // ---------------------------------------------------------------- dx
 
-template <typename T, int IM, int IN>
+template <typename T>
 __global__ __launch_bounds__(T::kThreads) void dx_part_kernel(LossArgs a, int first) {
-  __shared__ __attribute__((aligned(256))) char lds[2 * T::kStage];
+  __shared__ __attribute__((aligned(256))) char lds[T::kLds];
+  constexpr int IM = T::kIM, IN = T::kIN;
   const int rows = live_rows(a, first), lane = threadIdx.x & 63;
   const int mt = (rows + T::kM - 1) / T::kM, nt = (a.dim + T::kN - 1) / T::kN;
   if (mt == 0) return;
   // tiles of one part side by side: those of an XCD read the same rows of weights
-  const int splits = dx_splits(a, mt * nt), per = (a.vocab + kStep - 1) / kStep;
+  const int splits = dx_splits(a, mt * nt), per = (a.vocab + 63) / 64;
   const int all = mt * nt * splits, share = (all + 7) / 8, l = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
   if (static_cast<int>(blockIdx.x >> 3) >= share || l >= all) return;
   const int split = l / (mt * nt);
   const At at = tile_of(l - split * (mt * nt), mt, nt);
-  const int k0 = static_cast<int>(static_cast<int64_t>(per) * split / splits) * kStep;
-  const int k1 = static_cast<int>(static_cast<int64_t>(per) * (split + 1) / splits) * kStep;
+  const int k0 = static_cast<int>(static_cast<int64_t>(per) * split / splits) * 64;
+  const int k1 = static_cast<int>(static_cast<int64_t>(per) * (split + 1) / splits) * 64;
   const int i0 = at.m * T::kM, d0 = at.n * T::kN;
-  f32x16 acc[IM][IN];
+  typename T::Acc acc;
   clear(acc);
   T::run(z_side(a, i0, 0), w_side(a, 0, d0), k0, k1, k1, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
   float* part = a.part + static_cast<int64_t>(split) * a.piece * a.dpad;
@@ -419,12 +479,15 @@ __global__ __launch_bounds__(T::kThreads) void dx_part_kernel(LossArgs a, int fi
 // What the largest dz of each row lost when it was rounded to bf16, times the
 // row's x: without it a row's error would be that of its target's rounding, as
 // much again as dweight's own.  The rows whose entry lies in this tile are packed
-// 64 at a time, in order, into a step of their own: a sparse panel and the rows'
+// a step's worth at a time, in order, into a step of their own: a sparse panel and the rows'
 // x.
-template <typename T, int IM, int IN>
-__device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, int d0, char* lds, f32x16 (&acc)[IM][IN]) {
-  __shared__ int counts[T::kThreads / 64];
-  __shared__ int2 list[T::kThreads + 64];  // i, and v - v0 with the lost bits of a bf16
+template <typename T>
+__device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, int d0, char* lds, typename T::Acc& acc) {
+  constexpr int kStep = T::kStep;
+  // behind the stage that it uses
+  static_assert(T::kLds >= T::kStage + T::kThreads / 64 * 4 + (T::kThreads + kStep) * 8, "room for the list");
+  int2* list = reinterpret_cast<int2*>(lds + T::kStage);  // i, and v - v0 with the lost bits of a bf16
+  int* counts = reinterpret_cast<int*>(list + T::kThreads + kStep);
   char MSS_LDS* sh = (char MSS_LDS*)lds;
   const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
   int held = 0;
@@ -477,15 +540,16 @@ __device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, 
   if (held > 0) step(held);
 }
 
-template <typename IO, typename T, int IM, int IN>
+template <typename IO, typename T>
 __global__ __launch_bounds__(T::kThreads) void dw_tile_kernel(LossArgs a, int first) {
-  __shared__ __attribute__((aligned(256))) char lds[2 * T::kStage];
+  __shared__ __attribute__((aligned(256))) char lds[T::kLds];
+  constexpr int IM = T::kIM, IN = T::kIN;
   const int rows = live_rows(a, first), lane = threadIdx.x & 63;
   if (first > 0 && rows == 0) return;
   const At at = tile_at(blockIdx.x, (a.vocab + T::kM - 1) / T::kM, (a.dim + T::kN - 1) / T::kN);
   if (at.m < 0) return;
   const int v0 = at.m * T::kM, d0 = at.n * T::kN;
-  f32x16 acc[IM][IN];
+  typename T::Acc acc;
   clear(acc);
   T::run(z_side(a, 0, v0), x_side(a, first, d0), 0, rows, rows, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
   if (a.planes == 1) add_lost<T>(a, first, rows, v0, d0, lds, acc);
@@ -509,10 +573,13 @@ __global__ __launch_bounds__(T::kThreads) void dw_tile_kernel(LossArgs a, int fi
 
 // ---------------------------------------------------------------- launches
 
-template <bool A, bool B>
-using Big = Tile<A, B, 2, 4, 4, 2>;    // 256 x 256, 8 waves
-template <bool A, bool B>
-using Small = Tile<A, B, 2, 2, 2, 1>;  // 128 x 64, 4 waves (dx: 64 x 128)
+// 256 x 256 with 8 waves, and small ones with 4
+typedef Tile<true, 64, true, true, 64, 2, 4, 4, 2, 64, 2> LogitsBig;
+typedef Tile<true, 64, true, true, 64, 2, 2, 2, 1, 64, 2> LogitsSmall;
+typedef Tile<true, kZPanel, false, false, 64, 2, 4, 4, 2, 32, 5> DxBig;
+typedef Tile<true, kZPanel, false, false, 64, 2, 2, 1, 2, 32, 4> DxSmall;
+typedef Tile<false, kZPanel, false, false, 64, 4, 2, 2, 4, 64, 2> DwBig;
+typedef Tile<false, kZPanel, false, false, 64, 2, 2, 2, 1, 32, 4> DwSmall;
 
 int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
@@ -522,45 +589,42 @@ int loss_vocab_tile(bool small) { return small ? 64 : 128; }
 
 hipError_t launch_logits(const LossArgs& a, int first, bool io_bf16, bool keep, hipStream_t stream) {
   const int n = std::min(a.piece, a.rows - first);
-  if (a.small) {
-    typedef Small<true, true> T;
+  auto go = [&](auto t) {
+    typedef decltype(t) T;
     const unsigned g = tile_blocks(tiles(a.vocab, T::kM), tiles(n, T::kN));
-    if (io_bf16) logits_kernel<true, T, 2, 1><<<g, T::kThreads, 0, stream>>>(a, first, keep);
-    else logits_kernel<false, T, 2, 1><<<g, T::kThreads, 0, stream>>>(a, first, keep);
-  } else {
-    typedef Big<true, true> T;
-    const unsigned g = tile_blocks(tiles(a.vocab, T::kM), tiles(n, T::kN));
-    if (io_bf16) logits_kernel<true, T, 4, 2><<<g, T::kThreads, 0, stream>>>(a, first, keep);
-    else logits_kernel<false, T, 4, 2><<<g, T::kThreads, 0, stream>>>(a, first, keep);
-  }
+    if (io_bf16) logits_kernel<true, T><<<g, T::kThreads, 0, stream>>>(a, first, keep);
+    else logits_kernel<false, T><<<g, T::kThreads, 0, stream>>>(a, first, keep);
+  };
+  if (a.small) go(LogitsSmall{});
+  else go(LogitsBig{});
   return hipGetLastError();
 }
 
 hipError_t launch_dx(const LossArgs& a, int first, hipStream_t stream) {
   const int n = std::min(a.piece, a.rows - first);
-  const int64_t m = a.small ? 64 : 256, w = a.small ? 128 : 256;
-  int64_t g = 0;  // the most that any count of live rows asks for
-  for (int64_t mt = 1; mt <= tiles(n, m); ++mt) {
-    const int64_t t = mt * tiles(a.dim, w);
-    g = std::max<int64_t>(g, (t * dx_splits(a, static_cast<int>(t)) + 7) / 8 * 8);
-  }
-  if (a.small) dx_part_kernel<Tile<true, false, 2, 2, 1, 2>, 1, 2><<<static_cast<unsigned>(g), 256, 0, stream>>>(a, first);
-  else dx_part_kernel<Big<true, false>, 4, 2><<<static_cast<unsigned>(g), 512, 0, stream>>>(a, first);
+  auto go = [&](auto t) {
+    typedef decltype(t) T;
+    int64_t g = 0;  // the most that any count of live rows asks for
+    for (int64_t mt = 1; mt <= tiles(n, T::kM); ++mt) {
+      const int64_t all = mt * tiles(a.dim, T::kN);
+      g = std::max<int64_t>(g, (all * dx_splits(a, static_cast<int>(all)) + 7) / 8 * 8);
+    }
+    dx_part_kernel<T><<<static_cast<unsigned>(g), T::kThreads, 0, stream>>>(a, first);
+  };
+  if (a.small) go(DxSmall{});
+  else go(DxBig{});
   return hipGetLastError();
 }
 
 hipError_t launch_dw(const LossArgs& a, int first, bool io_bf16, hipStream_t stream) {
-  if (a.small) {
-    typedef Small<false, false> T;
+  auto go = [&](auto t) {
+    typedef decltype(t) T;
     const unsigned g = tile_blocks(tiles(a.vocab, T::kM), tiles(a.dim, T::kN));
-    if (io_bf16) dw_tile_kernel<bf16_t, T, 2, 1><<<g, T::kThreads, 0, stream>>>(a, first);
-    else dw_tile_kernel<float, T, 2, 1><<<g, T::kThreads, 0, stream>>>(a, first);
-  } else {
-    typedef Big<false, false> T;
-    const unsigned g = tile_blocks(tiles(a.vocab, T::kM), tiles(a.dim, T::kN));
-    if (io_bf16) dw_tile_kernel<bf16_t, T, 4, 2><<<g, T::kThreads, 0, stream>>>(a, first);
-    else dw_tile_kernel<float, T, 4, 2><<<g, T::kThreads, 0, stream>>>(a, first);
-  }
+    if (io_bf16) dw_tile_kernel<bf16_t, T><<<g, T::kThreads, 0, stream>>>(a, first);
+    else dw_tile_kernel<float, T><<<g, T::kThreads, 0, stream>>>(a, first);
+  };
+  if (a.small) go(DwSmall{});
+  else go(DwBig{});
   return hipGetLastError();
 }
 

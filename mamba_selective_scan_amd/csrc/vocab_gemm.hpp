@@ -12,6 +12,12 @@ namespace mss {
 // what its rounding to bf16 takes; one 64 below (1e-28 of its tile's largest) is 0.
 constexpr float kCodeSteps = 1024.0f;
 
+// Columns of dz's panels, and where its elements and those of the probabilities lie.
+constexpr int kZPanel = 32;
+__device__ inline int64_t z_index(const LossArgs& a, int i, int v) {
+  return (static_cast<int64_t>(v / kZPanel) * a.piece + i) * kZPanel + v % kZPanel;
+}
+
 // How many parts of the vocabulary the dx product is cut into, for `tiles` tiles
 // of its rows and columns: the least time, in steps of about a microsecond, of the
 // rounds that the parts' workgroups make (256 of large tiles at a time, 768 of

@@ -253,8 +253,8 @@ __global__ __launch_bounds__(256) void row_kernel(LossArgs a, int first, bool bf
   a.fix[i] = best;
 }
 
-// dz of 32 rows of a piece in `panels` panels: a panel's 32 rows are one stretch of
-// memory.  Rows behind the last one that counts, up to the next 64, and columns
+// dz of 32 rows of a piece in `panels` times 64 columns: a panel's rows are one
+// stretch of memory.  Rows behind the last one that counts, up to the next 64, and columns
 // behind the vocabulary are 0.
 template <typename IO>
 __global__ __launch_bounds__(256) void dz_kernel(LossArgs a, int first, int panels, int tile_shift) {
@@ -268,8 +268,8 @@ __global__ __launch_bounds__(256) void dz_kernel(LossArgs a, int first, int pane
   const int c = (threadIdx.x & 7) * 8;
 #pragma unroll 2
   for (int p = p0; p < p1; ++p) {
-    const int64_t at = (static_cast<int64_t>(p) * a.piece + i) * 64 + c;
     const int v = p * 64 + c;
+    const int64_t at = z_index(a, i, v);
     float q[8];
     if constexpr (sizeof(IO) == 2) {
       const uint4 raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.probs) + at);
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(256) void dz_kernel(LossArgs a, int first, int pane
     const int r = i0 + k / a.entries, e = k % a.entries;
     const int id = a.near[static_cast<int64_t>(first + r) * a.entries + e];
     if (id < p0 * 64 || id >= p1 * 64) continue;
-    uint16_t* z = a.dz + (static_cast<int64_t>(id / 64) * a.piece + r) * 64 + id % 64;
+    uint16_t* z = a.dz + z_index(a, r, id);
     float v = a.value[static_cast<int64_t>(r) * a.entries + e];
     for (int n = 0; n < (sizeof(IO) == 2 ? 1 : 3); ++n) {
       const uint16_t b = bf16_bits(v);
