@@ -242,20 +242,25 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void bwd_kernel(LayerNormBwd
   }
 }
 
-// The workgroups' sums of 64 columns: 4 threads a column, each over every fourth.
-__global__ __launch_bounds__(256) void bwd_sum_kernel(LayerNormBwdArgs a) {
-  __shared__ float meet[4][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+// The workgroups' sums of 32 columns: 32 threads a column, each over every 32nd
+// part, which meet in a fixed order.
+__global__ __launch_bounds__(1024) void bwd_sum_kernel(LayerNormBwdArgs a) {
+  __shared__ float meet[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
   float* out = blockIdx.y == 0 ? a.dweight : a.dbias;
   if (out == nullptr) return;
   const float* p = a.sums + static_cast<int64_t>(blockIdx.y) * a.parts * a.dim + c;
   float s = 0.0f;
   if (c < a.dim)
-    for (int i = q; i < a.parts; i += 4) s += p[static_cast<int64_t>(i) * a.dim];
-  meet[q][threadIdx.x & 63] = s;
+#pragma unroll 8
+    for (int i = q; i < a.parts; i += 32) s += p[static_cast<int64_t>(i) * a.dim];
+  meet[q][threadIdx.x & 31] = s;
   __syncthreads();
-  if (q == 0 && c < a.dim)
-    out[c] = (meet[0][threadIdx.x] + meet[1][threadIdx.x]) + (meet[2][threadIdx.x] + meet[3][threadIdx.x]);
+  if (threadIdx.x >= 32 || c >= a.dim) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s += meet[i][threadIdx.x];
+  out[c] = s;
 }
 
 template <typename IO, typename RES>
@@ -270,7 +275,7 @@ hipError_t launch_bwd(const LayerNormBwdArgs& a, hipStream_t stream) {
   else if (d <= 16384) bwd_kernel<IO, RES, 1024, 2, false><<<g, 1024, 0, stream>>>(a);
   else bwd_kernel<IO, RES, 1024, 4, true><<<g, 1024, 0, stream>>>(a);
   if (a.dweight != nullptr || a.dbias != nullptr)
-    bwd_sum_kernel<<<dim3(static_cast<unsigned>((d + 63) / 64), 2), 256, 0, stream>>>(a);
+    bwd_sum_kernel<<<dim3(static_cast<unsigned>((d + 31) / 32), 2), 1024, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -86,7 +86,8 @@ struct LossArgs {
   int64_t xrows;   // a multiple of 64; those behind the last row that counts, to the next 64, are 0
   uint16_t* wp;    // [planes][dpad / 64][vocab][64], or the weight itself
   bool pack_w;
-  bool small;      // small tiles of the products
+  bool small_logits, small_dx, small_dw;  // small tiles of a product
+  bool dw_vecs;    // dweight's rows are whole aligned 16-byte vectors
   // of a piece of rows
   int piece;       // rows of a piece, a multiple of 64
   int pieces;

@@ -70,11 +70,21 @@ size_t norm_bwd_workspace(const mss_layer_norm_bwd_args* a) {
 constexpr int64_t kPieceBytes = int64_t{2} << 30;
 
 struct LossPlan {
-  bool grad, pack_w, small;
+  bool grad, pack_w, small_logits, small_dx, small_dw;
   int64_t planes, dpad, vpad, tiles, words, piece, pieces, splits, xrows;
   size_t live, row_of, place, counts, share, known, near, where, picked, xp, wp, stats, sums, probs, dz, value, fix, part,
       dw_sum, bytes;
 };
+
+// Whether a product of m x n runs in small tiles (mt x nt): 256 large ones of 256 x
+// 256 run at once, 768 small ones.
+bool small_tiles(int64_t m, int64_t mt, int64_t n, int64_t nt, int64_t steps) {
+  auto tiles = [&](int64_t p, int64_t q) { return (m + p - 1) / p * ((n + q - 1) / q); };
+  const double large = static_cast<double>((tiles(256, 256) + 255) / 256) * (1.3 * static_cast<double>(steps) + 8);
+  const int64_t small = tiles(mt, nt);
+  const double rounds = static_cast<double>((small + 767) / 768), filled = std::min<double>(3, (small + 255) / 256);
+  return rounds * (0.2 * filled * static_cast<double>(steps) + 4) < large;
+}
 
 LossPlan loss_plan(const mss_linear_loss_args* a) {
   LossPlan p{};
@@ -83,8 +93,12 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.planes = f32 ? 3 : 1;
   p.dpad = up(a->dim, 64);
   p.vpad = up(a->vocab, 64);
-  p.small = a->rows <= 128;
-  p.tiles = (a->vocab + mss::loss_vocab_tile(p.small) - 1) / mss::loss_vocab_tile(p.small);
+  const int64_t pairs = f32 ? 6 : 1;
+  p.small_logits = small_tiles(a->vocab, 128, a->rows, 64, up(a->dim, 64) / 64 * pairs);
+  // (the dx product is cut along its sum: few rows are what leaves large tiles empty)
+  p.small_dx = a->rows <= 128;
+  p.small_dw = small_tiles(a->vocab, 128, a->dim, 64, up(a->rows, 64) / 64 * pairs);
+  p.tiles = (a->vocab + mss::loss_vocab_tile(p.small_logits) - 1) / mss::loss_vocab_tile(p.small_logits);
   p.words = (p.tiles + 31) / 32;
   // bf16 weights are read where they are if their rows are whole 16-byte vectors,
   // one behind another, and 256 of them within 32-bit offsets
@@ -324,7 +338,10 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.pack_w = p.pack_w;
   k.wp = p.pack_w ? reinterpret_cast<uint16_t*>(ws + p.wp) : const_cast<uint16_t*>(static_cast<const uint16_t*>(a->weight));
   k.xrows = p.xrows;
-  k.small = p.small;
+  k.small_logits = p.small_logits;
+  k.small_dx = p.small_dx;
+  k.small_dw = p.small_dw;
+  k.dw_vecs = D % 8 == 0 && aligned(a->dweight, 16) && (V == 1 || a->dweight_stride % 8 == 0);
   k.piece = static_cast<int>(p.piece);
   k.pieces = static_cast<int>(p.pieces);
   k.tiles = static_cast<int>(p.tiles);

@@ -553,6 +553,37 @@ __global__ __launch_bounds__(T::kThreads) void dw_tile_kernel(LossArgs a, int fi
   clear(acc);
   T::run(z_side(a, 0, v0), x_side(a, first, d0), 0, rows, rows, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
   if (a.planes == 1) add_lost<T>(a, first, rows, v0, d0, lds, acc);
+  if constexpr (sizeof(IO) == 2) {
+    if (a.pieces == 1 && a.dw_vecs) {
+      // bf16 through LDS, so that a lane stores 16 bytes: 32 rows of the wave at a
+      // time, the 16-byte vectors of a row turned by the row
+      constexpr int kRow = 4 * IN;  // vectors of a row
+      char MSS_LDS* mine = (char MSS_LDS*)lds + uniform(static_cast<int>(threadIdx.x) >> 6) * (kRow * 32 * 16);
+      static_assert(T::kLds >= T::kThreads / 64 * kRow * 32 * 16, "room for the waves' rows");
+#pragma unroll
+      for (int i = 0; i < IM; ++i) {
+#pragma unroll
+        for (int j = 0; j < IN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = acc_row(e), c = 32 * j + (lane & 31);
+            *reinterpret_cast<uint16_t MSS_LDS*>(mine + (r * kRow + ((c >> 3) ^ (r >> 1 & (kRow - 1)))) * 16 + (c & 7) * 2) =
+                bf16_bits(acc[i][j][e]);
+          }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int q = 0; q < kRow * 32 / 64; ++q) {
+          const int r = (q * 64 + lane) / kRow, c = lane % kRow;
+          const u32x4 p = *reinterpret_cast<const u32x4 MSS_LDS*>(mine + (r * kRow + (c ^ (r >> 1 & (kRow - 1)))) * 16);
+          const int64_t v = v0 + T::wave_m() + 32 * i + r;
+          const int d = d0 + T::wave_n() + c * 8;
+          if (v < a.vocab && d < a.dim) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.dweight) + v * a.sdw + d) = p;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+      return;
+    }
+  }
   const int d1 = d0 + T::wave_n() + (lane & 31);
 #pragma unroll
   for (int i = 0; i < IM; ++i)
@@ -579,7 +610,7 @@ typedef Tile<true, 64, true, true, 64, 2, 2, 2, 1, 64, 2> LogitsSmall;
 typedef Tile<true, kZPanel, false, false, 64, 2, 4, 4, 2, 32, 5> DxBig;
 typedef Tile<true, kZPanel, false, false, 64, 2, 2, 1, 2, 32, 4> DxSmall;
 typedef Tile<false, kZPanel, false, false, 64, 4, 2, 2, 4, 64, 2> DwBig;
-typedef Tile<false, kZPanel, false, false, 64, 2, 2, 2, 1, 32, 4> DwSmall;
+typedef Tile<false, kZPanel, false, false, 64, 4, 1, 1, 2, 32, 4> DwSmall;
 
 int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
@@ -595,7 +626,7 @@ hipError_t launch_logits(const LossArgs& a, int first, bool io_bf16, bool keep, 
     if (io_bf16) logits_kernel<true, T><<<g, T::kThreads, 0, stream>>>(a, first, keep);
     else logits_kernel<false, T><<<g, T::kThreads, 0, stream>>>(a, first, keep);
   };
-  if (a.small) go(LogitsSmall{});
+  if (a.small_logits) go(LogitsSmall{});
   else go(LogitsBig{});
   return hipGetLastError();
 }
@@ -611,7 +642,7 @@ hipError_t launch_dx(const LossArgs& a, int first, hipStream_t stream) {
     }
     dx_part_kernel<T><<<static_cast<unsigned>(g), T::kThreads, 0, stream>>>(a, first);
   };
-  if (a.small) go(DxSmall{});
+  if (a.small_dx) go(DxSmall{});
   else go(DxBig{});
   return hipGetLastError();
 }
@@ -623,7 +654,7 @@ hipError_t launch_dw(const LossArgs& a, int first, bool io_bf16, hipStream_t str
     if (io_bf16) dw_tile_kernel<bf16_t, T><<<g, T::kThreads, 0, stream>>>(a, first);
     else dw_tile_kernel<float, T><<<g, T::kThreads, 0, stream>>>(a, first);
   };
-  if (a.small) go(DwSmall{});
+  if (a.small_dw) go(DwSmall{});
   else go(DwBig{});
   return hipGetLastError();
 }

@@ -24,8 +24,8 @@ __device__ inline int64_t z_index(const LossArgs& a, int i, int v) {
 // small ones), each with some steps besides its own, and of writing and adding
 // the parts.  Host and device agree on it.
 __host__ __device__ inline int dx_splits(const LossArgs& a, int tiles) {
-  const float slots = a.small ? 768.0f : 256.0f, steps = static_cast<float>((a.vocab + 63) / 64);
-  const float part = a.small ? 0.016f : 0.13f;
+  const float slots = a.small_dx ? 768.0f : 256.0f, steps = static_cast<float>((a.vocab + 63) / 64 * (a.planes == 1 ? 1 : 6));
+  const float part = a.small_dx ? 0.016f : 0.13f;
   int best = 1;
   float least = 3e38f;
   for (int s = 1; s <= a.splits; s += s < 8 ? 1 : s / 4) {
@@ -40,7 +40,7 @@ __host__ __device__ inline int dx_splits(const LossArgs& a, int tiles) {
 
 // Tiles of the dx product for this many rows.
 __host__ __device__ inline int dx_tiles(const LossArgs& a, int rows) {
-  return a.small ? (rows + 63) / 64 * ((a.dim + 127) / 128) : (rows + 255) / 256 * ((a.dim + 255) / 256);
+  return a.small_dx ? (rows + 63) / 64 * ((a.dim + 127) / 128) : (rows + 255) / 256 * ((a.dim + 255) / 256);
 }
 
 // logits of the piece's rows: stats, and with `keep` the codes or logits

@@ -358,6 +358,48 @@ __global__ __launch_bounds__(256) void dx_kernel(LossArgs a, int first) {
   }
 }
 
+// The same where there are few rows and many parts: a workgroup 256 columns of a
+// row, its waves every fourth part.
+template <typename IO>
+__global__ __launch_bounds__(256) void dx_few_kernel(LossArgs a, int first) {
+  __shared__ float4 meet[3][64];
+  const int row = blockIdx.x, j = a.place[row], lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (j < 0 ? first != 0 : j < first || j >= first + a.piece) return;
+  const int splits = dx_splits(a, dx_tiles(a, min(a.piece, *a.live - first)));
+  const int c = blockIdx.y * 256 + lane * 4;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (j >= 0 && c < a.dim) {
+    const float* part = a.part + static_cast<int64_t>(j - first) * a.dpad + c;
+#pragma unroll 8
+    for (int q = wave; q < splits; q += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(q) * a.piece * a.dpad);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  if (wave > 0) meet[wave - 1][lane] = s;
+  __syncthreads();
+  if (wave > 0 || c >= a.dim) return;
+  float out[4] = {s.x, s.y, s.z, s.w};
+  for (int q = 0; q < 3; ++q) {
+    const float4 v = meet[q][lane];
+    out[0] += v.x;
+    out[1] += v.y;
+    out[2] += v.z;
+    out[3] += v.w;
+  }
+  const int2 f = sizeof(IO) == 2 && j >= 0 ? a.fix[j - first] : make_int2(-1, 0);
+  if (f.x >= 0) {
+    float w[4];
+    load_part<IO, 4>(static_cast<const IO*>(a.weight) + f.x * a.sw + c, a.dim - c, w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = fmaf(__int_as_float(f.y), w[e], out[e]);
+  }
+  store_part<IO, 4>(static_cast<IO*>(a.dx) + row * a.sdx + c, a.dim - c, out);
+}
+
 template <typename IO>
 __global__ __launch_bounds__(256) void dw_kernel(LossArgs a) {
   const int64_t v = blockIdx.x;
@@ -382,7 +424,7 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
     if (a.total != nullptr) total_kernel<<<1, 1024, 0, s>>>(a);
     return a.dweight != nullptr ? launch_dw(a, 0, sizeof(IO) == 2, s) : hipGetLastError();
   }
-  const int shift = loss_vocab_tile(a.small) == 64 ? 6 : 7;
+  const int shift = loss_vocab_tile(a.small_logits) == 64 ? 6 : 7;
   pack_kernel<IO><<<static_cast<unsigned>(a.xrows), 256, 0, s>>>(a, shift);
   if (a.pack_w) pack_weight_kernel<IO><<<static_cast<unsigned>(a.vocab + 7) / 8, 256, 0, s>>>(a);
   for (int p = 0; p < a.pieces; ++p) {
@@ -399,7 +441,8 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
     }
     if (a.dx != nullptr) {
       if ((e = launch_dx(a, first, s)) != hipSuccess) return e;
-      dx_kernel<IO><<<rows, 256, 0, s>>>(a, first);
+      if (a.small_dx) dx_few_kernel<IO><<<dim3(rows, static_cast<unsigned>(a.dim + 255) / 256), 256, 0, s>>>(a, first);
+      else dx_kernel<IO><<<rows, 256, 0, s>>>(a, first);
     }
     if (a.dweight != nullptr && (e = launch_dw(a, first, sizeof(IO) == 2, s)) != hipSuccess) return e;
   }
