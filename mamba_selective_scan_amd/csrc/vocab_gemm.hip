@@ -444,16 +444,15 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
 // ---------------------------------------------------------------- dx
 
 template <typename T>
-__global__ __launch_bounds__(T::kThreads) void dx_part_kernel(LossArgs a, int first) {
-  __shared__ __attribute__((aligned(256))) char lds[T::kLds];
+__device__ inline void dx_part(const LossArgs& a, int first, int id, char* lds) {
   constexpr int IM = T::kIM, IN = T::kIN;
   const int rows = live_rows(a, first), lane = threadIdx.x & 63;
   const int mt = (rows + T::kM - 1) / T::kM, nt = (a.dim + T::kN - 1) / T::kN;
   if (mt == 0) return;
   // tiles of one part side by side: those of an XCD read the same rows of weights
   const int splits = dx_splits(a, mt * nt), per = (a.vocab + 63) / 64;
-  const int all = mt * nt * splits, share = (all + 7) / 8, l = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
-  if (static_cast<int>(blockIdx.x >> 3) >= share || l >= all) return;
+  const int all = mt * nt * splits, share = (all + 7) / 8, l = (id & 7) * share + (id >> 3);
+  if ((id >> 3) >= share || l >= all) return;
   const int split = l / (mt * nt);
   const At at = tile_of(l - split * (mt * nt), mt, nt);
   const int k0 = static_cast<int>(static_cast<int64_t>(per) * split / splits) * 64;
@@ -472,6 +471,12 @@ __global__ __launch_bounds__(T::kThreads) void dx_part_kernel(LossArgs a, int fi
       for (int e = 0; e < 16; ++e)
         if (d < a.dim && r0 + acc_row(e) < rows) part[static_cast<int64_t>(r0 + acc_row(e)) * a.dpad + d] = acc[i][j][e];
     }
+}
+
+template <typename T>
+__global__ __launch_bounds__(T::kThreads) void dx_part_kernel(LossArgs a, int first) {
+  __shared__ __attribute__((aligned(256))) char lds[T::kLds];
+  dx_part<T>(a, first, static_cast<int>(blockIdx.x), lds);
 }
 
 // ---------------------------------------------------------------- dweight
@@ -541,12 +546,11 @@ __device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, 
 }
 
 template <typename IO, typename T>
-__global__ __launch_bounds__(T::kThreads) void dw_tile_kernel(LossArgs a, int first) {
-  __shared__ __attribute__((aligned(256))) char lds[T::kLds];
+__device__ inline void dw_tile(const LossArgs& a, int first, int id, char* lds) {
   constexpr int IM = T::kIM, IN = T::kIN;
   const int rows = live_rows(a, first), lane = threadIdx.x & 63;
   if (first > 0 && rows == 0) return;
-  const At at = tile_at(blockIdx.x, (a.vocab + T::kM - 1) / T::kM, (a.dim + T::kN - 1) / T::kN);
+  const At at = tile_at(id, (a.vocab + T::kM - 1) / T::kM, (a.dim + T::kN - 1) / T::kN);
   if (at.m < 0) return;
   const int v0 = at.m * T::kM, d0 = at.n * T::kN;
   typename T::Acc acc;
@@ -602,15 +606,31 @@ __global__ __launch_bounds__(T::kThreads) void dw_tile_kernel(LossArgs a, int fi
       }
 }
 
+template <typename IO, typename T>
+__global__ __launch_bounds__(T::kThreads) void dw_tile_kernel(LossArgs a, int first) {
+  __shared__ __attribute__((aligned(256))) char lds[T::kLds];
+  dw_tile<IO, T>(a, first, static_cast<int>(blockIdx.x), lds);
+}
+
+// Both products of small tiles in one launch, the dx product's workgroups first.
+template <typename IO, typename X, typename W>
+__global__ __launch_bounds__(X::kThreads) void small_kernel(LossArgs a, int first, int dx_blocks) {
+  static_assert(X::kThreads == W::kThreads, "one launch");
+  __shared__ __attribute__((aligned(256))) char lds[X::kLds > W::kLds ? X::kLds : W::kLds];
+  const int id = static_cast<int>(blockIdx.x);
+  if (id < dx_blocks) dx_part<X>(a, first, id, lds);
+  else dw_tile<IO, W>(a, first, id - dx_blocks, lds);
+}
+
 // ---------------------------------------------------------------- launches
 
 // 256 x 256 with 8 waves, and small ones with 4
 typedef Tile<true, 64, true, true, 64, 2, 4, 4, 2, 64, 2> LogitsBig;
 typedef Tile<true, 64, true, true, 64, 2, 2, 2, 1, 64, 2> LogitsSmall;
 typedef Tile<true, kZPanel, false, false, 64, 2, 4, 4, 2, 32, 5> DxBig;
-typedef Tile<true, kZPanel, false, false, 64, 2, 2, 1, 2, 32, 4> DxSmall;
+typedef Tile<true, kZPanel, false, false, 64, 2, 2, 1, 2, 32, 3> DxSmall;
 typedef Tile<false, kZPanel, false, false, 64, 4, 2, 2, 4, 64, 2> DwBig;
-typedef Tile<false, kZPanel, false, false, 64, 4, 1, 1, 2, 32, 4> DwSmall;
+typedef Tile<false, kZPanel, false, false, 64, 4, 1, 1, 2, 32, 3> DwSmall;
 
 int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
@@ -631,31 +651,44 @@ hipError_t launch_logits(const LossArgs& a, int first, bool io_bf16, bool keep, 
   return hipGetLastError();
 }
 
-hipError_t launch_dx(const LossArgs& a, int first, hipStream_t stream) {
+hipError_t launch_gradients(const LossArgs& a, int first, bool io_bf16, hipStream_t stream) {
   const int n = std::min(a.piece, a.rows - first);
-  auto go = [&](auto t) {
+  const bool dx = a.dx != nullptr && n > 0, dw = a.dweight != nullptr;
+  // the most workgroups that any count of live rows asks for
+  auto dx_blocks = [&](auto t) {
     typedef decltype(t) T;
-    int64_t g = 0;  // the most that any count of live rows asks for
+    int64_t g = 0;
     for (int64_t mt = 1; mt <= tiles(n, T::kM); ++mt) {
       const int64_t all = mt * tiles(a.dim, T::kN);
       g = std::max<int64_t>(g, (all * dx_splits(a, static_cast<int>(all)) + 7) / 8 * 8);
     }
-    dx_part_kernel<T><<<static_cast<unsigned>(g), T::kThreads, 0, stream>>>(a, first);
+    return static_cast<unsigned>(g);
   };
-  if (a.small_dx) go(DxSmall{});
-  else go(DxBig{});
-  return hipGetLastError();
-}
-
-hipError_t launch_dw(const LossArgs& a, int first, bool io_bf16, hipStream_t stream) {
-  auto go = [&](auto t) {
+  auto dw_blocks = [&](auto t) {
     typedef decltype(t) T;
-    const unsigned g = tile_blocks(tiles(a.vocab, T::kM), tiles(a.dim, T::kN));
-    if (io_bf16) dw_tile_kernel<bf16_t, T><<<g, T::kThreads, 0, stream>>>(a, first);
-    else dw_tile_kernel<float, T><<<g, T::kThreads, 0, stream>>>(a, first);
+    return tile_blocks(tiles(a.vocab, T::kM), tiles(a.dim, T::kN));
   };
-  if (a.small_dw) go(DwSmall{});
-  else go(DwBig{});
+  auto go_dx = [&](auto t) {
+    typedef decltype(t) T;
+    dx_part_kernel<T><<<dx_blocks(t), T::kThreads, 0, stream>>>(a, first);
+  };
+  auto go_dw = [&](auto t) {
+    typedef decltype(t) T;
+    if (io_bf16) dw_tile_kernel<bf16_t, T><<<dw_blocks(t), T::kThreads, 0, stream>>>(a, first);
+    else dw_tile_kernel<float, T><<<dw_blocks(t), T::kThreads, 0, stream>>>(a, first);
+  };
+  if (dx && dw && a.small_dx && a.small_dw) {
+    const unsigned gx = dx_blocks(DxSmall{}), g = gx + dw_blocks(DwSmall{});
+    if (io_bf16)
+      small_kernel<bf16_t, DxSmall, DwSmall><<<g, DxSmall::kThreads, 0, stream>>>(a, first, static_cast<int>(gx));
+    else
+      small_kernel<float, DxSmall, DwSmall><<<g, DxSmall::kThreads, 0, stream>>>(a, first, static_cast<int>(gx));
+    return hipGetLastError();
+  }
+  if (dx && a.small_dx) go_dx(DxSmall{});
+  else if (dx) go_dx(DxBig{});
+  if (dw && a.small_dw) go_dw(DwSmall{});
+  else if (dw) go_dw(DwBig{});
   return hipGetLastError();
 }
 
