@@ -68,6 +68,7 @@ struct LossArgs {
   void* dweight;
   // workspace
   int* live;       // [1] rows that count
+  int* cuts;       // [pieces] parts of the vocabulary that a piece's dx product is cut into
   int* row_of;     // [rows] row of the i-th of them
   int* place;      // [rows] the i of a row, or -1
   uint8_t* counts; // [rows] whether it counts
@@ -78,8 +79,8 @@ struct LossArgs {
   int where_words;
   float* picked;   // [rows][entries] their logits
   // Rows, weights and dz as bf16 operands of the products: one plane, or three
-  // whose sum is the fp32 value.  They lie in panels, [columns / 64][rows][64] (dz:
-  // 32), so that a tile's part of any of them is one stretch of memory.
+  // whose sum is the fp32 value.  They lie in panels, [columns / 64][rows][64] (32 in
+  // place of 64 for dz, and for all of three planes), so that a tile's part of any of them is one stretch of memory.
   int planes;
   int64_t dpad;    // columns of x and weight, a multiple of 64
   uint16_t* xp;    // [planes][dpad / 64][xrows][64]
@@ -87,6 +88,8 @@ struct LossArgs {
   uint16_t* wp;    // [planes][dpad / 64][vocab][64], or the weight itself
   bool pack_w;
   bool small_logits, small_dx, small_dw;  // small tiles of a product
+  int vocab_tile;  // vocabulary entries that share a maximum
+  int dw_blocks, dw_splits;  // workgroups of the dweight product, and the parts of the rows they are cut into
   bool dw_vecs;    // dweight's rows are whole aligned 16-byte vectors
   // of a piece of rows
   int piece;       // rows of a piece, a multiple of 64
@@ -95,16 +98,15 @@ struct LossArgs {
   int64_t vpad;    // columns of dz, a multiple of 64
   float2* stats;   // [piece][tiles] an integer R and the sum of e^(z - R)
   float2* sums;    // [piece] `from` and c / sum, the row's sum of e^z being sum e^from
-  void* probs;     // [vpad / 32][piece][32] codes of the logits (bf16), or the logits (fp32)
-  uint16_t* dz;    // [planes][vpad / 32][piece][32] (bf16: probs itself)
+  void* probs;     // [piece / 64][vpad / 32][64][32] codes of the logits (bf16), or the logits (fp32)
+  uint16_t* dz;    // [planes][piece / 64][vpad / 32][64][32] (bf16: probs itself)
   float* value;    // [piece][entries] dz of the entries
   int2* fix;       // [piece] (bf16) id and what its dz lost by its rounding, as float bits; or id -1
   float* part;     // [splits][piece][dpad]
   int splits;      // at most
-  float* dw_sum;   // [vocab][dpad] (more than one piece)
+  float* dw_sum;   // [dw_splits][vocab][dpad] (more than one part or piece; null otherwise)
 };
 
-int loss_vocab_tile(bool small);
 hipError_t launch_loss(const LossArgs& a, bool io_bf16, hipStream_t stream);
 hipError_t launch_scale(const void* in, const float* factor, void* out, int64_t n, bool bf16,
                         hipStream_t stream);

@@ -10,6 +10,7 @@
 #include "mss.h"
 #include "mss_checks.hpp"
 #include "mss_train.hpp"
+#include "vocab_gemm.hpp"
 
 namespace {
 
@@ -71,20 +72,10 @@ constexpr int64_t kPieceBytes = int64_t{2} << 30;
 
 struct LossPlan {
   bool grad, pack_w, small_logits, small_dx, small_dw;
-  int64_t planes, dpad, vpad, tiles, words, piece, pieces, splits, xrows;
-  size_t live, row_of, place, counts, share, known, near, where, picked, xp, wp, stats, sums, probs, dz, value, fix, part,
+  int64_t planes, dpad, vpad, tiles, words, piece, pieces, splits, xrows, vocab_tile, dw_splits;
+  size_t live, cuts, row_of, place, counts, share, known, near, where, picked, xp, wp, stats, sums, probs, dz, value, fix, part,
       dw_sum, bytes;
 };
-
-// Whether a product of m x n runs in small tiles (mt x nt): 256 large ones of 256 x
-// 256 run at once, 768 small ones.
-bool small_tiles(int64_t m, int64_t mt, int64_t n, int64_t nt, int64_t steps) {
-  auto tiles = [&](int64_t p, int64_t q) { return (m + p - 1) / p * ((n + q - 1) / q); };
-  const double large = static_cast<double>((tiles(256, 256) + 255) / 256) * (1.3 * static_cast<double>(steps) + 8);
-  const int64_t small = tiles(mt, nt);
-  const double rounds = static_cast<double>((small + 767) / 768), filled = std::min<double>(3, (small + 255) / 256);
-  return rounds * (0.2 * filled * static_cast<double>(steps) + 4) < large;
-}
 
 LossPlan loss_plan(const mss_linear_loss_args* a) {
   LossPlan p{};
@@ -93,12 +84,15 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.planes = f32 ? 3 : 1;
   p.dpad = up(a->dim, 64);
   p.vpad = up(a->vocab, 64);
-  const int64_t pairs = f32 ? 6 : 1;
-  p.small_logits = small_tiles(a->vocab, 128, a->rows, 64, up(a->dim, 64) / 64 * pairs);
-  // (the dx product is cut along its sum: few rows are what leaves large tiles empty)
-  p.small_dx = a->rows <= 128;
-  p.small_dw = small_tiles(a->vocab, 128, a->dim, 64, up(a->rows, 64) / 64 * pairs);
-  p.tiles = (a->vocab + mss::loss_vocab_tile(p.small_logits) - 1) / mss::loss_vocab_tile(p.small_logits);
+  const int64_t rows = std::max<int64_t>(a->rows, 1);
+  auto steps = [](int64_t n) { return (n + 63) / 64; };
+  auto logits_time = [&](bool small) {
+    const mss::TileShape t = mss::logits_shape(f32, small);
+    return mss::product_time(t, static_cast<float>(mss::tiles_of(t, a->vocab, rows)), 1.0f, static_cast<float>(steps(a->dim)));
+  };
+  p.small_logits = logits_time(true) < logits_time(false);
+  p.vocab_tile = f32 || p.small_logits ? 64 : 128;
+  p.tiles = (a->vocab + p.vocab_tile - 1) / p.vocab_tile;
   p.words = (p.tiles + 31) / 32;
   // bf16 weights are read where they are if their rows are whole 16-byte vectors,
   // one behind another, and 256 of them within 32-bit offsets
@@ -106,12 +100,36 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
              (a->vocab > 1 && (a->weight_stride % 8 != 0 || a->weight_stride < a->dim ||
                                a->weight_stride > (int64_t{1} << 21)));
   const int64_t a_row = p.tiles * 8 + (p.grad ? p.vpad * (f32 ? 10 : 2) : 0);
-  const int64_t rows = std::max<int64_t>(a->rows, 1);
   p.pieces = (rows * a_row + kPieceBytes - 1) / kPieceBytes;
   p.piece = up((rows + p.pieces - 1) / p.pieces, 256);
   p.pieces = (rows + p.piece - 1) / p.piece;
   // parts of the dx product, within 512 MiB of them
   p.splits = std::clamp<int64_t>((int64_t{1} << 29) / (p.piece * p.dpad * 4), 1, 64);
+  const int64_t piece_rows = std::min(rows, p.piece);
+  auto best_time = [&](mss::TileShape t, int64_t tiles, int64_t sum, int most, int64_t* parts) {
+    float least = 0.0f;
+    for (int s = 1; s <= most; ++s) {
+      const float time = mss::product_time(t, static_cast<float>(tiles), static_cast<float>(s), static_cast<float>(steps(sum)));
+      if (s > 1 && time >= least) continue;
+      least = time;
+      if (parts != nullptr) *parts = s;
+    }
+    return least;
+  };
+  auto dx_time = [&](bool small) {
+    const mss::TileShape t = mss::dx_shape(f32, small);
+    return best_time(t, mss::tiles_of(t, piece_rows, a->dim), a->vocab, static_cast<int>(p.splits), nullptr);
+  };
+  p.small_dx = dx_time(true) < dx_time(false);
+  // and of the dweight product, of which a piece after the first has none of its own
+  const int dw_most = p.pieces > 1 || a->dweight == nullptr ? 1 : static_cast<int>(std::clamp<int64_t>((int64_t{1} << 29) / (a->vocab * p.dpad * 4), 1, 64));
+  int64_t dw_parts[2];
+  auto dw_time = [&](bool small) {
+    const mss::TileShape t = mss::dw_shape(f32, small);
+    return best_time(t, mss::tiles_of(t, a->vocab, a->dim), piece_rows, dw_most, &dw_parts[small]);
+  };
+  p.small_dw = dw_time(true) < dw_time(false);
+  p.dw_splits = dw_parts[p.small_dw];
   p.xrows = up(rows, 64);
   size_t at = 0;
   auto room = [&](int64_t n) {
@@ -120,6 +138,7 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
     return here;
   };
   p.live = room(4);
+  p.cuts = room(p.pieces * 4);
   p.row_of = room(rows * 4);
   p.place = room(rows * 4);
   p.counts = room(rows);
@@ -137,7 +156,7 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.value = room(p.grad ? p.piece * a->entries * 4 : 0);
   p.fix = room(p.grad && !f32 ? p.piece * 8 : 0);
   p.part = room(a->dx != nullptr ? p.splits * p.piece * p.dpad * 4 : 0);
-  p.dw_sum = room(a->dweight != nullptr && p.pieces > 1 ? a->vocab * p.dpad * 4 : 0);
+  p.dw_sum = room(a->dweight != nullptr && (p.pieces > 1 || p.dw_splits > 1) ? p.dw_splits * a->vocab * p.dpad * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -323,6 +342,7 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.dx = R > 0 ? a->dx : nullptr;
   k.dweight = a->dweight;
   k.live = reinterpret_cast<int*>(ws + p.live);
+  k.cuts = reinterpret_cast<int*>(ws + p.cuts);
   k.row_of = reinterpret_cast<int*>(ws + p.row_of);
   k.place = reinterpret_cast<int*>(ws + p.place);
   k.counts = reinterpret_cast<uint8_t*>(ws + p.counts);
@@ -341,6 +361,10 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.small_logits = p.small_logits;
   k.small_dx = p.small_dx;
   k.small_dw = p.small_dw;
+  k.vocab_tile = static_cast<int>(p.vocab_tile);
+  const mss::TileShape dw = mss::dw_shape(p.planes == 3, p.small_dw);
+  k.dw_blocks = static_cast<int>((mss::tiles_of(dw, V, D) + 7) / 8 * 8);
+  k.dw_splits = static_cast<int>(p.dw_splits);
   k.dw_vecs = D % 8 == 0 && aligned(a->dweight, 16) && (V == 1 || a->dweight_stride % 8 == 0);
   k.piece = static_cast<int>(p.piece);
   k.pieces = static_cast<int>(p.pieces);
@@ -354,7 +378,7 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.sums = reinterpret_cast<float2*>(ws + p.sums);
   k.part = reinterpret_cast<float*>(ws + p.part);
   k.splits = static_cast<int>(p.splits);
-  k.dw_sum = reinterpret_cast<float*>(ws + p.dw_sum);
+  k.dw_sum = a->dweight != nullptr && (p.pieces > 1 || p.dw_splits > 1) ? reinterpret_cast<float*>(ws + p.dw_sum) : nullptr;
   const hipError_t e = mss::launch_loss(k, a->io_dtype == MSS_BF16, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MSS_OK : MSS_ERR_HIP;
 }

@@ -17,6 +17,8 @@
 // so that the swizzles that keep the reads free of bank conflicts are applied to
 // the addresses in memory.  Rows past an operand's end lie past its buffer's
 // range and read 0.
+#include <type_traits>
+
 #include "mss.h"
 #include "vocab_gemm.hpp"
 
@@ -24,8 +26,6 @@ namespace mss {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -35,17 +35,56 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // One operand of a tile, in bytes: rows of the tile's axis from `base` on, or rows
 // of the summed one with the tile's axis contiguous.  A row is `stride` behind the
 // one before it, columns W .. 2 W - 1 are `panel` behind columns 0 .. W - 1.
-// `span` from base on may be read (of a plane).  W columns a panel.
+// `span` from base on may be read (of a plane; the planes are `plane` apart).  W
+// columns a panel.
 template <int W>
 struct Side {
   const char* base;
   int64_t plane, span, panel;
   int stride;
+  int64_t block;  // of 64 rows
 };
 
-__device__ inline int plane_of(int pair, bool second) {
-  // (0,0) (0,1) (1,0) (0,2) (1,1) (2,0), two bits each
-  return (second ? 0x184 : 0x910) >> (2 * pair) & 3;
+// The transposing LDS reads of N fragments: four summed indices at p, the next four
+// NEXT bytes on.  In assembly, with their wait: before each of the compiler's own
+// it waits for all loads to LDS, the next steps' too, as if they might touch what
+// is read (the dx product of 4096 rows, 65536 x 2560: 1440 us, 1220 without).
+template <int NEXT, int N>
+__device__ inline void read_turned(const char MSS_LDS* (&p)[N], bf16x8 (&f)[N]) {
+  u32x2 lo[N], hi[N];
+  uint32_t at[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) at[i] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p[i]));
+  static_assert(N == 1 || N == 2 || N == 4, "fragments of a wave");
+  if constexpr (N == 1) {
+    asm volatile("ds_read_b64_tr_b16 %0, %2\n\t"
+                 "ds_read_b64_tr_b16 %1, %2 offset:%3\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]) : "v"(at[0]), "i"(NEXT) : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile("ds_read_b64_tr_b16 %0, %4\n\t"
+                 "ds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+                 "ds_read_b64_tr_b16 %2, %5\n\t"
+                 "ds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1])
+                 : "v"(at[0]), "v"(at[1]), "i"(NEXT) : "memory");
+  } else {
+    asm volatile("ds_read_b64_tr_b16 %0, %8\n\t"
+                 "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %2, %9\n\t"
+                 "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %4, %10\n\t"
+                 "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+                 "ds_read_b64_tr_b16 %6, %11\n\t"
+                 "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1]), "=&v"(lo[2]), "=&v"(hi[2]), "=&v"(lo[3]),
+                   "=&v"(hi[3])
+                 : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "i"(NEXT) : "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo[i], hi[i], 0, 1, 2, 3));
 }
 
 // How ROWS rows (KC: of the tile's axis, STEP wide; else STEP rows of the summed
@@ -80,35 +119,37 @@ struct Panel {
     return swizzle(first_row() + i * kApart, static_cast<int>(threadIdx.x) % kVecs);
   }
 
-  // Where the loads are: the steps of one pair of planes after those of another.
+  // Where the loads are.
   struct Feed {
     const char* at;
-    int64_t left, step;  // bytes that may be read, and to the next step
+    int64_t left, step, jump, plane;  // bytes that may be read, to the next step, and to the next plane
     uint32_t off, odd, next;
     int k;
-    __device__ inline Feed(const Side<W>& s) {
-      const uint32_t row = static_cast<uint32_t>(first_row() * s.stride), panel = static_cast<uint32_t>(s.panel);
+    __device__ inline Feed(const Side<W>& s, int k0) {
+      const uint32_t row = static_cast<uint32_t>(first_row() / 64 * s.block + first_row() % 64 * s.stride);
+      const uint32_t panel = static_cast<uint32_t>(s.panel);
       constexpr int v = W / 8;
       off = row + column(0) / v * panel + column(0) % v * 16;
       odd = row + column(1) / v * panel + column(1) % v * 16;
-      next = static_cast<uint32_t>(kApart * s.stride);
+      next = static_cast<uint32_t>(kApart % 64 == 0 ? kApart / 64 * s.block : kApart * s.stride);
       step = KC ? s.panel : static_cast<int64_t>(STEP) * s.stride;
-    }
-    __device__ inline void start(const Side<W>& s, int plane, int k0) {
-      const int64_t from = k0 / STEP * step;
-      at = s.base + plane * s.plane + from;
+      jump = KC ? 0 : s.block - 64 * s.stride;
+      plane = s.plane;
+      const int64_t from = KC ? k0 / STEP * step : k0 / 64 * s.block;
+      at = s.base + from;
       left = s.span - from;
       k = k0;
     }
     __device__ inline void advance() {
-      at += step;
-      left -= step;
       k += STEP;
+      const int64_t by = !KC && k % 64 == 0 ? step + jump : step;
+      at += by;
+      left -= by;
     }
-    // One step's loads; a lane past the range reads 0.
-    __device__ inline void issue(int dim, char MSS_LDS* stage) const {
+    // One step's loads of a plane; a lane past the range reads 0.
+    __device__ inline void issue(int p, int dim, char MSS_LDS* stage) const {
       const int range = static_cast<int>(left < 0 ? 0 : left < kRsrcRange ? left : kRsrcRange);
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, range, kRsrcFlags);
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at) + p * plane, 0, range, kRsrcFlags);
       char MSS_LDS* lds = stage + uniform(static_cast<int>(threadIdx.x) >> 6) * 1024;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -120,7 +161,6 @@ struct Panel {
   };
 
   // The fragments of N x 32 rows from `row` on, at summed indices 16 ks .. 16 ks + 15.
-  static constexpr int kReads = KC ? 1 : 2;  // LDS reads of one
   template <int N>
   __device__ static inline void fragments(const char MSS_LDS* lds, int row, int ks, bf16x8 (&f)[N]) {
     const int lane = static_cast<int>(threadIdx.x) & 63;
@@ -131,44 +171,53 @@ struct Panel {
     } else {
       // a group of 16 lanes reads 4 rows of 32 bytes and turns them about
       const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);
+      const char MSS_LDS* p[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = row / 8 + 4 * i + 2 * (lane >> 4 & 1) + ((lane & 3) >> 1);
-        const char MSS_LDS* p = lds + k * (ROWS * 2) + swizzle(k, c) * 16 + (lane & 1) * 8 + ks * 16 * ROWS * 2;
-        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 MSS_LDS*)p);
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((s16x4 MSS_LDS*)(p + 4 * ROWS * 2));
-        f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        p[i] = lds + k * (ROWS * 2) + swizzle(k, c) * 16 + (lane & 1) * 8 + ks * 16 * ROWS * 2;
       }
+      read_turned<4 * ROWS * 2>(p, f);
     }
   }
 };
 
 // A tile of WM x WN waves, each with IM x IN products of 32 x 32: A is KC or not
-// and in panels of PA columns, B likewise, STEP of the summed axis a stage, RING
-// stages.
-template <bool KCA, int PA, bool TAIL, bool KCB, int PB, int WM, int WN, int IM, int IN, int STEP, int RING>
+// and in panels of PA columns, B likewise, PL planes of either, STEP of the summed
+// axis a stage, RING stages.
+template <int PL, bool KCA, int PA, bool TAIL, bool KCB, int PB, int WM, int WN, int IM, int IN, int STEP, int RING>
 struct Tile {
-  static constexpr int kThreads = 64 * WM * WN, kM = 32 * WM * IM, kN = 32 * WN * IN, kStep = STEP;
+  static constexpr int kThreads = 64 * WM * WN, kM = 32 * WM * IM, kN = 32 * WN * IN, kStep = STEP, kPlanes = PL;
+  static constexpr int kPA = PA, kPB = PB;
   typedef Panel<KCA, kM, STEP, PA, TAIL, kThreads> A;
   typedef Panel<KCB, kN, STEP, PB, false, kThreads> B;
   typedef f32x16 Acc[IM][IN];
   static constexpr int kIM = IM, kIN = IN;
-  static constexpr int kStage = A::kBytes + B::kBytes, kLds = RING * kStage;
+  static constexpr int kStage = PL * (A::kBytes + B::kBytes), kLds = RING * kStage;
 
   __device__ static inline int wave_m() { return uniform(static_cast<int>(threadIdx.x) >> 6) / WN * (32 * IM); }
   __device__ static inline int wave_n() { return uniform(static_cast<int>(threadIdx.x) >> 6) % WN * (32 * IN); }
 
   struct Frags {
-    bf16x8 a[IM], b[IN];
+    bf16x8 a[PL][IM], b[PL][IN];
     __device__ inline void read(const char MSS_LDS* stage, int ks) {
-      A::fragments(stage, wave_m(), ks, a);
-      B::fragments(stage + A::kBytes, wave_n(), ks, b);
+#pragma unroll
+      for (int p = 0; p < PL; ++p) {
+        A::fragments(stage + p * A::kBytes, wave_m(), ks, a[p]);
+        B::fragments(stage + PL * A::kBytes + p * B::kBytes, wave_n(), ks, b[p]);
+      }
     }
+    // The products of planes whose orders sum to less than PL, the smallest first.
     __device__ inline void multiply(Acc& acc) const {
 #pragma unroll
-      for (int j = 0; j < IN; ++j)
+      for (int order = PL - 1; order >= 0; --order)
 #pragma unroll
-        for (int i = 0; i < IM; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        for (int p = 0; p <= order; ++p)
+#pragma unroll
+          for (int j = 0; j < IN; ++j)
+#pragma unroll
+            for (int i = 0; i < IM; ++i)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p][i], b[order - p][j], acc[i][j], 0, 0, 0);
     }
   };
 
@@ -182,36 +231,29 @@ struct Tile {
     }
   }
 
-  // The sum over summed indices [k0, k1) (k0 a multiple of 64) of all pairs of planes.
+  // The sum over summed indices [k0, k1) (k0 a multiple of 64).
   // While a part's products run, the next part's fragments are read.  At a step's
   // last part they come from the next stage, whose loads had all but one of the
   // ring's steps to land; then every wave has read this stage, and the loads of the
   // step a ring on go there.
-  __device__ static inline void run(const Side<PA>& a, const Side<PB>& b, int k0, int k1, int dim, int pairs,
-                                    char MSS_LDS* lds, Acc& acc) {
-    const int steps = (k1 - k0 + STEP - 1) / STEP, total = steps * pairs;
+  __device__ static inline void run(const Side<PA>& a, const Side<PB>& b, int k0, int k1, int dim, char MSS_LDS* lds,
+                                    Acc& acc) {
+    const int total = (k1 - k0 + STEP - 1) / STEP;
     if (total <= 0) return;
-    typename A::Feed fa(a);
-    typename B::Feed fb(b);
-    int pair = 0, togo = steps;
-    fa.start(a, 0, k0);
-    fb.start(b, 0, k0);
+    typename A::Feed fa(a, k0);
+    typename B::Feed fb(b, k0);
+    int togo = total;
     auto load = [&](char MSS_LDS* stage) __attribute__((always_inline)) {
-      fa.issue(dim, stage);
-      fb.issue(dim, stage + A::kBytes);
+#pragma unroll
+      for (int p = 0; p < PL; ++p) {
+        fa.issue(p, dim, stage + p * A::kBytes);
+        fb.issue(p, dim, stage + PL * A::kBytes + p * B::kBytes);
+      }
       fa.advance();
       fb.advance();
-      if (--togo == 0) {
-        if (++pair < pairs) {
-          fa.start(a, plane_of(pair, false), k0);
-          fb.start(b, plane_of(pair, true), k0);
-        } else {  // nothing is left: loads of 0
-          fa.left = fb.left = fa.step = fb.step = 0;
-        }
-        togo = steps;
-      }
+      if (--togo == 0) fa.left = fb.left = fa.step = fb.step = fa.jump = fb.jump = 0;  // nothing is left: loads of 0
     };
-    constexpr int kLoads = A::kLoads + B::kLoads, kReads = IM * A::kReads + IN * B::kReads, kProducts = IM * IN;
+    constexpr int kLoads = PL * (A::kLoads + B::kLoads);
 #pragma unroll
     for (int r = 0; r < RING; ++r) load(lds + r * kStage);
     meet<(RING - 1) * kLoads>();
@@ -234,12 +276,6 @@ struct Tile {
             load(here);
           }
           now.multiply(acc);
-#pragma unroll
-          for (int m = 0; m < kProducts; ++m) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product,
-            __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kProducts - 1) / kProducts, 0);  // LDS reads
-            if (last) __builtin_amdgcn_sched_group_barrier(0x010, (kLoads + kProducts - 1) / kProducts, 0);
-          }
           now = next;
         }
       }
@@ -271,24 +307,26 @@ __device__ inline int acc_row(int e) { return 8 * (e >> 2) + 4 * (static_cast<in
 
 __device__ inline int live_rows(const LossArgs& a, int first) { return max(min(a.piece, *a.live - first), 0); }
 
-// The operands.
-__device__ inline Side<64> x_side(const LossArgs& a, int row, int d) {
-  const int64_t panel = a.xrows * 128, from = d / 64 * panel + static_cast<int64_t>(row) * 128;
-  return {reinterpret_cast<const char*>(a.xp) + from, a.xrows * a.dpad * 2, a.xrows * a.dpad * 2 - from, panel, 128};
+// The operands: panels of W columns, or weights as they are.
+template <int W>
+__device__ inline Side<W> panels(const uint16_t* p, int64_t rows, int64_t cols, int64_t row, int c) {
+  const int64_t panel = rows * W * 2, from = c / W * panel + row * (W * 2), all = rows * cols * 2;
+  return {reinterpret_cast<const char*>(p) + from, all, all - from, panel, W * 2, 64 * W * 2};
 }
-__device__ inline Side<64> w_side(const LossArgs& a, int v, int d) {
-  if (a.pack_w) {
-    const int64_t panel = static_cast<int64_t>(a.vocab) * 128, from = d / 64 * panel + static_cast<int64_t>(v) * 128;
-    return {reinterpret_cast<const char*>(a.wp) + from, a.vocab * a.dpad * 2, a.vocab * a.dpad * 2 - from, panel, 128};
-  }
+template <int W>
+__device__ inline Side<W> x_side(const LossArgs& a, int row, int d) {
+  return panels<W>(a.xp, a.xrows, a.dpad, row, d);
+}
+template <int W>
+__device__ inline Side<W> w_side(const LossArgs& a, int v, int d) {
+  if (a.pack_w) return panels<W>(a.wp, a.vocab, a.dpad, v, d);
   const int64_t from = (v * a.sw + d) * 2;
-  return {reinterpret_cast<const char*>(a.wp) + from, 0, ((a.vocab - 1) * a.sw + a.dim) * 2 - from, 128,
-          static_cast<int>(a.sw * 2)};
+  return {reinterpret_cast<const char*>(a.wp) + from, 0, ((a.vocab - 1) * a.sw + a.dim) * 2 - from, W * 2,
+          static_cast<int>(a.sw * 2), a.sw * 128};
 }
 __device__ inline Side<kZPanel> z_side(const LossArgs& a, int row, int v) {
-  constexpr int kRow = kZPanel * 2;
-  const int64_t panel = static_cast<int64_t>(a.piece) * kRow, from = v / kZPanel * panel + static_cast<int64_t>(row) * kRow;
-  return {reinterpret_cast<const char*>(a.dz) + from, a.piece * a.vpad * 2, a.piece * a.vpad * 2 - from, panel, kRow};
+  const int64_t from = z_index(a, row, v) * 2, all = a.piece * a.vpad * 2;
+  return {reinterpret_cast<const char*>(a.dz) + from, all, all - from, 64 * kZPanel * 2, kZPanel * 2, a.vpad * 128};
 }
 // Where the summed axis of logits ends in the rows of weights.
 __device__ inline int w_cols(const LossArgs& a) { return a.pack_w ? static_cast<int>(a.dpad) : a.dim; }
@@ -325,7 +363,7 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
   typename T::Acc acc;
   clear(acc);
   char MSS_LDS* sh = (char MSS_LDS*)lds;
-  T::run(w_side(a, v0, 0), x_side(a, first + i0, 0), 0, a.dim, w_cols(a), a.planes == 1 ? 1 : 6, sh, acc);
+  T::run(w_side<T::kPA>(a, v0, 0), x_side<T::kPB>(a, first + i0, 0), 0, a.dim, w_cols(a), sh, acc);
 
   constexpr int kWide = 32 * IM;  // entries of a wave: those that share a maximum
   const int wv = v0 + T::wave_m(), wi = i0 + T::wave_n();
@@ -450,7 +488,7 @@ __device__ inline void dx_part(const LossArgs& a, int first, int id, char* lds) 
   const int mt = (rows + T::kM - 1) / T::kM, nt = (a.dim + T::kN - 1) / T::kN;
   if (mt == 0) return;
   // tiles of one part side by side: those of an XCD read the same rows of weights
-  const int splits = dx_splits(a, mt * nt), per = (a.vocab + 63) / 64;
+  const int splits = a.cuts[first / a.piece], per = (a.vocab + 63) / 64;
   const int all = mt * nt * splits, share = (all + 7) / 8, l = (id & 7) * share + (id >> 3);
   if ((id >> 3) >= share || l >= all) return;
   const int split = l / (mt * nt);
@@ -460,7 +498,7 @@ __device__ inline void dx_part(const LossArgs& a, int first, int id, char* lds) 
   const int i0 = at.m * T::kM, d0 = at.n * T::kN;
   typename T::Acc acc;
   clear(acc);
-  T::run(z_side(a, i0, 0), w_side(a, 0, d0), k0, k1, k1, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
+  T::run(z_side(a, i0, 0), w_side<T::kPB>(a, 0, d0), k0, k1, k1, (char MSS_LDS*)lds, acc);
   float* part = a.part + static_cast<int64_t>(split) * a.piece * a.dpad;
 #pragma unroll
   for (int i = 0; i < IM; ++i)
@@ -487,7 +525,7 @@ __global__ __launch_bounds__(T::kThreads) void dx_part_kernel(LossArgs a, int fi
 // a step's worth at a time, in order, into a step of their own: a sparse panel and the rows'
 // x.
 template <typename T>
-__device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, int d0, char* lds, typename T::Acc& acc) {
+__device__ inline void add_lost(const LossArgs& a, int first, int k0, int k1, int v0, int d0, char* lds, typename T::Acc& acc) {
   constexpr int kStep = T::kStep;
   // behind the stage that it uses
   static_assert(T::kLds >= T::kStage + T::kThreads / 64 * 4 + (T::kThreads + kStep) * 8, "room for the list");
@@ -515,9 +553,9 @@ __device__ inline void add_lost(const LossArgs& a, int first, int rows, int v0, 
     T::multiply(sh, acc);
     __syncthreads();
   };
-  for (int base = 0; base < rows; base += T::kThreads) {
+  for (int base = k0; base < k1; base += T::kThreads) {
     int2 f = make_int2(-1, 0);
-    if (base + t < rows) f = a.fix[base + t];
+    if (base + t < k1) f = a.fix[base + t];
     const bool in = f.x >= v0 && f.x < v0 + T::kM;
     const uint64_t mask = __ballot(in);
     if (lane == 0) counts[wave] = __popcll(mask);
@@ -550,15 +588,18 @@ __device__ inline void dw_tile(const LossArgs& a, int first, int id, char* lds) 
   constexpr int IM = T::kIM, IN = T::kIN;
   const int rows = live_rows(a, first), lane = threadIdx.x & 63;
   if (first > 0 && rows == 0) return;
-  const At at = tile_at(id, (a.vocab + T::kM - 1) / T::kM, (a.dim + T::kN - 1) / T::kN);
+  const int mt = (a.vocab + T::kM - 1) / T::kM, nt = (a.dim + T::kN - 1) / T::kN;
+  const int split = id / a.dw_blocks;
+  const At at = tile_at(id - split * a.dw_blocks, mt, nt);
   if (at.m < 0) return;
-  const int v0 = at.m * T::kM, d0 = at.n * T::kN;
+  const int v0 = at.m * T::kM, d0 = at.n * T::kN, per = (rows + 63) / 64;
+  const int k0 = per * split / a.dw_splits * 64, k1 = min(per * (split + 1) / a.dw_splits * 64, rows);
   typename T::Acc acc;
   clear(acc);
-  T::run(z_side(a, 0, v0), x_side(a, first, d0), 0, rows, rows, a.planes == 1 ? 1 : 6, (char MSS_LDS*)lds, acc);
-  if (a.planes == 1) add_lost<T>(a, first, rows, v0, d0, lds, acc);
+  T::run(z_side(a, 0, v0), x_side<T::kPB>(a, first, d0), k0, k1, k1, (char MSS_LDS*)lds, acc);
+  if constexpr (T::kPlanes == 1) add_lost<T>(a, first, k0, k1, v0, d0, lds, acc);
   if constexpr (sizeof(IO) == 2) {
-    if (a.pieces == 1 && a.dw_vecs) {
+    if (a.dw_sum == nullptr && a.dw_vecs) {
       // bf16 through LDS, so that a lane stores 16 bytes: 32 rows of the wave at a
       // time, the 16-byte vectors of a row turned by the row
       constexpr int kRow = 4 * IN;  // vectors of a row
@@ -597,10 +638,10 @@ __device__ inline void dw_tile(const LossArgs& a, int first, int id, char* lds) 
       for (int e = 0; e < 16; ++e) {
         const int v = v0 + T::wave_m() + 32 * i + acc_row(e), d = d1 + 32 * j;
         if (v >= a.vocab || d >= a.dim) continue;
-        if (a.pieces == 1) {
+        if (a.dw_sum == nullptr) {
           io_traits<IO>::store(static_cast<IO*>(a.dweight) + v * a.sdw + d, acc[i][j][e]);
         } else {
-          float* p = a.dw_sum + v * a.dpad + d;
+          float* p = a.dw_sum + (static_cast<int64_t>(split) * a.vocab + v) * a.dpad + d;
           *p = acc[i][j][e] + (first > 0 ? *p : 0.0f);
         }
       }
@@ -624,72 +665,73 @@ __global__ __launch_bounds__(X::kThreads) void small_kernel(LossArgs a, int firs
 
 // ---------------------------------------------------------------- launches
 
-// 256 x 256 with 8 waves, and small ones with 4
-typedef Tile<true, 64, true, true, 64, 2, 4, 4, 2, 64, 2> LogitsBig;
-typedef Tile<true, 64, true, true, 64, 2, 2, 2, 1, 64, 2> LogitsSmall;
-typedef Tile<true, kZPanel, false, false, 64, 2, 4, 4, 2, 32, 5> DxBig;
-typedef Tile<true, kZPanel, false, false, 64, 2, 2, 1, 2, 32, 3> DxSmall;
-typedef Tile<false, kZPanel, false, false, 64, 4, 2, 2, 4, 64, 2> DwBig;
-typedef Tile<false, kZPanel, false, false, 64, 4, 1, 1, 2, 32, 3> DwSmall;
+// Large tiles with 8 waves, small ones with 4: bf16, then three planes of fp32.
+typedef Tile<1, true, 64, true, true, 64, 2, 4, 4, 2, 64, 2> LogitsBig;
+typedef Tile<1, true, 64, true, true, 64, 2, 2, 2, 1, 64, 2> LogitsSmall;
+typedef Tile<1, true, kZPanel, false, false, 64, 4, 2, 2, 4, 32, 5> DxBig;
+typedef Tile<1, true, kZPanel, false, false, 64, 2, 2, 1, 2, 32, 3> DxSmall;
+typedef Tile<1, false, kZPanel, false, false, 64, 4, 2, 2, 4, 64, 2> DwBig;
+typedef Tile<1, false, kZPanel, false, false, 64, 4, 1, 1, 2, 32, 3> DwSmall;
+typedef Tile<3, true, 32, false, true, 32, 4, 2, 2, 2, 32, 2> LogitsBig3;
+typedef Tile<3, true, 32, false, true, 32, 2, 2, 2, 1, 32, 2> LogitsSmall3;
+typedef Tile<3, true, kZPanel, false, false, 32, 2, 4, 2, 2, 32, 2> DxBig3;
+typedef Tile<3, true, kZPanel, false, false, 32, 2, 2, 1, 2, 32, 2> DxSmall3;
+typedef Tile<3, false, kZPanel, false, false, 32, 4, 2, 2, 2, 32, 2> DwBig3;
+typedef Tile<3, false, kZPanel, false, false, 32, 4, 1, 1, 2, 32, 2> DwSmall3;
+
+template <typename T>
+constexpr bool has_shape(TileShape t) {
+  return T::kM == t.m && T::kN == t.n;
+}
+
+static_assert(has_shape<LogitsBig>(logits_shape(false, false)) && has_shape<LogitsSmall>(logits_shape(false, true)) &&
+              has_shape<LogitsBig3>(logits_shape(true, false)) && has_shape<LogitsSmall3>(logits_shape(true, true)) &&
+              has_shape<DxBig>(dx_shape(false, false)) && has_shape<DxSmall>(dx_shape(false, true)) &&
+              has_shape<DxBig3>(dx_shape(true, false)) && has_shape<DxSmall3>(dx_shape(true, true)) &&
+              has_shape<DwBig>(dw_shape(false, false)) && has_shape<DwSmall>(dw_shape(false, true)) &&
+              has_shape<DwBig3>(dw_shape(true, false)) && has_shape<DwSmall3>(dw_shape(true, true)), "as planned");
 
 int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
 }  // namespace
 
-int loss_vocab_tile(bool small) { return small ? 64 : 128; }
-
-hipError_t launch_logits(const LossArgs& a, int first, bool io_bf16, bool keep, hipStream_t stream) {
+hipError_t launch_logits(const LossArgs& a, int first, bool keep, hipStream_t stream) {
   const int n = std::min(a.piece, a.rows - first);
-  auto go = [&](auto t) {
+  auto go = [&](auto t, auto bf16) {
     typedef decltype(t) T;
     const unsigned g = tile_blocks(tiles(a.vocab, T::kM), tiles(n, T::kN));
-    if (io_bf16) logits_kernel<true, T><<<g, T::kThreads, 0, stream>>>(a, first, keep);
-    else logits_kernel<false, T><<<g, T::kThreads, 0, stream>>>(a, first, keep);
+    logits_kernel<decltype(bf16)::value, T><<<g, T::kThreads, 0, stream>>>(a, first, keep);
   };
-  if (a.small_logits) go(LogitsSmall{});
-  else go(LogitsBig{});
+  if (a.planes == 1) {
+    if (a.small_logits) go(LogitsSmall{}, std::true_type{});
+    else go(LogitsBig{}, std::true_type{});
+  } else {
+    if (a.small_logits) go(LogitsSmall3{}, std::false_type{});
+    else go(LogitsBig3{}, std::false_type{});
+  }
   return hipGetLastError();
 }
 
-hipError_t launch_gradients(const LossArgs& a, int first, bool io_bf16, hipStream_t stream) {
+template <typename IO, typename XB, typename XS, typename WB, typename WS>
+hipError_t launch_gradients_as(const LossArgs& a, int first, hipStream_t stream) {
   const int n = std::min(a.piece, a.rows - first);
   const bool dx = a.dx != nullptr && n > 0, dw = a.dweight != nullptr;
-  // the most workgroups that any count of live rows asks for
-  auto dx_blocks = [&](auto t) {
-    typedef decltype(t) T;
-    int64_t g = 0;
-    for (int64_t mt = 1; mt <= tiles(n, T::kM); ++mt) {
-      const int64_t all = mt * tiles(a.dim, T::kN);
-      g = std::max<int64_t>(g, (all * dx_splits(a, static_cast<int>(all)) + 7) / 8 * 8);
-    }
-    return static_cast<unsigned>(g);
-  };
-  auto dw_blocks = [&](auto t) {
-    typedef decltype(t) T;
-    return tile_blocks(tiles(a.vocab, T::kM), tiles(a.dim, T::kN));
-  };
-  auto go_dx = [&](auto t) {
-    typedef decltype(t) T;
-    dx_part_kernel<T><<<dx_blocks(t), T::kThreads, 0, stream>>>(a, first);
-  };
-  auto go_dw = [&](auto t) {
-    typedef decltype(t) T;
-    if (io_bf16) dw_tile_kernel<bf16_t, T><<<dw_blocks(t), T::kThreads, 0, stream>>>(a, first);
-    else dw_tile_kernel<float, T><<<dw_blocks(t), T::kThreads, 0, stream>>>(a, first);
-  };
+  const unsigned gx = static_cast<unsigned>(dx_blocks(a, n));
+  const unsigned gw = static_cast<unsigned>(a.dw_blocks) * static_cast<unsigned>(a.dw_splits);
   if (dx && dw && a.small_dx && a.small_dw) {
-    const unsigned gx = dx_blocks(DxSmall{}), g = gx + dw_blocks(DwSmall{});
-    if (io_bf16)
-      small_kernel<bf16_t, DxSmall, DwSmall><<<g, DxSmall::kThreads, 0, stream>>>(a, first, static_cast<int>(gx));
-    else
-      small_kernel<float, DxSmall, DwSmall><<<g, DxSmall::kThreads, 0, stream>>>(a, first, static_cast<int>(gx));
+    small_kernel<IO, XS, WS><<<gx + gw, XS::kThreads, 0, stream>>>(a, first, static_cast<int>(gx));
     return hipGetLastError();
   }
-  if (dx && a.small_dx) go_dx(DxSmall{});
-  else if (dx) go_dx(DxBig{});
-  if (dw && a.small_dw) go_dw(DwSmall{});
-  else if (dw) go_dw(DwBig{});
+  if (dx && a.small_dx) dx_part_kernel<XS><<<gx, XS::kThreads, 0, stream>>>(a, first);
+  else if (dx) dx_part_kernel<XB><<<gx, XB::kThreads, 0, stream>>>(a, first);
+  if (dw && a.small_dw) dw_tile_kernel<IO, WS><<<gw, WS::kThreads, 0, stream>>>(a, first);
+  else if (dw) dw_tile_kernel<IO, WB><<<gw, WB::kThreads, 0, stream>>>(a, first);
   return hipGetLastError();
+}
+
+hipError_t launch_gradients(const LossArgs& a, int first, hipStream_t stream) {
+  return a.planes == 1 ? launch_gradients_as<bf16_t, DxBig, DxSmall, DwBig, DwSmall>(a, first, stream)
+                       : launch_gradients_as<float, DxBig3, DxSmall3, DwBig3, DwSmall3>(a, first, stream);
 }
 
 }  // namespace mss

@@ -34,6 +34,15 @@ __device__ inline int id_at(const LossArgs& a, int64_t row, int k) {
   return id >= 0 && id < a.vocab ? static_cast<int>(id) : -1;
 }
 
+// The parts of each piece's dx product: one wave's work.
+__device__ inline void set_cuts(const LossArgs& a, int live) {
+  if (a.dx == nullptr) return;
+  for (int p = 0; p < a.pieces; ++p) {
+    const int s = dx_cuts(a, min(a.piece, live - p * a.piece));
+    if ((threadIdx.x & 63) == 0) a.cuts[p] = s;
+  }
+}
+
 // Whether a row counts, and the shares of its entries: one wave's work.
 __device__ inline bool row_entries(const LossArgs& a, int row, int lane) {
   bool any = false;
@@ -85,6 +94,12 @@ __global__ __launch_bounds__(1024) void few_rows_kernel(LossArgs a) {
     if (lane == 0) counts[row] = any ? 1 : 0;
   }
   __syncthreads();
+  if (threadIdx.x >= 960) {  // the last wave
+    int live = 0;
+    for (int r = 0; r < a.rows; ++r) live += counts[r];
+    set_cuts(a, live);
+    return;
+  }
   const int row = threadIdx.x;
   if (row > a.rows) return;
   int at = 0;
@@ -132,6 +147,7 @@ __global__ __launch_bounds__(1024) void place_kernel(LossArgs a) {
       }
   }
   if (threadIdx.x == 0) *a.live = base;
+  if (threadIdx.x < 64) set_cuts(a, base);
 }
 
 // 8 values as bf16, or as three bf16 planes whose sums they are (exact: 3 x 8 bits).
@@ -148,6 +164,10 @@ __device__ inline void to_planes(float (&v)[8], uint16_t* p, int64_t plane, int 
   }
 }
 
+// Columns of x's and weight's panels.
+template <typename IO>
+constexpr int kPanel = sizeof(IO) == 2 ? 64 : 32;
+
 constexpr int kMaxWords = (1 << 22) / 64 / 32;  // of the largest vocabulary's tiles
 
 // One workgroup a row that counts: its x as an operand, its ids, and the tiles of
@@ -160,10 +180,11 @@ __global__ __launch_bounds__(256) void pack_kernel(LossArgs a, int tile_shift) {
   if (j >= (live + 63) / 64 * 64) return;
   const int row = j < live ? a.row_of[j] : 0;
   const IO* x = static_cast<const IO*>(a.x) + row * a.sx;
+  constexpr int w = kPanel<IO>;
   for (int c = threadIdx.x * 8; c < a.dpad; c += 2048) {
     float v[8];
     load_part<IO, 8>(x + c, j < live ? a.dim - c : 0, v);
-    to_planes(v, a.xp + (c / 64 * a.xrows + j) * 64 + c % 64, a.xrows * a.dpad, a.planes);
+    to_planes(v, a.xp + (c / w * a.xrows + j) * w + c % w, a.xrows * a.dpad, a.planes);
   }
   if (j >= live) return;
   for (int i = threadIdx.x; i < a.where_words; i += 256) where[i] = 0;
@@ -183,10 +204,11 @@ __global__ __launch_bounds__(256) void pack_weight_kernel(LossArgs a) {
   const int v = blockIdx.x * 8 + (threadIdx.x >> 3 & 7);
   if (v >= a.vocab) return;
   const IO* w = static_cast<const IO*>(a.weight) + v * a.sw;
+  constexpr int p = kPanel<IO>;
   for (int c = (threadIdx.x >> 6) * 64 + (threadIdx.x & 7) * 8; c < a.dpad; c += 256) {
     float q[8];
     load_part<IO, 8>(w + c, a.dim - c, q);
-    to_planes(q, a.wp + (static_cast<int64_t>(c / 64) * a.vocab + v) * 64 + c % 64, a.vocab * a.dpad, a.planes);
+    to_planes(q, a.wp + (static_cast<int64_t>(c / p) * a.vocab + v) * p + c % p, a.vocab * a.dpad, a.planes);
   }
 }
 
@@ -357,7 +379,7 @@ template <typename IO>
 __global__ __launch_bounds__(256) void dx_kernel(LossArgs a, int first) {
   const int row = blockIdx.x, j = a.place[row];
   if (j < 0 ? first != 0 : j < first || j >= first + a.piece) return;
-  const int splits = dx_splits(a, dx_tiles(a, min(a.piece, *a.live - first)));
+  const int splits = a.cuts[first / a.piece];
   IO* out = static_cast<IO*>(a.dx) + row * a.sdx;
   const float* part = a.part + static_cast<int64_t>(j < 0 ? 0 : j - first) * a.dpad;
   const int64_t next = static_cast<int64_t>(a.piece) * a.dpad;
@@ -391,7 +413,7 @@ __global__ __launch_bounds__(256) void dx_few_kernel(LossArgs a, int first) {
   __shared__ float4 meet[3][64];
   const int row = blockIdx.x, j = a.place[row], lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (j < 0 ? first != 0 : j < first || j >= first + a.piece) return;
-  const int splits = dx_splits(a, dx_tiles(a, min(a.piece, *a.live - first)));
+  const int splits = a.cuts[first / a.piece];
   const int c = blockIdx.y * 256 + lane * 4;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (j >= 0 && c < a.dim) {
@@ -426,11 +448,22 @@ __global__ __launch_bounds__(256) void dx_few_kernel(LossArgs a, int first) {
   store_part<IO, 4>(static_cast<IO*>(a.dx) + row * a.sdx + c, a.dim - c, out);
 }
 
+// dweight from its sums.
 template <typename IO>
 __global__ __launch_bounds__(256) void dw_kernel(LossArgs a) {
-  const int64_t v = blockIdx.x;
-  for (int c = threadIdx.x; c < a.dim; c += 256)
-    io_traits<IO>::store(static_cast<IO*>(a.dweight) + v * a.sdw + c, a.dw_sum[v * a.dpad + c]);
+  const int64_t v = blockIdx.x, next = a.vocab * a.dpad;
+  for (int c = threadIdx.x * 4; c < a.dim; c += 1024) {
+    float s[4] = {};
+#pragma unroll 4
+    for (int q = 0; q < a.dw_splits; ++q) {
+      const float4 p = *reinterpret_cast<const float4*>(a.dw_sum + q * next + v * a.dpad + c);
+      s[0] += p.x;
+      s[1] += p.y;
+      s[2] += p.z;
+      s[3] += p.w;
+    }
+    store_part<IO, 4>(static_cast<IO*>(a.dweight) + v * a.sdw + c, a.dim - c, s);
+  }
 }
 
 template <typename IO>
@@ -444,6 +477,11 @@ template <typename IO>
 hipError_t launch_io(const LossArgs& a, hipStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.rows);
   const bool grad = a.dx != nullptr || a.dweight != nullptr;
+  auto end = [&](hipError_t e) {
+    if (e != hipSuccess || a.dw_sum == nullptr) return e;
+    dw_kernel<IO><<<static_cast<unsigned>(a.vocab), 256, 0, s>>>(a);
+    return hipGetLastError();
+  };
   if (a.rows <= kFewRows) {
     few_rows_kernel<<<1, 1024, 0, s>>>(a);
   } else {
@@ -452,15 +490,15 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
   }
   if (rows == 0) {  // (dweight and the total are 0)
     if (a.total != nullptr) total_kernel<<<1, 1024, 0, s>>>(a);
-    return launch_gradients(a, 0, sizeof(IO) == 2, s);
+    return end(launch_gradients(a, 0, s));
   }
-  const int shift = loss_vocab_tile(a.small_logits) == 64 ? 6 : 7;
+  const int shift = a.vocab_tile == 64 ? 6 : 7;
   pack_kernel<IO><<<static_cast<unsigned>(a.xrows), 256, 0, s>>>(a, shift);
   if (a.pack_w) pack_weight_kernel<IO><<<static_cast<unsigned>(a.vocab + 7) / 8, 256, 0, s>>>(a);
   for (int p = 0; p < a.pieces; ++p) {
     const int first = p * a.piece;
     const unsigned n = static_cast<unsigned>(std::min(a.piece, a.rows - first));
-    hipError_t e = launch_logits(a, first, sizeof(IO) == 2, grad, s);
+    hipError_t e = launch_logits(a, first, grad, s);
     if (e != hipSuccess) return e;
     row_kernel<<<n, 256, 0, s>>>(a, first, sizeof(IO) == 2, grad);
     if (grad) {
@@ -469,16 +507,14 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
       const unsigned panels = std::clamp(all * groups / 2048, 1u, 32u);
       dz_kernel<IO><<<dim3(groups, (all + panels - 1) / panels), 256, 0, s>>>(a, first, static_cast<int>(panels), shift);
     }
-    if (grad && (e = launch_gradients(a, first, sizeof(IO) == 2, s)) != hipSuccess) return e;
+    if (grad && (e = launch_gradients(a, first, s)) != hipSuccess) return e;
     if (a.dx != nullptr) {
       if (a.small_dx) dx_few_kernel<IO><<<dim3(rows, static_cast<unsigned>(a.dim + 255) / 256), 256, 0, s>>>(a, first);
       else dx_kernel<IO><<<rows, 256, 0, s>>>(a, first);
     }
   }
   if (a.total != nullptr) total_kernel<<<1, 1024, 0, s>>>(a);
-  if (a.dweight != nullptr && a.pieces > 1)
-    dw_kernel<IO><<<static_cast<unsigned>(a.vocab), 256, 0, s>>>(a);
-  return hipGetLastError();
+  return end(hipGetLastError());
 }
 
 }  // namespace
