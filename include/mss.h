@@ -734,7 +734,7 @@ typedef struct mss_linear_loss_args {
     uint32_t struct_size;
     int32_t io_dtype;            /* mss_dtype of x, weight, dx and dweight               */
     int64_t rows;                /* 0..2^24                                              */
-    int64_t dim;                 /* 1..32768                                             */
+    int64_t dim;                 /* 1..32768; rows dim and vocab dim at most 2^36        */
     int64_t vocab;               /* 1..2^22                                              */
     int64_t entries;             /* 1..MSS_MAX_LOSS_ENTRIES; 1 without teacher           */
     const void *x;               /* [r,d], unit stride in d                              */
@@ -746,8 +746,9 @@ typedef struct mss_linear_loss_args {
     const void *teacher;         /* [r,k] logits; NULL: cross entropy                    */
     int64_t teacher_stride[2];
     int32_t teacher_dtype;       /* mss_dtype of teacher                                 */
-    float logit_scale;           /* finite                                               */
-    float temperature;           /* finite, > 0; 1 without teacher                       */
+    float logit_scale;           /* finite, as are its product and quotient with ...     */
+    float temperature;           /* ... > 0, with a finite square and inverse; 1 without */
+                                 /* teacher                                              */
     int32_t reserved0;           /* must be 0                                            */
     const float *row_weight;     /* [r] c, fp32 contiguous; NULL: 1 / (rows that count)  */
     float *loss;                 /* [r] fp32 contiguous                                  */

@@ -168,8 +168,13 @@ mss_status check_loss_shape(const mss_linear_loss_args* a) {
     return MSS_ERR_UNSUPPORTED_DTYPE;
   if (a->rows < 0 || a->rows > (int64_t{1} << 22) || a->dim < 1 || a->dim > kMaxNormDim || a->vocab < 1 ||
       a->vocab > (int64_t{1} << 22) || a->entries < 1 || a->entries > MSS_MAX_LOSS_ENTRIES ||
-      (a->teacher == nullptr && (a->entries != 1 || a->temperature != 1.0f)) || !std::isfinite(a->logit_scale) ||
-      !std::isfinite(a->temperature) || !(a->temperature > 0.0f))
+      (a->teacher == nullptr && (a->entries != 1 || a->temperature != 1.0f)))
+    return MSS_ERR_BAD_SHAPE;
+  // (workgroups of the products and of what they leave, 2^23 of 8192 elements)
+  if (a->vocab * a->dim > (int64_t{1} << 36) || a->rows * a->dim > (int64_t{1} << 36)) return MSS_ERR_BAD_SHAPE;
+  const float s = a->logit_scale, t = a->temperature;
+  if (!(t > 0.0f) || !std::isfinite(s) || !std::isfinite(t * t) || !std::isfinite(1.0f / t) || !std::isfinite(s / t) ||
+      !std::isfinite(s * t))
     return MSS_ERR_BAD_SHAPE;
   return MSS_OK;
 }

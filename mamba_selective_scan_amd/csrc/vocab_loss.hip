@@ -509,7 +509,8 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
     }
     if (grad && (e = launch_gradients(a, first, s)) != hipSuccess) return e;
     if (a.dx != nullptr) {
-      if (a.small_dx) dx_few_kernel<IO><<<dim3(rows, static_cast<unsigned>(a.dim + 255) / 256), 256, 0, s>>>(a, first);
+      const unsigned cols = static_cast<unsigned>(a.dim + 255) / 256;
+      if (a.small_dx && rows <= (1u << 20) / cols) dx_few_kernel<IO><<<dim3(rows, cols), 256, 0, s>>>(a, first);
       else dx_kernel<IO><<<rows, 256, 0, s>>>(a, first);
     }
   }

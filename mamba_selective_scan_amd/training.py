@@ -25,6 +25,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .heads import (_Tensor, _current_device, _current_stream, _give_workspace, _gpu, _io, _launch, _like, _out,
@@ -137,13 +138,19 @@ def _needed(t, name):
     return t
 
 
+def _flat(t, rows=None):
+    """The rows of t's last dimension, with unit stride."""
+    if t is None:
+        return None
+    t = t.reshape((t.numel() // max(t.shape[-1], 1) if rows is None else rows, t.shape[-1]))
+    return t if t.shape[1] == 1 or t.stride(1) == 1 else t.contiguous()
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, eps):
-        wide, rest = x.shape, None
-        x = x.reshape(-1, wide[-1])
-        if residual is not None:
-            residual = residual.reshape(x.shape)
+        wide = x.shape
+        x, residual = _flat(x), _flat(residual)
         y, mean, rstd, *rest = layer_norm_fwd(x, weight, bias, residual=residual, eps=eps)
         r = rest[0] if rest else x
         ctx.save_for_backward(r, weight, mean, rstd)
@@ -151,15 +158,18 @@ class _LayerNorm(torch.autograd.Function):
         return (y.view(wide), r.view(wide)) if rest else y.view(wide)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dr=None):
         r, weight, mean, rstd = ctx.saved_tensors
-        flat = [None if t is None else t.reshape(-1, ctx.wide[-1]) for t in (dy, dr)]
-        flat = [t if t is None or t.shape[1] == 1 or t.stride(1) == 1 else t.contiguous() for t in flat]
         want = ctx.needs_input_grad
-        g = layer_norm_bwd(flat[0], r, weight, mean, rstd, dr=flat[1], bias=ctx.bias and want[2],
+        g = layer_norm_bwd(_flat(dy), r, weight, mean, rstd, dr=_flat(dr), bias=ctx.bias and want[2],
                            params=want[1] or (ctx.bias and want[2]))
+        # (where both gradients are one, it is handed over as one tensor: two views of
+        # it would each become a leaf's .grad, and sums into one would reach the other)
         dx = g["x"].view(ctx.wide)
-        dres = (g["residual"] if "residual" in g else g["x"]).view(ctx.wide) if ctx.pair and want[3] else None
+        dres = None
+        if ctx.pair and want[3]:
+            dres = dx if g.get("residual", g["x"]) is g["x"] else g["residual"].view(ctx.wide)
         return (dx if want[0] else None, g.get("weight") if want[1] else None,
                 g.get("bias") if want[2] else None, dres, None)
 
@@ -283,12 +293,12 @@ class _LinearLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, ids, teacher, row_weight, scale, tau):
         wide = x.shape
-        flat = x.reshape(-1, wide[-1])
+        flat = _flat(x)
         ids = ids.reshape(-1) if teacher is None else ids.reshape(flat.shape[0], -1)
         if teacher is not None:
             teacher = teacher.reshape(ids.shape)
         if row_weight is not None:
-            row_weight = row_weight.reshape(-1)
+            row_weight = row_weight.reshape(-1).contiguous()
         want = ctx.needs_input_grad[:2]
         total = torch.empty((), dtype=torch.float32, device=x.device)
         _, _, dx, dw = _loss(flat, weight, ids, teacher, row_weight, scale, tau, want, (None, None), None, total)
@@ -296,6 +306,7 @@ class _LinearLoss(torch.autograd.Function):
         return total
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         g = g.float().contiguous()
         return (*(None if t is None else _scaled(t, g) for t in ctx.saved_tensors), None, None, None, None, None)

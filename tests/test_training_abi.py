@@ -84,7 +84,11 @@ BAD = [
     ("loss", dict(entries=0), "MSS_ERR_BAD_SHAPE"), ("loss", dict(entries=1025), "MSS_ERR_BAD_SHAPE"),
     ("loss", dict(teacher=0), "MSS_ERR_BAD_SHAPE"), ("loss", dict(teacher=0, entries=1), "MSS_ERR_BAD_SHAPE"),
     ("loss", dict(temperature=0.0), "MSS_ERR_BAD_SHAPE"), ("loss", dict(temperature=float("inf")), "MSS_ERR_BAD_SHAPE"),
-    ("loss", dict(logit_scale=float("nan")), "MSS_ERR_BAD_SHAPE"),
+    ("loss", dict(logit_scale=float("nan")), "MSS_ERR_BAD_SHAPE"), ("loss", dict(temperature=float("nan")), "MSS_ERR_BAD_SHAPE"),
+    ("loss", dict(temperature=1e-39), "MSS_ERR_BAD_SHAPE"), ("loss", dict(temperature=1e20), "MSS_ERR_BAD_SHAPE"),
+    ("loss", dict(logit_scale=1e30, temperature=1e-10), "MSS_ERR_BAD_SHAPE"),
+    ("loss", dict(logit_scale=1e30, temperature=1e10), "MSS_ERR_BAD_SHAPE"),
+    ("loss", dict(vocab=1 << 22, dim=16400), "MSS_ERR_BAD_SHAPE"), ("loss", dict(rows=1 << 22, dim=16400), "MSS_ERR_BAD_SHAPE"),
     ("loss", dict(x=0), "MSS_ERR_NULL_POINTER"), ("loss", dict(weight=0), "MSS_ERR_NULL_POINTER"),
     ("loss", dict(ids=0), "MSS_ERR_NULL_POINTER"), ("loss", dict(loss=0), "MSS_ERR_NULL_POINTER"),
     ("loss", dict(x_stride=-1), "MSS_ERR_BAD_STRIDE"), ("loss", dict(ids_stride=(-4, 1)), "MSS_ERR_BAD_STRIDE"),

@@ -184,6 +184,40 @@ def test_layer_norm_autograd(with_res):
     assert x.grad.shape == x.shape and x.grad.float().abs().max() < 1
 
 
+@gpu
+def test_layer_norm_gradients_of_leaves_are_their_own():
+    note("layer_norm: x and residual of one dtype, gradients added up over two passes")
+    g = gen(9)
+    leaves = [randn(g, 7, 96).requires_grad_() for _ in range(2)]
+    w, b = randn(g, 96).requires_grad_(), randn(g, 96).requires_grad_()
+    dy, dr = randn(g, 7, 96), randn(g, 7, 96)
+
+    def once():
+        y, r = mss.layer_norm(leaves[0], w, b, leaves[1])
+        return torch.autograd.grad((y, r), (*leaves, w, b), (dy, dr))
+
+    want = [2 * t for t in once()]
+    for _ in range(2):
+        y, r = mss.layer_norm(leaves[0], w, b, leaves[1])
+        torch.autograd.backward((y, r), (dy, dr))
+    assert leaves[0].grad.data_ptr() != leaves[1].grad.data_ptr()
+    assert all(torch.equal(t.grad, q) for t, q in zip((*leaves, w, b), want))
+    # x itself as the residual: its gradient is the sum of both
+    y, r = mss.layer_norm(leaves[0], w, b, leaves[0])
+    both, = torch.autograd.grad((y, r), leaves[0], (dy, dr))
+    assert both.shape == (7, 96) and both.isfinite().all()
+    # only one of the outputs used, and gradients that are expanded or transposed views
+    y, r = mss.layer_norm(leaves[0], w, None, leaves[1])
+    one, = torch.autograd.grad(r.sum(), leaves[1])
+    assert torch.equal(one, torch.ones_like(one))
+    x = randn(g, 96, 7).t().requires_grad_()  # columns not adjacent
+    dx, = torch.autograd.grad(mss.layer_norm(x, w, b), x, randn(g, 96, 7).t())
+    assert dx.shape == x.shape
+    with pytest.raises(RuntimeError):  # (no second derivative)
+        dx, = torch.autograd.grad(mss.layer_norm(x, w, b).sum(), x, create_graph=True)
+        torch.autograd.grad(dx.sum(), x)
+
+
 # ---------------------------------------------------------------- losses
 
 def loss_case(rows, dim, vocab, dtype, seed=0, ignored=0.0, spread=6.0):
@@ -433,6 +467,88 @@ def test_losses_of_no_rows(dtype):
     assert mss.linear_cross_entropy(x[:0], w, ids[:0]).item() == 0
     tops, teacher = top_case(4, 300, 3)
     assert not mss.linear_distillation_grad(x[:0], w, tops[:0], teacher[:0])[3].any()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,dim,vocab", [(2300, 64, 300), (1500, 72, 120), (3000, 8, 5), (130, 1032, 64), (700, 2051, 90)])
+def test_products_cut_along_their_sums(rows, dim, vocab, dtype):
+    """Few tiles: dweight's sum over the rows, and dx's over the vocabulary, in parts."""
+    note(f"cross entropy of few tiles {rows} x {dim} x {vocab} {dtype}")
+    x, w, ids = loss_case(rows, dim, vocab, dtype, ignored=0.3)
+    check_loss(x, w, ids, row_weight=torch.rand(rows, generator=gen(2)).to(DEV))
+
+
+@gpu
+def test_the_gradients_of_a_loss_are_taken_once_and_kept():
+    note("losses: a second backward pass, a scaled total, a second derivative")
+    x, w, ids = loss_case(60, 64, 300, BF16)
+    x.requires_grad_()
+    total = mss.linear_cross_entropy(x, w, ids)
+    a, = torch.autograd.grad(total, x, retain_graph=True)
+    b, = torch.autograd.grad(total * 4, x)
+    assert torch.equal(a * 4, b)
+    assert torch.equal(a, mss.linear_cross_entropy_grad(x.detach(), w, ids)[2])
+    wide = x.detach().t().contiguous().t().requires_grad_()  # columns not adjacent
+    c, = torch.autograd.grad(mss.linear_cross_entropy(wide, w, ids), wide)
+    assert torch.equal(a, c)
+    with pytest.raises(RuntimeError):  # (no second derivative)
+        d, = torch.autograd.grad(mss.linear_cross_entropy(x, w, ids), x, create_graph=True)
+        torch.autograd.grad(d.float().sum(), x)
+
+
+@gpu
+def test_two_losses_at_once_on_two_streams():
+    note("losses on two streams")
+    cases = [loss_case(400, 256, 5000, BF16, seed=s) for s in (1, 2)]
+    want = [mss.linear_cross_entropy_grad(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for turn in range(5):
+        got = []
+        for c, s in zip(cases, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(mss.linear_cross_entropy_grad(*c))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for a, b in zip(got, want) for p, q in zip(a, b))
+
+
+@gpu
+def test_what_lies_around_the_outputs_and_the_workspace():
+    """Outputs and a workspace of exactly the size asked for in the middle of larger
+    buffers: nothing outside them changes, whatever the workspace held before."""
+    note("losses between guards")
+    import ctypes
+    from mamba_selective_scan_amd import _lib, heads
+    for dtype, (rows, dim, vocab) in ((BF16, (150, 136, 777)), (F32, (150, 100, 777)), (BF16, (40, 64, 3001))):
+        x, w, ids = loss_case(rows, dim, vocab, dtype, ignored=0.2)
+        sizes = []
+        real = heads._give_workspace
+        want = mss.linear_cross_entropy_grad(x, w, ids)
+        import mamba_selective_scan_amd.training as training
+        def spy(a, need, workspace, device):
+            sizes.append(need)
+            return real(a, need, workspace, device)
+        training._give_workspace = spy
+        try:
+            mss.linear_cross_entropy_grad(x, w, ids)
+        finally:
+            training._give_workspace = real
+        need = sizes[0]
+        for fill in (0xff, 0x7f, 0):
+            big = torch.full((need + 2048,), fill, dtype=torch.uint8, device=DEV)
+            dx = torch.full((rows + 4, dim), 3.0, dtype=dtype, device=DEV)
+            dw = torch.full((vocab + 4, dim), 3.0, dtype=dtype, device=DEV)
+            got = mss.linear_cross_entropy_grad(x, w, ids, dx=dx[2:-2], dweight=dw[2:-2],
+                                                workspace=big[1024:1024 + need])
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, want)), (dtype, fill)
+            assert (big[:1024] == fill).all() and (big[1024 + need:] == fill).all()
+            for t in (dx, dw):
+                assert (t[:2] == 3).all() and (t[-2:] == 3).all()
+        with pytest.raises(mss.MssError, match="WORKSPACE"):
+            mss.linear_cross_entropy_grad(x, w, ids, workspace=big[:need - 1])
 
 
 @gpu
