@@ -370,16 +370,14 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
   if (wv >= a.vocab) return;
   const int tile = wv / kWide;
   char MSS_LDS* mine = sh + uniform(static_cast<int>(threadIdx.x) >> 6) * (kWide * 32 * 4);
-  float scale = a.scale;
-  if (wv + kWide > a.vocab || scale < 0.0f) {  // (from here on the scale only has to keep the order)
+  if (wv + kWide > a.vocab || a.scale != 1.0f) {
 #pragma unroll
     for (int m = 0; m < IM; ++m)
 #pragma unroll
       for (int j = 0; j < IN; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          acc[m][j][e] = wv + 32 * m + acc_row(e) < a.vocab ? acc[m][j][e] * scale : -INFINITY;
-    scale = 1.0f;
+          acc[m][j][e] = wv + 32 * m + acc_row(e) < a.vocab ? acc[m][j][e] * a.scale : -INFINITY;
   }
 #pragma unroll
   for (int j = 0; j < IN; ++j) {
@@ -389,7 +387,7 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
     for (int m = 0; m < IM; ++m)
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[m][j][e]);
-    top = ceilf(fmaxf(top, __shfl_xor(top, 32, 64)) * scale);
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
     const float from = top == -INFINITY ? 0.0f : top;
     // The rows' logits in LDS, [32 rows][kWide] with the 16-byte vectors of a row
     // turned by the row; this wave's own.
@@ -399,10 +397,8 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int c = 8 * m + 2 * q + (lane >> 5), r = lane & 31;
-          f32x4 z;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[e] = acc[m][j][4 * q + e] * scale;
-          *reinterpret_cast<f32x4 MSS_LDS*>(mine + (r * (kWide / 4) + (c ^ (r & (kWide / 4 - 1)))) * 16) = z;
+          *reinterpret_cast<f32x4 MSS_LDS*>(mine + (r * (kWide / 4) + (c ^ (r & (kWide / 4 - 1)))) * 16) =
+              f32x4{acc[m][j][4 * q], acc[m][j][4 * q + 1], acc[m][j][4 * q + 2], acc[m][j][4 * q + 3]};
         }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
@@ -438,12 +434,12 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    // distances from the ceiling, in place, and the sum
+    // distances from the maximum, in place, and the sum
 #pragma unroll
     for (int m = 0; m < IM; ++m)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float d = fmaf(acc[m][j][e], scale, -from);
+        const float d = acc[m][j][e] - from;
         acc[m][j][e] = d;
         sum += fast_exp2(d * kLog2e);
       }

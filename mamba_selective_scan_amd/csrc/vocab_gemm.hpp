@@ -7,7 +7,7 @@
 
 namespace mss {
 
-// bf16 losses keep a logit as its distance below its tile's ceiling in 16 bits:
+// bf16 losses keep a logit as its distance below its tile's maximum in 16 bits:
 // steps of 2^-10, so that a probability is off by at most 2^-11, an eighth of
 // what its rounding to bf16 takes; one 64 below (1e-28 of its tile's largest) is 0.
 constexpr float kCodeSteps = 1024.0f;

@@ -212,9 +212,9 @@ __global__ __launch_bounds__(256) void pack_weight_kernel(LossArgs a) {
   }
 }
 
-// A row's sum of e^z from its tiles, as sum e^from with an integer `from`, so that
-// a logit's distance from it keeps its last bits.  Every thread of the workgroup
-// takes part and has it.
+// A row's sum of e^z from its tiles, as sum e^from with its largest logit `from`: the
+// sum of a row that is sure of one entry is 1 and the others, to the last bit.
+// Every thread of the workgroup takes part and has it.
 struct RowSum {
   float from, sum;
 };
