@@ -138,8 +138,10 @@ hipError_t launch_fwd(const LayerNormArgs& a, hipStream_t stream) {
   const unsigned by4 = static_cast<unsigned>((a.rows + 3) / 4), by1 = static_cast<unsigned>(a.rows);
   if (d <= 512) fwd_kernel<IO, RES, 64, 1><<<by4, 256, 0, stream>>>(a);
   else if (d <= 1024) fwd_kernel<IO, RES, 64, 2><<<by4, 256, 0, stream>>>(a);
+  else if (d <= 1536) fwd_kernel<IO, RES, 64, 3><<<by4, 256, 0, stream>>>(a);
   else if (d <= 2048) fwd_kernel<IO, RES, 64, 4><<<by4, 256, 0, stream>>>(a);
   else if (d <= 4096) fwd_kernel<IO, RES, 256, 2><<<by1, 256, 0, stream>>>(a);
+  else if (d <= 6144) fwd_kernel<IO, RES, 256, 3><<<by1, 256, 0, stream>>>(a);
   else if (d <= 8192) fwd_kernel<IO, RES, 256, 4><<<by1, 256, 0, stream>>>(a);
   else if (d <= 16384) fwd_kernel<IO, RES, 1024, 2><<<by1, 1024, 0, stream>>>(a);
   else fwd_kernel<IO, RES, 1024, 4><<<by1, 1024, 0, stream>>>(a);
@@ -147,8 +149,9 @@ hipError_t launch_fwd(const LayerNormArgs& a, hipStream_t stream) {
 }
 
 // One workgroup walks rows blockIdx.x * (rows a pass), ... and keeps the sums of
-// its columns in registers.  LEAN: a row is read again (from the caches) for its
-// output instead of being kept, which leaves the registers to the sums.
+// its columns in registers.  LEAN, for the longest rows: a row is read again (from
+// the caches) for its output instead of being kept, and the sums are another
+// kernel's: both do not fit the registers (4096 rows of 32768: 1590 us with them).
 template <typename IO, typename RES, int TPR, int K, bool LEAN>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void bwd_kernel(LayerNormBwdArgs a) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR;
@@ -183,8 +186,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void bwd_kernel(LayerNormBwd
         const float g = dy[o][i] * w[i];
         s1 += g;
         s2 = fmaf(g, h[o][i], s2);
-        dw[k][i] = fmaf(dy[o][i], h[o][i], dw[k][i]);
-        db[k][i] += dy[o][i];
+        if (!LEAN) {
+          dw[k][i] = fmaf(dy[o][i], h[o][i], dw[k][i]);
+          db[k][i] += dy[o][i];
+        }
       }
     }
     if (a.dx == nullptr && a.dres == nullptr) continue;
@@ -206,7 +211,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void bwd_kernel(LayerNormBwd
       if (a.dres != nullptr) store_part<RES, kV>(static_cast<RES*>(a.dres) + row * a.sdres + c, a.dim - c, q);
     }
   }
-  if (a.dweight == nullptr && a.dbias == nullptr) return;
+  if (LEAN || (a.dweight == nullptr && a.dbias == nullptr)) return;
   if constexpr (kRows > 1) {
     // the waves' sums meet in a fixed order
     __shared__ float meet[kRows][K * 64 * kV];
@@ -242,6 +247,29 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void bwd_kernel(LayerNormBwd
   }
 }
 
+// The sums of 2048 columns over every gridDim.x-th row, for rows too long for
+// bwd_kernel to hold them.
+template <typename IO, typename RES>
+__global__ __launch_bounds__(256) void bwd_cols_kernel(LayerNormBwdArgs a) {
+  const int c = (blockIdx.y * 256 + threadIdx.x) * kV;
+  float dw[kV] = {}, db[kV] = {};
+#pragma unroll 4
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float y[kV], x[kV];
+    load_part<IO, kV>(static_cast<const IO*>(a.dy) + row * a.sdy + c, a.dim - c, y);
+    load_part<RES, kV>(static_cast<const RES*>(a.r) + row * a.sr + c, a.dim - c, x);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      dw[i] = fmaf(y[i], (x[i] - mean) * rstd, dw[i]);
+      db[i] += y[i];
+    }
+  }
+  float* sums = a.sums + static_cast<int64_t>(blockIdx.x) * a.dim + c;
+  store_part<float, kV>(sums, a.dim - c, dw);
+  store_part<float, kV>(sums + static_cast<int64_t>(gridDim.x) * a.dim, a.dim - c, db);
+}
+
 // The workgroups' sums of 32 columns: 32 threads a column, each over every 32nd
 // part, which meet in a fixed order.
 __global__ __launch_bounds__(1024) void bwd_sum_kernel(LayerNormBwdArgs a) {
@@ -271,9 +299,17 @@ hipError_t launch_bwd(const LayerNormBwdArgs& a, hipStream_t stream) {
   else if (d <= 1024) bwd_kernel<IO, RES, 64, 2, false><<<g, 256, 0, stream>>>(a);
   else if (d <= 2048) bwd_kernel<IO, RES, 256, 1, false><<<g, 256, 0, stream>>>(a);
   else if (d <= 4096) bwd_kernel<IO, RES, 256, 2, false><<<g, 256, 0, stream>>>(a);
+  else if (d <= 6144) bwd_kernel<IO, RES, 256, 3, false><<<g, 256, 0, stream>>>(a);
   else if (d <= 8192) bwd_kernel<IO, RES, 256, 4, false><<<g, 256, 0, stream>>>(a);
   else if (d <= 16384) bwd_kernel<IO, RES, 1024, 2, false><<<g, 1024, 0, stream>>>(a);
-  else bwd_kernel<IO, RES, 1024, 4, true><<<g, 1024, 0, stream>>>(a);
+  else {
+    if (a.dx != nullptr || a.dres != nullptr) {
+      const unsigned rows = static_cast<unsigned>(a.rows < 1024 ? a.rows : 1024);
+      bwd_kernel<IO, RES, 1024, 4, true><<<rows, 1024, 0, stream>>>(a);
+    }
+    if (a.dweight != nullptr || a.dbias != nullptr)
+      bwd_cols_kernel<IO, RES><<<dim3(g, static_cast<unsigned>((d + 2047) / 2048)), 256, 0, stream>>>(a);
+  }
   if (a.dweight != nullptr || a.dbias != nullptr)
     bwd_sum_kernel<<<dim3(static_cast<unsigned>((d + 31) / 32), 2), 1024, 0, stream>>>(a);
   return hipGetLastError();
@@ -281,9 +317,18 @@ hipError_t launch_bwd(const LayerNormBwdArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// As many workgroups as run at once, by the registers of their kernels (32768 rows
+// of 5120 with gradients of an fp32 residual: 529 us at 768, 573 at 2048, 590 at
+// 512, 689 at 1024).
 int layer_norm_bwd_parts(int64_t rows, int64_t dim) {
   const int64_t pass = dim <= 1024 ? 4 : 1;  // rows a workgroup takes at a time
-  const int64_t most = dim <= 8192 ? 1024 : 512;
+  const int64_t most = dim <= 512    ? 1280
+                       : dim <= 1024 ? 1024
+                       : dim <= 2048 ? 1280
+                       : dim <= 4096 ? 1024
+                       : dim <= 6144 ? 768
+                       : dim <= 8192 ? 512
+                                     : 256;
   const int64_t n = (rows + pass - 1) / pass;
   return static_cast<int>(n < most ? n : most);
 }
