@@ -80,7 +80,8 @@ struct LossArgs {
   float* picked;   // [rows][entries] their logits
   // Rows, weights and dz as bf16 operands of the products: one plane, or three
   // whose sum is the fp32 value.  They lie in panels, [columns / 64][rows][64] (32 in
-  // place of 64 for dz, and for all of three planes), so that a tile's part of any of them is one stretch of memory.
+  // place of 64 for dz, and for all of three planes), so that a tile's part of any
+  // of them is one stretch of memory.
   int planes;
   int64_t dpad;    // columns of x and weight, a multiple of 64
   uint16_t* xp;    // [planes][dpad / 64][xrows][64]
