@@ -147,29 +147,40 @@ def _flat(t, rows=None):
 
 
 class _LayerNorm(torch.autograd.Function):
+    # The outputs are tensors of their own, not views of any: a caller may change them
+    # in place, as any operation's.
     @staticmethod
     def forward(ctx, x, weight, bias, residual, eps):
-        wide = x.shape
-        x, residual = _flat(x), _flat(residual)
-        y, mean, rstd, *rest = layer_norm_fwd(x, weight, bias, residual=residual, eps=eps)
-        r = rest[0] if rest else x
-        ctx.save_for_backward(r, weight, mean, rstd)
-        ctx.bias, ctx.wide, ctx.pair = bias is not None, wide, bool(rest)
-        return (y.view(wide), r.view(wide)) if rest else y.view(wide)
+        ctx.set_materialize_grads(False)
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        rows = _flat(x)
+        if residual is None:
+            _, mean, rstd = layer_norm_fwd(rows, weight, bias, eps=eps, out=_flat(y))
+        else:
+            r = torch.empty_like(residual, memory_format=torch.contiguous_format)
+            _, mean, rstd, _ = layer_norm_fwd(rows, weight, bias, residual=_flat(residual), eps=eps, out=_flat(y),
+                                              residual_out=_flat(r))
+        ctx.save_for_backward(rows if residual is None else r, weight, mean, rstd)
+        ctx.bias, ctx.pair, ctx.wide, ctx.dtype = bias is not None, residual is not None, x.shape, x.dtype
+        return (y, r) if ctx.pair else y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dr=None):
+        if dy is None and dr is None:
+            return (None,) * 5
         r, weight, mean, rstd = ctx.saved_tensors
-        want = ctx.needs_input_grad
-        g = layer_norm_bwd(_flat(dy), r, weight, mean, rstd, dr=_flat(dr), bias=ctx.bias and want[2],
+        want, wide = ctx.needs_input_grad, ctx.wide
+        if dy is None:  # (r alone was used)
+            dy = torch.zeros(wide, dtype=ctx.dtype, device=r.device)
+        g = layer_norm_bwd(_flat(dy), _flat(r), weight, mean, rstd, dr=_flat(dr), bias=ctx.bias and want[2],
                            params=want[1] or (ctx.bias and want[2]))
         # (where both gradients are one, it is handed over as one tensor: two views of
         # it would each become a leaf's .grad, and sums into one would reach the other)
-        dx = g["x"].view(ctx.wide)
+        dx = g["x"].view(wide)
         dres = None
         if ctx.pair and want[3]:
-            dres = dx if g.get("residual", g["x"]) is g["x"] else g["residual"].view(ctx.wide)
+            dres = dx if g.get("residual", g["x"]) is g["x"] else g["residual"].view(wide)
         return (dx if want[0] else None, g.get("weight") if want[1] else None,
                 g.get("bias") if want[2] else None, dres, None)
 
@@ -294,11 +305,17 @@ class _LinearLoss(torch.autograd.Function):
     def forward(ctx, x, weight, ids, teacher, row_weight, scale, tau):
         wide = x.shape
         flat = _flat(x)
-        ids = ids.reshape(-1) if teacher is None else ids.reshape(flat.shape[0], -1)
-        if teacher is not None:
-            teacher = teacher.reshape(ids.shape)
+        if teacher is None:
+            ids = _like(ids, "targets", wide[:-1], torch.int64, x.device).reshape(-1)
+        else:
+            if not isinstance(ids, _Tensor):
+                raise TypeError("ids must be a torch.Tensor")
+            if not isinstance(teacher, _Tensor):
+                raise TypeError("teacher must be a torch.Tensor")
+            ids = _flat(_like(ids, "ids", (*wide[:-1], *ids.shape[-1:]), torch.int64, x.device))
+            teacher = _flat(_like(teacher, "teacher", (*wide[:-1], ids.shape[1]), teacher.dtype, x.device))
         if row_weight is not None:
-            row_weight = row_weight.reshape(-1).contiguous()
+            row_weight = _like(row_weight, "row_weight", wide[:-1], torch.float32, x.device).reshape(-1).contiguous()
         want = ctx.needs_input_grad[:2]
         total = torch.empty((), dtype=torch.float32, device=x.device)
         _, _, dx, dw = _loss(flat, weight, ids, teacher, row_weight, scale, tau, want, (None, None), None, total)
@@ -318,6 +335,8 @@ def linear_cross_entropy(x, weight, targets, row_weight=None, *, logit_scale=1.0
     row_weight [...] (see linear_cross_entropy_grad; targets and row_weight have
     no gradient)."""
     _gpu(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least 1 dimension")
     return _LinearLoss.apply(x, weight, targets, None, row_weight, logit_scale, 1.0)
 
 
@@ -327,4 +346,6 @@ def linear_distillation(x, weight, ids, teacher, row_weight=None, *, temperature
     [..., K], row_weight [...] (see linear_distillation_grad; only x and weight
     have gradients)."""
     _gpu(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least 1 dimension")
     return _LinearLoss.apply(x, weight, ids, _needed(teacher, "teacher"), row_weight, logit_scale, temperature)

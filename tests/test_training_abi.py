@@ -201,6 +201,13 @@ REFUSED = {
     "norm_bwd_mean": (lambda t: mss.layer_norm_bwd(t["x"], t["x"], t["nw"], t["rw"][:3], t["rw"]), ValueError),
     "norm_bwd_none": (lambda t: mss.layer_norm_bwd(t["x"], t["x"], None, t["rw"], t["rw"]), TypeError),
     "norm_bwd_dr": (lambda t: mss.layer_norm_bwd(t["x"], t["x"], t["nw"], t["rw"], t["rw"], dr=t["x"].bfloat16()), TypeError),
+    "targets_transposed": (lambda t: mss.linear_cross_entropy(t["x"].view(2, 2, 8), t["w"], t["ids"]), ValueError),
+    "row_weight_flat": (lambda t: mss.linear_cross_entropy(t["x"].view(2, 2, 8), t["w"], t["ids"].view(2, 2), t["rw"]),
+                        ValueError),
+    "ids_flat": (lambda t: mss.linear_distillation(t["x"], t["w"], t["ids"], t["teach"]), ValueError),
+    "ids_list": (lambda t: mss.linear_distillation(t["x"], t["w"], [[1, 2]] * 4, t["teach"]), TypeError),
+    "teacher_entries": (lambda t: mss.linear_distillation(t["x"], t["w"], t["top"], t["teach"][:, :1]), ValueError),
+    "no_rows_dim": (lambda t: mss.linear_cross_entropy(on(torch.zeros(())), t["w"], t["ids"]), ValueError),
     "norm_autograd_residual": (lambda t: mss.layer_norm(t["x"], t["nw"], None, t["x"][:3]), ValueError),
 }
 

@@ -218,6 +218,36 @@ def test_layer_norm_gradients_of_leaves_are_their_own():
         torch.autograd.grad(dx.sum(), x)
 
 
+@gpu
+def test_layer_norm_outputs_may_change_in_place():
+    note("layer_norm: outputs changed in place, one of two outputs used")
+    g = gen(10)
+    x, res = randn(g, 3, 5, 96, dtype=BF16).requires_grad_(), randn(g, 3, 5, 96).requires_grad_()
+    w, b = randn(g, 96).requires_grad_(), randn(g, 96).requires_grad_()
+    dy = randn(g, 3, 5, 96, dtype=BF16)
+    y, r = mss.layer_norm(x, w, b, res)
+    want = torch.autograd.grad((y, r), (x, res, w, b), (dy, torch.zeros_like(r)))
+    # y alone: as with a gradient of 0 for r
+    y, r = mss.layer_norm(x, w, b, res)
+    assert all(torch.equal(p, q) for p, q in zip(torch.autograd.grad(y, (x, res, w, b), dy), want))
+    y, r = mss.layer_norm(x, w, b, res)
+    y.mul_(2)
+    assert all(torch.equal(p, 2 * q) for p, q in zip(torch.autograd.grad(y, (x, res), dy), want))
+    y = mss.layer_norm(x, w, b)
+    y.add_(1)
+    y.backward(dy)
+    # r alone: its gradient passes through
+    y, r = mss.layer_norm(x, w, b, res)
+    dr = randn(g, 3, 5, 96)
+    dx, dres, dw = torch.autograd.grad(r, (x, res, w), dr)
+    assert torch.equal(dres, dr) and torch.equal(dx, dr.bfloat16()) and not dw.any()
+    # r is read by the backward
+    y, r = mss.layer_norm(x, w, b, res)
+    r.add_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward(dy)
+
+
 # ---------------------------------------------------------------- losses
 
 def loss_case(rows, dim, vocab, dtype, seed=0, ignored=0.0, spread=6.0):
@@ -467,6 +497,7 @@ def test_losses_of_no_rows(dtype):
     assert mss.linear_cross_entropy(x[:0], w, ids[:0]).item() == 0
     tops, teacher = top_case(4, 300, 3)
     assert not mss.linear_distillation_grad(x[:0], w, tops[:0], teacher[:0])[3].any()
+    assert mss.linear_distillation(x[:0].view(2, 0, 64), w, tops[:0].view(2, 0, 3), teacher[:0].view(2, 0, 3)).item() == 0
 
 
 @gpu
