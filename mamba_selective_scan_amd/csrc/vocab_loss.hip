@@ -14,8 +14,7 @@
 // codes.  These passes are bound by HBM: 6144 rows that count of 65536, 805 MB in
 // and out each: dz 337 us (4.8 TB/s), the sums of dx 31, the rows' sums 20, x's
 // operand 17, of 5.7 ms.  With few rows the launches count: 24 rows (18 count) of
-// 32768 x 768: 60 us, 21 of them two reads of the weight's and one write of
-// dweight's bytes.
+// 32768 x 768: 60 us, 21 of them to read the weight's bytes and write dweight's.
 #include "mss.h"
 #include "mss_train.hpp"
 #include "vocab_gemm.hpp"
