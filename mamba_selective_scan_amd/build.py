@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libmss.so")
 SOURCES = ["mss_api.hip", "scan_fwd.hip", "state_update.hip", "conv1d.hip", "scan_bwd.hip",
            "scan_cplx.hip", "head_api.hip", "conv_prompts.hip", "head_scan.hip", "head_step.hip",
            "rms_norm.hip", "train_api.hip", "layer_norm.hip", "vocab_loss.hip",
-           "vocab_gemm.hip"]
+           "vocab_gemm.hip", "vocab_few.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 instructions are disabled for every kernel: the compiler would

@@ -83,6 +83,7 @@ struct LossArgs {
   // place of 64 for dz, and for all of three planes), so that a tile's part of any
   // of them is one stretch of memory.
   int planes;
+  bool direct;     // few rows of fp32: xp and dz are fp32, weights are read where they are
   int64_t dpad;    // columns of x and weight, a multiple of 64
   uint16_t* xp;    // [planes][dpad / 64][xrows][64]
   int64_t xrows;   // a multiple of 64; those behind the last row that counts, to the next 64, are 0

@@ -74,7 +74,7 @@ size_t norm_bwd_workspace(const mss_layer_norm_bwd_args* a) {
 constexpr int64_t kPieceBytes = int64_t{2} << 30;
 
 struct LossPlan {
-  bool grad, pack_w, small_logits, small_dx, small_dw;
+  bool grad, direct, pack_w, small_logits, small_dx, small_dw;
   int64_t planes, dpad, vpad, tiles, words, piece, pieces, splits, xrows, vocab_tile, dw_splits;
   size_t live, cuts, row_of, place, counts, share, known, near, where, picked, xp, wp, stats, sums, probs, dz, value, fix, part,
       dw_sum, bytes;
@@ -85,6 +85,7 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   const bool f32 = a->io_dtype == MSS_F32;
   p.grad = a->dx != nullptr || a->dweight != nullptr;
   p.planes = f32 ? 3 : 1;
+  p.direct = f32 && a->rows >= 1 && a->rows <= mss::kDirectRows;
   p.dpad = up(a->dim, 64);
   p.vpad = up(a->vocab, 64);
   const int64_t rows = std::max<int64_t>(a->rows, 1);
@@ -94,17 +95,17 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
     return mss::product_time(t, static_cast<float>(mss::tiles_of(t, a->vocab, rows)), 1.0f, static_cast<float>(steps(a->dim)));
   };
   p.small_logits = logits_time(true) < logits_time(false);
-  p.vocab_tile = f32 || p.small_logits ? 64 : 128;
+  p.vocab_tile = p.direct ? 32 : f32 || p.small_logits ? 64 : 128;
   p.tiles = (a->vocab + p.vocab_tile - 1) / p.vocab_tile;
-  p.words = (p.tiles + 31) / 32;
+  p.words = p.direct ? 0 : (p.tiles + 31) / 32;
   // bf16 weights are read where they are if their rows are whole 16-byte vectors,
   // one behind another, and 256 of them within 32-bit offsets
-  p.pack_w = f32 || a->dim % 8 != 0 || !aligned(a->weight, 16) ||
+  p.pack_w = f32 ? !p.direct : a->dim % 8 != 0 || !aligned(a->weight, 16) ||
              (a->vocab > 1 && (a->weight_stride % 8 != 0 || a->weight_stride < a->dim ||
                                a->weight_stride > (int64_t{1} << 21)));
-  const int64_t a_row = p.tiles * 8 + (p.grad ? p.vpad * (f32 ? 10 : 2) : 0);
+  const int64_t a_row = p.tiles * 8 + (p.direct ? p.vpad * 4 : p.grad ? p.vpad * (f32 ? 10 : 2) : 0);
   p.pieces = (rows * a_row + kPieceBytes - 1) / kPieceBytes;
-  p.piece = up((rows + p.pieces - 1) / p.pieces, 256);
+  p.piece = up((rows + p.pieces - 1) / p.pieces, p.direct ? 64 : 256);
   p.pieces = (rows + p.piece - 1) / p.piece;
   // parts of the dx product, within 512 MiB of them
   p.splits = std::clamp<int64_t>((int64_t{1} << 29) / (p.piece * p.dpad * 4), 1, 64);
@@ -133,6 +134,13 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   };
   p.small_dw = dw_time(true) < dw_time(false);
   p.dw_splits = dw_parts[p.small_dw];
+  if (p.direct) {
+    // about 1024 workgroups of dx, each with 8 panels of the vocabulary at least
+    const int64_t cols = (a->dim + 127) / 128;
+    p.splits = std::clamp<int64_t>(std::min(1024 / cols, a->vocab / 256), 1, p.splits);
+    p.small_dx = true;
+    p.dw_splits = 1;
+  }
   p.xrows = up(rows, 64);
   size_t at = 0;
   auto room = [&](int64_t n) {
@@ -150,12 +158,12 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   p.near = room(rows * a->entries * 4);
   p.where = room(rows * p.words * 4);
   p.picked = room(rows * a->entries * 4);
-  p.xp = room(p.planes * p.xrows * p.dpad * 2);
+  p.xp = room(p.xrows * p.dpad * (p.direct ? 4 : p.planes * 2));
   p.wp = room(p.pack_w ? p.planes * a->vocab * p.dpad * 2 : 0);
   p.stats = room(p.piece * p.tiles * 8);
   p.sums = room(p.grad ? p.piece * 8 : 0);
-  p.probs = room(p.grad ? p.piece * p.vpad * (f32 ? 4 : 2) : 0);
-  p.dz = p.grad && f32 ? room(3 * p.piece * p.vpad * 2) : p.probs;
+  p.probs = room(p.grad || p.direct ? p.piece * p.vpad * (f32 ? 4 : 2) : 0);
+  p.dz = p.grad && f32 && !p.direct ? room(3 * p.piece * p.vpad * 2) : p.probs;
   p.value = room(p.grad ? p.piece * a->entries * 4 : 0);
   p.fix = room(p.grad && !f32 ? p.piece * 8 : 0);
   p.part = room(a->dx != nullptr ? p.splits * p.piece * p.dpad * 4 : 0);
@@ -361,6 +369,7 @@ mss_status mss_linear_loss(const mss_linear_loss_args* a, void* stream) {
   k.where_words = static_cast<int>(p.words);
   k.picked = reinterpret_cast<float*>(ws + p.picked);
   k.planes = static_cast<int>(p.planes);
+  k.direct = p.direct;
   k.dpad = p.dpad;
   k.xp = reinterpret_cast<uint16_t*>(ws + p.xp);
   k.pack_w = p.pack_w;

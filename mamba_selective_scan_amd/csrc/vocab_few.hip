@@ -1,0 +1,242 @@
+// vocab_few.hip -- the three products of the losses over a vocabulary for up to 64
+// rows of fp32, gfx950:
+//   logits z[i, v] = scale sum_d x[i, d] w[v, d], with the softmax sums of 32 entries
+//   dx     part[i, d] = sum_v dz[i, v] w[v, d], cut over v
+//   dw     dw[v, d] = sum_i dz[i, v] x[i, d]
+//
+// So few rows make no use of what lies in a tile of weights: the products are bound
+// by reading the matrix twice and writing its gradient.  They are taken on the fp32
+// matrix instruction, whose rate holds up with memory to about 64 rows, straight
+// from the matrix as it is; three bf16 planes of it would have to be written and
+// read first, five times its bytes.  Two of the instruction's summed indices are
+// one of each half wave's, so that a lane's 4 adjacent elements serve 4 of them.
+#include "mss.h"
+#include "vocab_gemm.hpp"
+
+namespace mss {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ inline f32x16 product(float a, float b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+}
+// The row of a 32 x 32 product that element e of a lane holds; its column is the
+// lane's, modulo 32.
+__device__ inline int acc_row(int e) { return 8 * (e >> 2) + 4 * (static_cast<int>(threadIdx.x) >> 5 & 1) + (e & 3); }
+
+// 64 entries a workgroup, N times 32 rows.  Its waves take every fourth 32 columns,
+// 512 bytes of a row side by side, and their sums meet in a fixed order.
+template <int N>
+__global__ __launch_bounds__(256) void few_logits_kernel(LossArgs a) {
+  __shared__ f32x4 meet[4][2 * N][4][64];
+  const int live = *a.live;
+  if (live == 0) return;
+  const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), h = lane >> 5, l = lane & 31;
+  const int v0 = static_cast<int>(blockIdx.x) * 64;
+  const float* w[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+    w[m] = static_cast<const float*>(a.weight) + min(v0 + 32 * m + l, a.vocab - 1) * a.sw + 4 * h;
+  const float* x = reinterpret_cast<const float*>(a.xp) + l * 32 + 4 * h;
+  f32x16 acc[2][N];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[m][n] = f32x16{0};
+  auto step = [&](int p, bool whole) __attribute__((always_inline)) {
+    float fw[2][4][4];
+    f32x4 fx[N][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (whole) vecio<float, 4>::load(w[m] + p * 32 + 8 * q, fw[m][q]);
+        else load_part<float, 4>(w[m] + p * 32 + 8 * q, a.dim - (p * 32 + 8 * q + 4 * h), fw[m][q]);
+      }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        fx[n][q] = *reinterpret_cast<const f32x4*>(x + p * a.xrows * 32 + n * 1024 + 8 * q);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < N; ++n) acc[m][n] = product(fw[m][q][e], fx[n][q][e], acc[m][n]);
+  };
+  const int full = a.dim / 32;
+  for (int p = wave; p < full; p += 4) step(p, true);
+  if (a.dim % 32 != 0 && (full & 3) == wave) step(full, false);
+
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        meet[wave][m * N + n][q][lane] = f32x4{acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
+  __syncthreads();
+  if (wave >= 2 * N) return;
+  const int m = wave / N, i = wave % N * 32 + l, v = v0 + 32 * m;
+  if (v >= a.vocab) return;
+  f32x4 z[4];
+  float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    z[q] = ((meet[0][wave][q][lane] + meet[1][wave][q][lane]) + meet[2][wave][q][lane]) + meet[3][wave][q][lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      z[q][e] = v + 8 * q + 4 * h + e < a.vocab ? z[q][e] * a.scale : -INFINITY;
+      top = fmaxf(top, z[q][e]);
+    }
+  }
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  const float from = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += fast_exp2((z[q][e] - from) * kLog2e);
+  sum += __shfl_xor(sum, 32, 64);
+  if (i >= live) return;
+  if (h == 0) a.stats[static_cast<int64_t>(i) * a.tiles + v / 32] = make_float2(top, sum);
+  float* out = static_cast<float*>(a.probs) + z_index(a, i, v) + 4 * h;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) *reinterpret_cast<f32x4*>(out + 8 * q) = z[q];
+}
+
+// 128 columns of M times 32 rows and a part of the vocabulary a workgroup, whose
+// waves take every fourth 32 entries of it.  A lane's products are of 4 adjacent
+// columns.
+template <int M>
+__device__ inline void few_dx(const LossArgs& a, int id, f32x4 (&meet)[4][4][4][64]) {
+  const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), h = lane >> 5, l = lane & 31;
+  const int tiles = (a.dim + 127) / 128, split = id / tiles, d0 = id % tiles * 128, d = d0 + 4 * l;
+  if (*a.live == 0) return;
+  const int64_t panels = (a.vocab + 31) / 32;
+  const int p0 = static_cast<int>(panels * split / a.splits), p1 = static_cast<int>(panels * (split + 1) / a.splits);
+  const float* dz = static_cast<const float*>(a.probs) + l * 32 + 4 * h;
+  const float* w = static_cast<const float*>(a.weight) + d;
+  f32x16 acc[M][4];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[m][t] = f32x16{0};
+  auto step = [&](int p, bool whole) __attribute__((always_inline)) {
+    f32x4 fz[M][4];
+    float fw[4][4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        fz[m][q] = *reinterpret_cast<const f32x4*>(dz + static_cast<int64_t>(p) * 2048 + m * 1024 + 8 * q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* row = w + min(p * 32 + 8 * q + 4 * h + e, a.vocab - 1) * a.sw;  // (dz is 0 behind the last)
+        if (whole) vecio<float, 4>::load(row, fw[q][e]);
+        else load_part<float, 4>(row, a.dim - d, fw[q][e]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int m = 0; m < M; ++m) acc[m][t] = product(fz[m][q][e], fw[q][e][t], acc[m][t]);
+  };
+  if (d0 + 128 <= a.dim)
+    for (int p = p0 + wave; p < p1; p += 4) step(p, true);
+  else
+    for (int p = p0 + wave; p < p1; p += 4) step(p, false);
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (m > 0) __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        meet[wave][t][q][lane] = f32x4{acc[m][t][4 * q], acc[m][t][4 * q + 1], acc[m][t][4 * q + 2], acc[m][t][4 * q + 3]};
+    __syncthreads();
+    f32x4 s[4];  // of rows 8 wave + 4 h ..
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      s[t] = ((meet[0][t][wave][lane] + meet[1][t][wave][lane]) + meet[2][t][wave][lane]) + meet[3][t][wave][lane];
+    float* out = a.part + (static_cast<int64_t>(split) * a.piece + 32 * m + 8 * wave + 4 * h) * a.dpad + d;
+    if (d < a.dpad)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f32x4*>(out + e * a.dpad) = f32x4{s[0][e], s[1][e], s[2][e], s[3][e]};
+  }
+}
+
+// 32 entries a wave, 128 columns at a time; the entries' dz of M times 32 rows stay
+// in registers.
+template <int M>
+__device__ inline void few_dw(const LossArgs& a, int id, int groups) {
+  const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), h = lane >> 5, l = lane & 31;
+  const int live = *a.live, of = (a.vocab + 127) / 128, v0 = id % of * 128 + wave * 32;
+  if (v0 >= a.vocab) return;
+  const int steps = live == 0 ? 0 : 16 * M;
+  float fz[16 * M] = {};
+  if (live != 0)
+#pragma unroll
+    for (int j = 0; j < 16 * M; ++j)
+      fz[j] = static_cast<const float*>(a.probs)[v0 * INT64_C(64) + (2 * j + h) * 32 + l];
+  for (int d0 = id / of * 128; d0 < a.dim; d0 += groups * 128) {
+    const int d = d0 + 4 * l, dx = min(d, static_cast<int>(a.dpad) - 4);
+    const float* x = reinterpret_cast<const float*>(a.xp) + (dx / 32 * a.xrows + h) * 32 + dx % 32;
+    f32x16 acc[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[t] = f32x16{0};
+    if (steps != 0)
+#pragma unroll
+      for (int j = 0; j < 16 * M; ++j) {
+        const f32x4 fx = *reinterpret_cast<const f32x4*>(x + j * 64);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[t] = product(fz[j], fx[t], acc[t]);
+      }
+    float* out = static_cast<float*>(a.dweight) + d;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int v = v0 + acc_row(e);
+      const float row[4] = {acc[0][e], acc[1][e], acc[2][e], acc[3][e]};
+      if (v < a.vocab) store_part<float, 4>(out + v * a.sdw, a.dim - d, row);
+    }
+  }
+}
+
+// Both products in one launch, the dx product's workgroups first.
+template <int M>
+__global__ __launch_bounds__(256) void few_gradients_kernel(LossArgs a, int dx_blocks, int groups) {
+  __shared__ f32x4 meet[4][4][4][64];
+  const int id = static_cast<int>(blockIdx.x);
+  if (id < dx_blocks) few_dx<M>(a, id, meet);
+  else few_dw<M>(a, id - dx_blocks, groups);
+}
+
+}  // namespace
+
+hipError_t launch_few_logits(const LossArgs& a, hipStream_t stream) {
+  const unsigned g = static_cast<unsigned>((a.vocab + 63) / 64);
+  if (a.rows <= 32) few_logits_kernel<1><<<g, 256, 0, stream>>>(a);
+  else few_logits_kernel<2><<<g, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_few_gradients(const LossArgs& a, hipStream_t stream) {
+  const int cols = (a.dim + 127) / 128, of = (a.vocab + 127) / 128;
+  const int dx = a.dx != nullptr ? cols * a.splits : 0;
+  const int groups = std::clamp(2048 / of, 1, cols);
+  const unsigned g = static_cast<unsigned>(dx + (a.dweight != nullptr ? of * groups : 0));
+  if (a.rows <= 32) few_gradients_kernel<1><<<g, 256, 0, stream>>>(a, dx, groups);
+  else few_gradients_kernel<2><<<g, 256, 0, stream>>>(a, dx, groups);
+  return hipGetLastError();
+}
+
+}  // namespace mss

@@ -78,10 +78,16 @@ __device__ inline int dx_cuts(const LossArgs& a, int rows) {
   return best;
 }
 
+// Up to so many rows of fp32 take their products from the matrix as it is.
+constexpr int kDirectRows = 64;
+
 // logits of the piece's rows: stats, and with `keep` the codes or logits
 hipError_t launch_logits(const LossArgs& a, int first, bool keep, hipStream_t stream);
 // The products of dz that are wanted: part = dz weight, by splits of the vocabulary;
 // dweight = dz^T x, or its sums over parts of the rows, or over the pieces so far.
 hipError_t launch_gradients(const LossArgs& a, int first, hipStream_t stream);
+// The same of few rows of fp32.
+hipError_t launch_few_logits(const LossArgs& a, hipStream_t stream);
+hipError_t launch_few_gradients(const LossArgs& a, hipStream_t stream);
 
 }  // namespace mss

@@ -48,7 +48,7 @@ __device__ inline int id_at(const LossArgs& a, int64_t row, int k) {
 __device__ inline void set_cuts(const LossArgs& a, int live) {
   if (a.dx == nullptr) return;
   for (int p = 0; p < a.pieces; ++p) {
-    const int s = dx_cuts(a, min(a.piece, live - p * a.piece));
+    const int s = a.direct ? a.splits : dx_cuts(a, min(a.piece, live - p * a.piece));
     if ((threadIdx.x & 63) == 0) a.cuts[p] = s;
   }
 }
@@ -194,7 +194,9 @@ __global__ __launch_bounds__(256) void pack_kernel(LossArgs a, int tile_shift) {
   for (int c = threadIdx.x * 8; c < a.dpad; c += 2048) {
     float v[8];
     load_part<IO, 8>(x + c, j < live ? a.dim - c : 0, v);
-    to_planes(v, a.xp + (c / w * a.xrows + j) * w + c % w, a.xrows * a.dpad, a.planes);
+    const int64_t at = (c / w * a.xrows + j) * w + c % w;
+    if (a.direct) vecio<float, 8>::store(reinterpret_cast<float*>(a.xp) + at, v);
+    else to_planes(v, a.xp + at, a.xrows * a.dpad, a.planes);
   }
   if (j >= live) return;
   for (int i = threadIdx.x; i < a.where_words; i += 256) where[i] = 0;
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(256) void pack_kernel(LossArgs a, int tile_shift) {
   for (int k = threadIdx.x; k < a.entries; k += 256) {
     const int id = id_at(a, row, k);
     a.near[static_cast<int64_t>(j) * a.entries + k] = id;
-    if (id >= 0) atomicOr(where + (id >> tile_shift >> 5), 1u << (id >> tile_shift & 31));
+    if (id >= 0 && !a.direct) atomicOr(where + (id >> tile_shift >> 5), 1u << (id >> tile_shift & 31));
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.where_words; i += 256) a.where[static_cast<int64_t>(j) * a.where_words + i] = where[i];
@@ -257,7 +259,9 @@ __global__ __launch_bounds__(256) void row_kernel(LossArgs a, int first, bool bf
   const int row = a.row_of[j];
   const RowSum all = row_sum(a, i, meet);
   const int* near = a.near + static_cast<int64_t>(j) * a.entries;
-  const float* picked = a.picked + static_cast<int64_t>(j) * a.entries;
+  auto logit = [&](int k, int id) __attribute__((always_inline)) {
+    return a.direct ? static_cast<const float*>(a.probs)[z_index(a, i, id)] : a.picked[static_cast<int64_t>(j) * a.entries + k];
+  };
   const float* share = a.teacher != nullptr ? a.share + static_cast<int64_t>(row) * a.entries : nullptr;
   const float log_sum = logf(all.sum);
   const float c = (a.row_weight != nullptr ? a.row_weight[row] : 1.0f / static_cast<float>(live)) * a.back;
@@ -267,15 +271,16 @@ __global__ __launch_bounds__(256) void row_kernel(LossArgs a, int first, bool bf
   for (int k = threadIdx.x; k < a.entries; k += 256) {
     const int id = near[k];
     if (id < 0) continue;
+    const float z = logit(k, id);
     float t = share != nullptr ? share[k] : 1.0f;
-    if (t != 0.0f) s += t * ((all.from - picked[k]) + log_sum);
+    if (t != 0.0f) s += t * ((all.from - z) + log_sum);
     if (!grad) continue;
     if (share != nullptr) {  // all shares of this id
       t = 0.0f;
       for (int q = 0; q < a.entries; ++q)
         if (near[q] == id) t += share[q];
     }
-    const float v = fmaf(-t, all.sum, expf(picked[k] - all.from)) * by;
+    const float v = fmaf(-t, all.sum, expf(z - all.from)) * by;
     a.value[static_cast<int64_t>(i) * a.entries + k] = v;
     const float miss = v - __uint_as_float(static_cast<uint32_t>(bf16_bits(v)) << 16);
     if (fabsf(miss) > most) {
@@ -346,15 +351,20 @@ __global__ __launch_bounds__(256) void dz_kernel(LossArgs a, int first, int pane
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = on && v + e < a.vocab ? q[e] * sum.y : 0.0f;
-    to_planes(q, a.dz + at, plane, sizeof(IO) == 2 ? 1 : 3);
+    if (sizeof(IO) == 4 && a.direct) vecio<float, 8>::store(static_cast<float*>(a.probs) + at, q);
+    else to_planes(q, a.dz + at, plane, sizeof(IO) == 2 ? 1 : 3);
   }
   __syncthreads();
   for (int k = threadIdx.x; k < min(32, rows - i0) * a.entries; k += 256) {
     const int r = i0 + k / a.entries, e = k % a.entries;
     const int id = a.near[static_cast<int64_t>(first + r) * a.entries + e];
     if (id < p0 * 64 || id >= p1 * 64) continue;
-    uint16_t* z = a.dz + z_index(a, r, id);
     float v = a.value[static_cast<int64_t>(r) * a.entries + e];
+    if (sizeof(IO) == 4 && a.direct) {
+      static_cast<float*>(a.probs)[z_index(a, r, id)] = v;
+      continue;
+    }
+    uint16_t* z = a.dz + z_index(a, r, id);
     for (int n = 0; n < (sizeof(IO) == 2 ? 1 : 3); ++n) {
       const uint16_t b = bf16_bits(v);
       z[n * plane] = b;
@@ -508,7 +518,7 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
   for (int p = 0; p < a.pieces; ++p) {
     const int first = p * a.piece;
     const unsigned n = static_cast<unsigned>(std::min(a.piece, a.rows - first));
-    hipError_t e = launch_logits(a, first, grad, s);
+    hipError_t e = a.direct ? launch_few_logits(a, s) : launch_logits(a, first, grad, s);
     if (e != hipSuccess) return e;
     row_kernel<<<n, 256, 0, s>>>(a, first, sizeof(IO) == 2, grad);
     if (grad) {
@@ -517,7 +527,7 @@ hipError_t launch_io(const LossArgs& a, hipStream_t s) {
       const unsigned panels = std::clamp(all * groups / 2048, 1u, 32u);
       dz_kernel<IO><<<dim3(groups, (all + panels - 1) / panels), 256, 0, s>>>(a, first, static_cast<int>(panels), shift);
     }
-    if (grad && (e = launch_gradients(a, first, s)) != hipSuccess) return e;
+    if (grad && (e = a.direct ? launch_few_gradients(a, s) : launch_gradients(a, first, s)) != hipSuccess) return e;
     if (a.dx != nullptr) {
       const unsigned cols = static_cast<unsigned>(a.dim + 255) / 256;
       if (a.small_dx && rows <= (1u << 20) / cols) dx_few_kernel<IO><<<dim3(rows, cols), 256, 0, s>>>(a, first);
