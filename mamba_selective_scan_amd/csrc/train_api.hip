@@ -85,7 +85,7 @@ LossPlan loss_plan(const mss_linear_loss_args* a) {
   const bool f32 = a->io_dtype == MSS_F32;
   p.grad = a->dx != nullptr || a->dweight != nullptr;
   p.planes = f32 ? 3 : 1;
-  p.direct = f32 && a->rows >= 1 && a->rows <= mss::kDirectRows;
+  p.direct = f32 && a->rows >= 1 && a->rows <= (p.grad ? mss::kDirectRows : mss::kDirectLossRows);
   p.dpad = up(a->dim, 64);
   p.vpad = up(a->vocab, 64);
   const int64_t rows = std::max<int64_t>(a->rows, 1);

@@ -1,15 +1,17 @@
-// vocab_few.hip -- the three products of the losses over a vocabulary for up to 64
-// rows of fp32, gfx950:
+// vocab_few.hip -- the three products of the losses over a vocabulary for few rows of
+// fp32, up to 64, or 128 without gradients, gfx950:
 //   logits z[i, v] = scale sum_d x[i, d] w[v, d], with the softmax sums of 32 entries
 //   dx     part[i, d] = sum_v dz[i, v] w[v, d], cut over v
 //   dw     dw[v, d] = sum_i dz[i, v] x[i, d]
 //
-// So few rows make no use of what lies in a tile of weights: the products are bound
-// by reading the matrix twice and writing its gradient.  They are taken on the fp32
-// matrix instruction, whose rate holds up with memory to about 64 rows, straight
+// So few rows make little use of what lies in a tile of weights: the products are
+// bound by reading the matrix twice and writing its gradient.  They are taken on the
+// fp32 matrix instruction, whose rate holds up with memory to about 64 rows, straight
 // from the matrix as it is; three bf16 planes of it would have to be written and
 // read first, five times its bytes.  Two of the instruction's summed indices are
 // one of each half wave's, so that a lane's 4 adjacent elements serve 4 of them.
+// 16 rows, 32000 x 4096 (524 MB): logits 130 us (4.0 TB/s), dx and dweight 280 (3.7
+// TB/s).
 #include "mss.h"
 #include "vocab_gemm.hpp"
 
@@ -26,69 +28,97 @@ __device__ inline f32x16 product(float a, float b, f32x16 c) {
 // lane's, modulo 32.
 __device__ inline int acc_row(int e) { return 8 * (e >> 2) + 4 * (static_cast<int>(threadIdx.x) >> 5 & 1) + (e & 3); }
 
-// 64 entries a workgroup, N times 32 rows.  Its waves take every fourth 32 columns,
-// 512 bytes of a row side by side, and their sums meet in a fixed order.
+// 32 entries a workgroup, N times 32 rows.  Its waves take every fourth 32 columns,
+// 512 bytes of a row side by side, and their sums meet in a fixed order.  A load
+// takes whole 128-byte pieces of rows, which a wave turns about through its own LDS
+// (16 rows, 32000 x 4096: 133 us; where a lane loads what it multiplies, 16 bytes of
+// a row, 164).  One part is loaded while the one before it is multiplied.  Twice the
+// entries read x half as often, and leave fewer workgroups than the card holds (60
+// rows, 20000 x 2560: 121 us, 96 so; 16 rows, 32000 x 4096: 130).
 template <int N>
 __global__ __launch_bounds__(256) void few_logits_kernel(LossArgs a) {
-  __shared__ f32x4 meet[4][2 * N][4][64];
+  constexpr int kRows = 32 + 32 * N;  // of weights, then of x
+  union Shared {
+    f32x4 part[4][kRows][8];          // the 16-byte vectors of a row turned by the row
+    f32x4 meet[4][N][4][64];
+  };
+  __shared__ Shared sh;
   const int live = *a.live;
   if (live == 0) return;
   const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), h = lane >> 5, l = lane & 31;
-  const int v0 = static_cast<int>(blockIdx.x) * 64;
-  const float* w[2];
+  const int v = static_cast<int>(blockIdx.x) * 32, row = lane >> 3, col = lane & 7;
+  const float* w[4];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
-    w[m] = static_cast<const float*>(a.weight) + min(v0 + 32 * m + l, a.vocab - 1) * a.sw + 4 * h;
-  const float* x = reinterpret_cast<const float*>(a.xp) + l * 32 + 4 * h;
-  f32x16 acc[2][N];
+  for (int j = 0; j < 4; ++j)
+    w[j] = static_cast<const float*>(a.weight) + min(v + 8 * j + row, a.vocab - 1) * a.sw + 4 * col;
+  const float* x = reinterpret_cast<const float*>(a.xp) + row * 32 + 4 * col;
+  f32x16 acc[N];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int n = 0; n < N; ++n) acc[n] = f32x16{0};
+  f32x4 part[kRows / 8];
+  auto load = [&](int p, bool whole) __attribute__((always_inline)) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) acc[m][n] = f32x16{0};
-  auto step = [&](int p, bool whole) __attribute__((always_inline)) {
-    float fw[2][4][4];
-    f32x4 fx[N][4];
+    for (int j = 0; j < 4; ++j) {
+      float q[4];
+      if (whole) vecio<float, 4>::load(w[j] + p * 32, q);
+      else load_part<float, 4>(w[j] + p * 32, a.dim - p * 32 - 4 * col, q);
+      part[j] = f32x4{q[0], q[1], q[2], q[3]};
+    }
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int j = 0; j < 4 * N; ++j) part[4 + j] = *reinterpret_cast<const f32x4*>(x + p * a.xrows * 32 + j * 256);
+  };
+  auto turn = [](int r, int c) __attribute__((always_inline)) { return c ^ (r >> 1 & 7); };
+  auto put = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (whole) vecio<float, 4>::load(w[m] + p * 32 + 8 * q, fw[m][q]);
-        else load_part<float, 4>(w[m] + p * 32 + 8 * q, a.dim - (p * 32 + 8 * q + 4 * h), fw[m][q]);
-      }
+    for (int j = 0; j < kRows / 8; ++j) sh.part[wave][8 * j + row][turn(8 * j + row, col)] = part[j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
+  auto multiply = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int q = 0; q < 4; ++q) {
+      const f32x4 fw = sh.part[wave][l][turn(l, 2 * q + h)];
+      f32x4 fx[N];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        fx[n][q] = *reinterpret_cast<const f32x4*>(x + p * a.xrows * 32 + n * 1024 + 8 * q);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
+      for (int n = 0; n < N; ++n) fx[n] = sh.part[wave][32 + 32 * n + l][turn(l, 2 * q + h)];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int n = 0; n < N; ++n) acc[m][n] = product(fw[m][q][e], fx[n][q][e], acc[m][n]);
+        for (int n = 0; n < N; ++n) acc[n] = product(fw[e], fx[n][e], acc[n]);
+    }
   };
-  const int full = a.dim / 32;
-  for (int p = wave; p < full; p += 4) step(p, true);
-  if (a.dim % 32 != 0 && (full & 3) == wave) step(full, false);
+  // (without a branch around the loads, which would be waited for as if it had not
+  // been taken: the last part is loaded twice)
+  const int full = a.dim / 32, last = full - 1 - ((full - 1 - wave) & 3);
+  if (wave < full) {
+    load(wave, true);
+    for (int p = wave; p < full; p += 4) {
+      put();
+      load(min(p + 4, last), true);
+      asm volatile("" ::: "memory");  // (the compiler would load behind the products)
+      multiply();
+    }
+  }
+  if (a.dim % 32 != 0 && (full & 3) == wave) {
+    load(full, false);
+    put();
+    multiply();
+  }
 
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        meet[wave][m * N + n][q][lane] = f32x4{acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
   __syncthreads();
-  if (wave >= 2 * N) return;
-  const int m = wave / N, i = wave % N * 32 + l, v = v0 + 32 * m;
-  if (v >= a.vocab) return;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      sh.meet[wave][n][q][lane] = f32x4{acc[n][4 * q], acc[n][4 * q + 1], acc[n][4 * q + 2], acc[n][4 * q + 3]};
+  __syncthreads();
+  const int i = wave * 32 + l;
+  if (wave >= N) return;
   f32x4 z[4];
   float top = -INFINITY, sum = 0.0f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    z[q] = ((meet[0][wave][q][lane] + meet[1][wave][q][lane]) + meet[2][wave][q][lane]) + meet[3][wave][q][lane];
+    z[q] = ((sh.meet[0][wave][q][lane] + sh.meet[1][wave][q][lane]) + sh.meet[2][wave][q][lane]) + sh.meet[3][wave][q][lane];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       z[q][e] = v + 8 * q + 4 * h + e < a.vocab ? z[q][e] * a.scale : -INFINITY;
@@ -223,9 +253,11 @@ __global__ __launch_bounds__(256) void few_gradients_kernel(LossArgs a, int dx_b
 }  // namespace
 
 hipError_t launch_few_logits(const LossArgs& a, hipStream_t stream) {
-  const unsigned g = static_cast<unsigned>((a.vocab + 63) / 64);
+  const unsigned g = static_cast<unsigned>((a.vocab + 31) / 32);
   if (a.rows <= 32) few_logits_kernel<1><<<g, 256, 0, stream>>>(a);
-  else few_logits_kernel<2><<<g, 256, 0, stream>>>(a);
+  else if (a.rows <= 64) few_logits_kernel<2><<<g, 256, 0, stream>>>(a);
+  else if (a.rows <= 96) few_logits_kernel<3><<<g, 256, 0, stream>>>(a);
+  else few_logits_kernel<4><<<g, 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -140,8 +140,13 @@ def test_workspace_sizes():
     assert size("loss", vocab=0) == (0, "MSS_ERR_BAD_SHAPE")
     n, ok = size("loss")
     assert ok == "MSS_OK" and n > 30 * 1000 * 2
-    # without gradients no probabilities are kept; fp32 takes planes of its operands
-    assert size("loss", dx=0, dweight=0)[0] < n < size("loss", io_dtype=0)[0]
+    # without gradients no probabilities are kept
+    assert size("loss", dx=0, dweight=0)[0] < n
+    # fp32 takes planes of its operands, a few rows of it the matrix as it is
+    assert size("loss", rows=65)[0] + 1000 * 256 * 4 < size("loss", rows=65, io_dtype=0)[0]
+    assert size("loss", rows=64, io_dtype=0)[0] < 1000 * 256 * 4
+    assert size("loss", rows=128, io_dtype=0, dx=0, dweight=0)[0] < 1000 * 256 * 4
+    assert size("loss", rows=129, io_dtype=0, dx=0, dweight=0)[0] > 1000 * 256 * 4
     # an unaligned matrix is copied
     assert size("loss", weight=fake(1) + 2)[0] >= n + 1000 * 256 * 2
     # the probabilities of all rows are never there: a piece of them takes 2 GiB

@@ -299,6 +299,27 @@ def test_cross_entropy(rows, dim, vocab, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("rows,dim,vocab", [(1, 20, 31), (3, 1030, 4099), (31, 31, 33), (32, 32, 64), (33, 129, 500),
+                                            (64, 260, 1025), (65, 160, 96), (96, 95, 257), (97, 64, 130), (128, 600, 700),
+                                            (129, 33, 300), (2, 5, 70000)])
+def test_few_rows_of_fp32(rows, dim, vocab):
+    """Up to 64 rows (128 without gradients) of fp32 read the matrix as it is: rows of
+    it at any distance and any element, all rows, some and none with a target."""
+    note(f"few rows of fp32 {rows} x {dim} x {vocab}")
+    x, w, ids = loss_case(rows, dim, vocab, F32)
+    wide = torch.full((vocab, dim + 5), float("nan"), device=DEV)
+    wide[:, 1:dim + 1] = w
+    check_loss(x, wide[:, 1:dim + 1], ids, scale=0.7)
+    check_loss(x, w, torch.where(torch.arange(rows, device=DEV) % 3 == 1, ids, -100))
+    check_loss(x, w, torch.full_like(ids, vocab))
+    k = min(5, vocab)
+    ids, teacher = top_case(rows, vocab, k)
+    if k > 1:
+        ids[:, 1] = ids[:, 0]  # (the same id twice)
+    check_loss(x, w, ids, teacher, torch.rand(rows, generator=gen(4)).to(DEV), tau=1.3)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("ignored", [0.4, 0.95, 1.0])
 def test_cross_entropy_of_rows_without_a_target(dtype, ignored):
