@@ -10,7 +10,7 @@
 // from the matrix as it is; three bf16 planes of it would have to be written and
 // read first, five times its bytes.  Two of the instruction's summed indices are
 // one of each half wave's, so that a lane's 4 adjacent elements serve 4 of them.
-// 16 rows, 32000 x 4096 (524 MB): logits 130 us (4.0 TB/s), dx and dweight 280 (3.7
+// 16 rows, 32000 x 4096 (524 MB): logits 134 us (3.9 TB/s), dx and dweight 280 (3.7
 // TB/s).
 #include "mss.h"
 #include "vocab_gemm.hpp"
@@ -74,7 +74,12 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LossArgs a) {
     for (int j = 0; j < kRows / 8; ++j) sh.part[wave][8 * j + row][turn(8 * j + row, col)] = part[j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
+  // (the sum of a part apart: addends of a sum as large as a logit would each lose
+  // bits of its size, 9e-6 of a logit of 11 over 656 columns)
   auto multiply = [&]() __attribute__((always_inline)) {
+    f32x16 sum[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) sum[n] = f32x16{0};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const f32x4 fw = sh.part[wave][l][turn(l, 2 * q + h)];
@@ -84,8 +89,10 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LossArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int n = 0; n < N; ++n) acc[n] = product(fw[e], fx[n][e], acc[n]);
+        for (int n = 0; n < N; ++n) sum[n] = product(fw[e], fx[n][e], sum[n]);
     }
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[n] += sum[n];
   };
   // (without a branch around the loads, which would be waited for as if it had not
   // been taken: the last part is loaded twice)

@@ -80,7 +80,7 @@ __device__ inline int dx_cuts(const LossArgs& a, int rows) {
 
 // Up to so many rows of fp32, with gradients and without, take their products from
 // the matrix as it is, not from planes of it (20000 x 2560, 60 rows with gradients:
-// 256 us, 382 from planes; without, 72 rows: 130 us, 226 from planes).
+// 259 us, 382 from planes; without, 72 rows: 133 us, 226 from planes; 129 rows: 216).
 constexpr int kDirectRows = 64, kDirectLossRows = 128;
 
 // logits of the piece's rows: stats, and with `keep` the codes or logits
