@@ -733,7 +733,7 @@ typedef struct mss_layer_norm_bwd_args {
 typedef struct mss_linear_loss_args {
     uint32_t struct_size;
     int32_t io_dtype;            /* mss_dtype of x, weight, dx and dweight               */
-    int64_t rows;                /* 0..2^24                                              */
+    int64_t rows;                /* 0..2^22                                              */
     int64_t dim;                 /* 1..32768; rows dim and vocab dim at most 2^36        */
     int64_t vocab;               /* 1..2^22                                              */
     int64_t entries;             /* 1..MSS_MAX_LOSS_ENTRIES; 1 without teacher           */
