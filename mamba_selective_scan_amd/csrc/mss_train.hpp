@@ -98,7 +98,7 @@ struct LossArgs {
   int pieces;
   int tiles;       // vocabulary tiles, whose entries share a maximum
   int64_t vpad;    // columns of dz, a multiple of 64
-  float2* stats;   // [piece][tiles] the largest logit R and the sum of e^(z - R)
+  float2* stats;   // [piece][tiles] the largest logit R and the sum of e^(z - R) without R's own 1
   float2* sums;    // [piece] `from` and c / sum, the row's sum of e^z being sum e^from
   void* probs;     // [piece / 64][vpad / 32][64][32] codes of the logits (bf16), or the logits (fp32; `direct`: then dz)
   uint16_t* dz;    // [planes][piece / 64][vpad / 32][64][32] (bf16: probs itself)

@@ -123,6 +123,7 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LossArgs a) {
   if (wave >= N) return;
   f32x4 z[4];
   float top = -INFINITY, sum = 0.0f;
+  int ones = 0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     z[q] = ((sh.meet[0][wave][q][lane] + sh.meet[1][wave][q][lane]) + sh.meet[2][wave][q][lane]) + sh.meet[3][wave][q][lane];
@@ -137,10 +138,15 @@ __global__ __launch_bounds__(256) void few_logits_kernel(LossArgs a) {
 #pragma unroll
   for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum += fast_exp2((z[q][e] - from) * kLog2e);
+    for (int e = 0; e < 4; ++e) {
+      const float d = z[q][e] - from, p = fast_exp2(d * kLog2e);
+      sum += d != 0.0f ? p : 0.0f;
+      ones += d == 0.0f;
+    }
   sum += __shfl_xor(sum, 32, 64);
+  ones += __shfl_xor(ones, 32, 64);
   if (i >= live) return;
-  if (h == 0) a.stats[static_cast<int64_t>(i) * a.tiles + v / 32] = make_float2(top, sum);
+  if (h == 0) a.stats[static_cast<int64_t>(i) * a.tiles + v / 32] = make_float2(top, sum + static_cast<float>(ones - 1));
   float* out = static_cast<float*>(a.probs) + z_index(a, i, v) + 4 * h;
 #pragma unroll
   for (int q = 0; q < 4; ++q) *reinterpret_cast<f32x4*>(out + 8 * q) = z[q];

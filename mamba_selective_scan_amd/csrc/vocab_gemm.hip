@@ -392,6 +392,7 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
   for (int j = 0; j < IN; ++j) {
     const int i = wi + 32 * j + (lane & 31);
     float top = -INFINITY, sum = 0.0f;
+    int ones = 0;
 #pragma unroll
     for (int m = 0; m < IM; ++m)
 #pragma unroll
@@ -443,17 +444,20 @@ __global__ __launch_bounds__(T::kThreads) void logits_kernel(LossArgs a, int fir
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    // distances from the maximum, in place, and the sum
+    // distances from the maximum, in place, and the sum without the maximum's 1
 #pragma unroll
     for (int m = 0; m < IM; ++m)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float d = acc[m][j][e] - from;
         acc[m][j][e] = d;
-        sum += fast_exp2(d * kLog2e);
+        const float p = fast_exp2(d * kLog2e);
+        sum += d != 0.0f ? p : 0.0f;
+        ones += d == 0.0f;
       }
     sum += __shfl_xor(sum, 32, 64);
-    if (i < rows && lane < 32) a.stats[static_cast<int64_t>(i) * a.tiles + tile] = make_float2(top, sum);
+    ones += __shfl_xor(ones, 32, 64);
+    if (i < rows && lane < 32) a.stats[static_cast<int64_t>(i) * a.tiles + tile] = make_float2(top, sum + static_cast<float>(ones - 1));
   }
   if (!BF16 || !keep) return;
   // Codes of all the wave's rows, two bytes each, then 16 bytes a lane of 16 rows

@@ -224,11 +224,12 @@ __global__ __launch_bounds__(256) void pack_weight_kernel(LossArgs a) {
   }
 }
 
-// A row's sum of e^z from its tiles, as sum e^from with its largest logit `from`:
-// the sum of a row that is sure of one entry is 1 and the others, to the last bit.
-// Every thread of the workgroup takes part and has it.
+// A row's sum of e^z from its tiles, as (1 + others) e^from with its largest logit
+// `from`: a row that is sure of one entry has a loss and gradients of the size of
+// `others`, of which a sum with the 1 would leave few bits.  Every thread of the
+// workgroup takes part and has it.
 struct RowSum {
-  float from, sum;
+  float from, others;
 };
 __device__ inline RowSum row_sum(const LossArgs& a, int i, float* meet) {
   const float2* st = a.stats + static_cast<int64_t>(i) * a.tiles;
@@ -238,21 +239,29 @@ __device__ inline RowSum row_sum(const LossArgs& a, int i, float* meet) {
   if ((threadIdx.x & 63) == 0) meet[threadIdx.x >> 6] = top;
   __syncthreads();
   top = fmaxf(fmaxf(meet[0], meet[1]), fmaxf(meet[2], meet[3]));
-  const float from = top == -INFINITY ? 0.0f : top;
-  float s = 0.0f;
-  for (int t = threadIdx.x; t < a.tiles; t += 256) s += st[t].y * expf(st[t].x - from);
+  float s = 0.0f, ones = 0.0f;
+  for (int t = threadIdx.x; t < a.tiles; t += 256) {
+    const float2 q = st[t];
+    s += q.x == top ? q.y : (1.0f + q.y) * expf(q.x - top);
+    ones += q.x == top ? 1.0f : 0.0f;
+  }
   s = wave_sum(s);
-  if ((threadIdx.x & 63) == 0) meet[4 + (threadIdx.x >> 6)] = s;
+  ones = wave_sum(ones);
+  if ((threadIdx.x & 63) == 0) {
+    meet[4 + (threadIdx.x >> 6)] = s;
+    meet[8 + (threadIdx.x >> 6)] = ones;
+  }
   __syncthreads();
   s = (meet[4] + meet[5]) + (meet[6] + meet[7]);
-  return {from, s};
+  ones = (meet[8] + meet[9]) + (meet[10] + meet[11]);
+  return {top == -INFINITY ? 0.0f : top, s + (ones - 1.0f)};
 }
 
 // One workgroup a row of a piece: loss and lse, and with gradients what its dz is
 // made of: the sum, and dz of its entries.  In bf16 the entry that lost most by its
 // rounding, of equal ones the one with the lowest id, is carried apart.
 __global__ __launch_bounds__(256) void row_kernel(LossArgs a, int first, bool bf16, bool grad) {
-  __shared__ float meet[8];
+  __shared__ float meet[12];
   __shared__ int2 lost[4];
   const int i = blockIdx.x, j = first + i, live = *a.live;
   if (j >= live) return;
@@ -263,9 +272,9 @@ __global__ __launch_bounds__(256) void row_kernel(LossArgs a, int first, bool bf
     return a.direct ? static_cast<const float*>(a.probs)[z_index(a, i, id)] : a.picked[static_cast<int64_t>(j) * a.entries + k];
   };
   const float* share = a.teacher != nullptr ? a.share + static_cast<int64_t>(row) * a.entries : nullptr;
-  const float log_sum = logf(all.sum);
+  const float log_sum = log1pf(all.others);
   const float c = (a.row_weight != nullptr ? a.row_weight[row] : 1.0f / static_cast<float>(live)) * a.back;
-  const float by = c / all.sum;
+  const float by = c / (1.0f + all.others);
   float s = 0.0f, most = 0.0f;
   int2 best = make_int2(-1, 0);
   for (int k = threadIdx.x; k < a.entries; k += 256) {
@@ -280,7 +289,7 @@ __global__ __launch_bounds__(256) void row_kernel(LossArgs a, int first, bool bf
       for (int q = 0; q < a.entries; ++q)
         if (near[q] == id) t += share[q];
     }
-    const float v = fmaf(-t, all.sum, expf(z - all.from)) * by;
+    const float v = fmaf(-t, all.others, expf(z - all.from) - t) * by;
     a.value[static_cast<int64_t>(i) * a.entries + k] = v;
     const float miss = v - __uint_as_float(static_cast<uint32_t>(bf16_bits(v)) << 16);
     if (fabsf(miss) > most) {
