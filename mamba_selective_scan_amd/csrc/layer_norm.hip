@@ -46,6 +46,21 @@ __device__ inline void row_sums(float& a, float& b, float2* buf) {
   }
 }
 
+// The sum of a row's elements, in 64 bits: a mean near 0 keeps its last bits.
+template <int TPR>
+__device__ inline double row_sum(double a, double* buf) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) a += __shfl_xor(a, o, 64);
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = a;
+    __syncthreads();
+    a = 0.0;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) a += buf[i];
+  }
+  return a;
+}
+
 // A mean square below kFewBits may have lost addends, and one past fp32 is
 // infinite: such rows are scaled towards 1 by a power of two, as the
 // root-mean-square norm's are.
@@ -55,7 +70,8 @@ constexpr float kFewBits = 0x1p-80f, kScaleUp = 0x1p75f;
 template <typename IO, typename RES, int TPR, int K>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void fwd_kernel(LayerNormArgs a) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR;
-  __shared__ float2 buf[4][TPR > 64 ? TPR / 64 : 1];
+  __shared__ float2 buf[2][TPR > 64 ? TPR / 64 : 1];
+  __shared__ double wide[2][TPR > 64 ? TPR / 64 : 1];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kBlock / TPR) + threadIdx.x / TPR;
   if (TPR == 64 && row >= a.rows) return;  // (whole waves; never with barriers)
   const int tid = threadIdx.x % TPR;
@@ -86,37 +102,36 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void fwd_kernel(LayerNormArg
     }
   }
   const float n = static_cast<float>(a.dim);
-  // The first mean is rounded; what it misses (`rest`, about half a bit of it)
-  // is found with the squares and taken out of both.
+  // The mean is rounded; what it misses (`rest`, half a bit of it at most) is taken
+  // out of the distances by itself.
   float mean, rest, var;
   auto statistics = [&](float by, int at) __attribute__((always_inline)) {
-    float s = 0.0f, unused = 0.0f;
+    double s = 0.0;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < kV; ++i) s += r[k][i] * by;
-    row_sums<TPR>(s, unused, buf[at]);
-    mean = s / n;
-    float d1 = 0.0f, d2 = 0.0f;
+      for (int i = 0; i < kV; ++i) s += static_cast<double>(r[k][i] * by);
+    s = row_sum<TPR>(s, wide[at]) / a.dim;
+    mean = static_cast<float>(s);
+    rest = static_cast<float>(s - static_cast<double>(mean));
+    float none = 0.0f, d2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * TPR + tid) * kV;
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
-        const float d = c + i < a.dim ? fmaf(r[k][i], by, -mean) : 0.0f;
-        d1 += d;
+        const float d = c + i < a.dim ? fmaf(r[k][i], by, -mean) - rest : 0.0f;
         d2 = fmaf(d, d, d2);
       }
     }
-    row_sums<TPR>(d1, d2, buf[at + 1]);
-    rest = d1 / n;
-    var = fmaxf(d2 / n - rest * rest, 0.0f) + (d2 - d2);  // (fmax drops a NaN, the sum keeps it)
+    row_sums<TPR>(none, d2, buf[at]);
+    var = d2 / n;
   };
   statistics(1.0f, 0);
   float by = 1.0f, spread = var + a.eps;
   if (!(spread < INFINITY) || spread < kFewBits || !(fabsf(mean) < INFINITY)) {
     by = spread < kFewBits ? kScaleUp : 1.0f / kScaleUp;
-    statistics(by, 2);
+    statistics(by, 1);
     spread = var + a.eps * by * by;
   }
   const float inv = 1.0f / sqrtf(spread);  // of the row times `by`
